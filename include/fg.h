@@ -89,6 +89,18 @@ typedef enum fg_mode {
                                         /* nothing arrives at, so every bounded wait    */
                                         /* runs out and the call ends in FG_ERR_TIMEOUT */
 
+/* element types of the operators' plain inputs and outputs */
+typedef enum fg_type { FG_TYPE_F32 = 0, FG_TYPE_BF16 = 1 } fg_type;
+
+/* what fg_quantize applies to its input first */
+typedef enum fg_act {
+  FG_ACT_NONE = 0,
+  FG_ACT_SWIGLU = 1 /* rows of 2K values (g, u): silu(g) * u = g / (1 + exp(-g)) * u */
+} fg_act;
+
+/* fg_moe_route flag: weights over the chosen experts only (they sum to 1) */
+#define FG_FLAG_RENORMALIZE 0x1u
+
 #define FG_BSHUF_MAGIC 0x31424746u /* "FGB1" */
 #define FG_BSHUF_VERSION 1u
 
@@ -280,6 +292,74 @@ FG_API fg_status fg_gemm_splitk_reduce(const float* ws, int split_k, int64_t M, 
  */
 FG_API fg_status fg_gemm_noalloc(const void* A, const void* a_scales, int64_t M, const fg_bshuf* b, int mode,
                                  int split_k, void* Y, uint32_t flags, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Operators around the GEMM: activations into the A formats, and a
+ * mixture-of-experts layer (routing, products grouped by expert, weighted
+ * sum).  Conventions as above; no pointer may alias another unless said.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Codes and scales of the A operand of `mode` from x [M][K] (or, with
+ * FG_ACT_SWIGLU, from rows (g, u) of 2K values), rows ldx elements apart.
+ *  mode    MXFP8, MXFP4, MXFP8_B32, MXFP4_FP8A (its activations: e4m3, 32-K
+ *          blocks) or FP8_BLOCK128.
+ *  codes   [M][K] e4m3, or [M][K/2] packed e2m1 for MXFP4; scales as a_scales
+ *          of fg_gemm.
+ * E8M0 c = 127 + ceil(log2(amax / elem_max)) clamped to 0..254 (127 for an
+ * all-zero block), code = RNE(v * 2^(127-c)); FP8_BLOCK128: scale = amax / 448
+ * (1 for an all-zero block), code = RNE(v / scale).  A block with a NaN or an
+ * infinity gets the NaN scale (255; fp32 NaN) and zero codes.
+ * A weight's [N][K] rows quantise the same way (not FP8_BLOCK128, whose
+ * weights have 128 x 128 blocks).
+ * Errors: INVALID_ARG, SHAPE (K not a multiple of the block), ALIGN (x and its
+ * rows 16 bytes, codes 16, fp32 scales 4), UNSUPPORTED_ARCH, CUDA.
+ */
+FG_API fg_status fg_quantize(int mode, int act, const void* x, int type, int64_t M, int64_t K, int64_t ldx,
+                             void* codes, void* scales, void* stream);
+
+/*
+ * h = x + residual (x alone when residual is NULL),
+ * y = h / sqrt(mean(h^2) + eps) * weight, all in 32 bits; residual_out = h and
+ * y rounded once to the type (each only if not NULL), and y's codes and scales
+ * as fg_quantize gives them (from the unrounded y).  x and residual: rows ldx
+ * and ldr elements apart; weight [K]; outputs contiguous.  mode FG_BF16: no
+ * codes and scales (both NULL), y required.  residual_out may be residual, and
+ * residual_out or y may be x, where that has contiguous rows.
+ * Errors as fg_quantize (K at most 32768; a multiple of 8 for FG_BF16).
+ */
+FG_API fg_status fg_rmsnorm_quantize(int mode, const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                                     const void* weight, float eps, int type, int64_t M, int64_t K,
+                                     void* residual_out, void* y, void* codes, void* scales, void* stream);
+
+/* Workspace of fg_moe_route: 0 for up to 64 tokens, else the blocks' counts. */
+FG_API fg_status fg_moe_route_workspace_size(int64_t T, int E, uint64_t* bytes);
+
+/*
+ * Routing of T tokens to top_k of E experts (E <= 1024, top_k <= 32) by their
+ * logits (rows ldl elements apart).  Per token the top_k largest logits, the
+ * lowest expert first among equals; NaN counts as -infinity, and -infinity is
+ * never picked.  weights [T][top_k] (fp32): softmax over all experts, or with
+ * FG_FLAG_RENORMALIZE over the chosen ones (where the largest logit is
+ * +infinity, the infinite ones share the weight).  experts [T][top_k].
+ * The pairs (t, j) in stable order of their expert: offsets [E+1], expert e's
+ * pairs are slots offsets[e] .. offsets[e+1]-1; rows[slot] = t, slots[t][j] =
+ * the pair's slot.  Where a token has fewer than top_k logits to pick, its last
+ * choices are expert -1, weight 0, slot -1, and the rows from offsets[E] on are
+ * -1.  Errors: INVALID_ARG, SHAPE, ALIGN, WORKSPACE, UNSUPPORTED_ARCH, CUDA.
+ */
+FG_API fg_status fg_moe_route(const void* logits, int type, int64_t T, int E, int64_t ldl, int top_k, uint32_t flags,
+                              float* weights, int32_t* experts, int32_t* offsets, int32_t* rows, int32_t* slots,
+                              void* workspace, uint64_t workspace_bytes, void* stream);
+
+/*
+ * out[t] = residual[t] + sum_j weights[t][j] * Y[slots[t][j]] (bf16, 32-bit
+ * sums in the order of j, rounded once; residual may be NULL).  Y [R][N]; a slot
+ * outside 0..R-1 counts as no choice.  out may be residual.  top_k <= 32.
+ * Errors: INVALID_ARG, SHAPE (N % 8), ALIGN, UNSUPPORTED_ARCH, CUDA.
+ */
+FG_API fg_status fg_moe_combine(const void* Y, int64_t R, const int32_t* slots, const float* weights,
+                                const void* residual, int64_t T, int top_k, int64_t N, void* out, void* stream);
 
 /*
  * Synchronises the current device and returns (and clears) the error word

@@ -67,6 +67,11 @@ def lib():
         "fg_gemm": ([vp, vp, i64, ctypes.POINTER(BShuf), i32, i32, vp, vp, u64, u32, vp], i32),
         "fg_gemm_splitk_reduce": ([vp, i32, i64, i64, vp, vp, vp, vp], i32),
         "fg_gemm_noalloc": ([vp, vp, i64, ctypes.POINTER(BShuf), i32, i32, vp, u32, vp], i32),
+        "fg_quantize": ([i32, i32, vp, i32, i64, i64, i64, vp, vp, vp], i32),
+        "fg_rmsnorm_quantize": ([i32, vp, i64, vp, i64, vp, ctypes.c_float, i32, i64, i64, vp, vp, vp, vp, vp], i32),
+        "fg_moe_route_workspace_size": ([i64, i32, ctypes.POINTER(u64)], i32),
+        "fg_moe_route": ([vp, i32, i64, i32, i64, i32, u32, vp, vp, vp, vp, vp, vp, u64, vp], i32),
+        "fg_moe_combine": ([vp, i64, vp, vp, vp, i64, i32, i64, vp, vp], i32),
         "fg_get_error": ([], i32),
         "fg_set_wait_timeout_ns": ([u64], None),
         "fg_debug_override_cc": ([i32, i32], None),
@@ -345,3 +350,7 @@ def gemm_splitk_reduce(ws, split_k, M, N, a_s=None, b_s=None, Y=None, stream=Non
     _check(lib().fg_gemm_splitk_reduce(_ptr(ws), split_k, M, N, _ptr(a_s), _ptr(b_s), _ptr(Y),
                                        _stream(stream)))
     return Y
+
+
+from .moe import (FG_ACT_NONE, FG_ACT_SWIGLU, FG_TYPE_BF16, FG_TYPE_F32, Routing, moe_combine, moe_route,  # noqa: E402,F401
+                  quantize, rmsnorm_quantize)

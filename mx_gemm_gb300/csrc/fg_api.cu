@@ -23,6 +23,7 @@
 #include <vector>
 
 #include "../../include/fg.h"
+#include "fg_host.cuh"
 #include "fg_internal.cuh"
 
 namespace fg {
@@ -34,6 +35,12 @@ namespace {
 thread_local char g_msg[512] = "";
 std::atomic<uint64_t> g_timeout_ns{4000000000ull};
 std::atomic<int> g_cc_major_override{-1}, g_cc_minor_override{0};
+
+}  // namespace
+
+// ------------------------------------------- host helpers (see fg_host.cuh)
+
+uint64_t wait_timeout_ns() { return g_timeout_ns.load(); }
 
 fg_status fail(fg_status s, const char* fmt, ...) {
   va_list ap;
@@ -102,13 +109,13 @@ uint32_t* dev_error_ptr() {
   return ptrs[dev];
 }
 
-uint64_t fnv1a(const void* data, size_t n, uint64_t h = 1469598103934665603ull) {
+static uint64_t fnv1a(const void* data, size_t n, uint64_t h = 1469598103934665603ull) {
   const uint8_t* b = static_cast<const uint8_t*>(data);
   for (size_t i = 0; i < n; ++i) h = (h ^ b[i]) * 1099511628211ull;
   return h;
 }
 
-uint64_t desc_check(const fg_bshuf* d) { return fnv1a(d, offsetof(fg_bshuf, check)) ^ 0x5eedf00dcafe1234ull; }
+static uint64_t desc_check(const fg_bshuf* d) { return fnv1a(d, offsetof(fg_bshuf, check)) ^ 0x5eedf00dcafe1234ull; }
 
 fg_status check_desc(const fg_bshuf* d) {
   if (!d) return fail(FG_ERR_INVALID_ARG, "null weight descriptor");
@@ -116,6 +123,8 @@ fg_status check_desc(const fg_bshuf* d) {
     return fail(FG_ERR_LAYOUT, "weight descriptor was not produced by fg_preshuffle_b (or was modified)");
   return FG_OK;
 }
+
+namespace {
 
 uint64_t sf_image_bytes(int mode, int64_t N, int64_t K) {
   switch (mode) {
@@ -358,6 +367,8 @@ uint64_t large_streamk_plan(int mode, int64_t tiles, int64_t KB, int ctas, Large
   return large_streamk_bytes(ctas, wide);
 }
 
+}  // namespace
+
 // A 64-bit tag per call: a partial's flag matches only the launch that wrote
 // it (workspace contents from earlier calls never do), and the CTA that
 // consumes a partial clears its flag, so a replay of a captured launch (which
@@ -371,7 +382,7 @@ uint64_t next_epoch() {
 
 // ---------------------------------------------------------- TMA set-up
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -400,6 +411,8 @@ fg_status make_tmap(CUtensorMap* map, const void* base, int64_t rows, int64_t rb
   if (r != CUDA_SUCCESS) return fail(FG_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
   return FG_OK;
 }
+
+namespace {
 
 // The bf16 output Y [rows][n] as rows of 2n bytes, boxes of 32 rows x 64
 // bytes (32 columns) in the 64-byte swizzle: the store map of the large-M MX
@@ -436,6 +449,8 @@ fg_status make_tmap_rows(CUtensorMap* map, const void* base, int64_t rows, uint3
   return FG_OK;
 }
 
+}  // namespace
+
 // MXFP4_FP8A weight image (blocks of 128 rows x 64 bytes of packed e2m1, see
 // fg_preshuffle_b) as a 3-D map of 4-bit codes {128 codes, 128 rows,
 // N/128 * K/128 blocks}.  Its box is one block, loaded with every 16 codes
@@ -457,8 +472,6 @@ fg_status make_tmap_fp4w(CUtensorMap* map, const void* base, int64_t N, int64_t 
     return fail(FG_ERR_CUDA, "cuTensorMapEncodeTiled (fp4 weight image) failed (%d)", static_cast<int>(r));
   return FG_OK;
 }
-
-}  // namespace
 
 bool pdl_enabled() { return getenv("FG_NO_PDL") == nullptr; }
 
