@@ -353,6 +353,27 @@ FG_API fg_status fg_moe_route(const void* logits, int type, int64_t T, int E, in
                               void* workspace, uint64_t workspace_bytes, void* stream);
 
 /*
+ * Products grouped by expert: Y[i] = dequant(A[rows[i]]) . dequant(B_e)^T for
+ * offsets[e] <= i < offsets[e+1], fp32 accumulation, bf16 Y [R][N].
+ *  b        the experts' weights stacked to one [E * N][K] and preshuffled as
+ *           one weight (fg_preshuffle_b; FP8_TENSOR: one b_s for all); N, the
+ *           rows of one expert, a multiple of 128.
+ *  A        [T][K] codes as in fg_gemm, a_scales likewise ([T] rows).
+ *  rows     device int32 [R]: the row of A that row i multiplies, clamped into
+ *           0..T-1; NULL: row i itself (T >= R).
+ *  offsets  device int32 [E + 1], not decreasing, clamped into 0..R.  Rows of Y
+ *           before offsets[0] and from offsets[E] on are not written.
+ *  workspace  fg_grouped_gemm_workspace_size bytes; any contents.  Calls that
+ *           overlap on the GPU need a workspace each.
+ * All modes but FP8_BLOCK128; E <= 1024; R, T <= 2^24.
+ * Errors: INVALID_ARG, SHAPE, ALIGN, LAYOUT, WORKSPACE, UNSUPPORTED_ARCH, CUDA.
+ */
+FG_API fg_status fg_grouped_gemm_workspace_size(int mode, int64_t R, int E, int64_t N, int64_t K, uint64_t* bytes);
+FG_API fg_status fg_grouped_gemm(const void* A, const void* a_scales, int64_t T, const int32_t* rows, int64_t R,
+                                 const int32_t* offsets, int E, const fg_bshuf* b, int mode, void* Y, void* workspace,
+                                 uint64_t workspace_bytes, uint32_t flags, void* stream);
+
+/*
  * out[t] = residual[t] + sum_j weights[t][j] * Y[slots[t][j]] (bf16, 32-bit
  * sums in the order of j, rounded once; residual may be NULL).  Y [R][N]; a slot
  * outside 0..R-1 counts as no choice.  out may be residual.  top_k <= 32.

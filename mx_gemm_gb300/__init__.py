@@ -72,6 +72,8 @@ def lib():
         "fg_moe_route_workspace_size": ([i64, i32, ctypes.POINTER(u64)], i32),
         "fg_moe_route": ([vp, i32, i64, i32, i64, i32, u32, vp, vp, vp, vp, vp, vp, u64, vp], i32),
         "fg_moe_combine": ([vp, i64, vp, vp, vp, i64, i32, i64, vp, vp], i32),
+        "fg_grouped_gemm_workspace_size": ([i32, i64, i32, i64, i64, ctypes.POINTER(u64)], i32),
+        "fg_grouped_gemm": ([vp, vp, i64, vp, i64, vp, i32, ctypes.POINTER(BShuf), i32, vp, vp, u64, u32, vp], i32),
         "fg_get_error": ([], i32),
         "fg_set_wait_timeout_ns": ([u64], None),
         "fg_debug_override_cc": ([i32, i32], None),
@@ -352,5 +354,5 @@ def gemm_splitk_reduce(ws, split_k, M, N, a_s=None, b_s=None, Y=None, stream=Non
     return Y
 
 
-from .moe import (FG_ACT_NONE, FG_ACT_SWIGLU, FG_TYPE_BF16, FG_TYPE_F32, Routing, moe_combine, moe_route,  # noqa: E402,F401
-                  quantize, rmsnorm_quantize)
+from .moe import (FG_ACT_NONE, FG_ACT_SWIGLU, FG_TYPE_BF16, FG_TYPE_F32, Routing, grouped_gemm,  # noqa: E402,F401
+                  grouped_gemm_workspace_size, moe_combine, moe_route, quantize, rmsnorm_quantize)

@@ -1,0 +1,691 @@
+// Products grouped by expert: Y[i] = A[rows[i]] . B_e^T for the rows i of
+// expert e, offsets[e] <= i < offsets[e+1], with ragged counts known only on
+// the device.
+//
+// Orientation.  The weight is the MMA's M operand (128 of its rows per tile,
+// one 128 x 128-byte slab of the preshuffled image per K step) and the tokens
+// its N operand, so a ragged expert costs what it holds: the instruction's N
+// is set per tile to the tile's rows, rounded up to 16.  The accumulator (128
+// lanes x up to TT fp32 columns) lives in tensor memory.
+//
+// Schedule.  Every block reads the offsets and sums, per expert, its token
+// tiles (an expert's rows are cut into as few tiles of at most TT rows as hold
+// them, of equal size); a unit is one token tile x one weight tile.  Units run
+// expert by expert, the token tiles of one weight tile next to one another, so
+// the blocks that share a weight tile take it at the same time and HBM moves
+// it once.  No work is launched for experts without rows, and nothing comes
+// back to the host.
+//
+//  - TT = 256 (many rows an expert): units are dealt out whole.  Bound by the
+//    tensor cores and the stream from L2.
+//  - TT = 32 (decoding): bound by the weights' bytes from HBM, whatever the
+//    rows.  The K steps of all units form one line that is cut evenly over the
+//    blocks, wherever the cuts fall, so that all SMs stream to the end.  Blocks
+//    that share a unit leave fp32 partials in the workspace; the last to
+//    arrive adds them in the order of K (the same bits each time) and stores.
+//    Nobody waits for another block.
+//
+// Warp roles: 0 copies (weights by bulk copy, tokens by tensor copy: boxes of
+// 16 rows, or four rows at a time by their index where rows are gathered);
+// 1 issues the MMAs; 2-3 build the token scale atoms of the MX modes from the
+// caller's E8M0 bytes; the others take the results out.
+#include <cuda_bf16.h>
+
+#include <cstring>
+
+#include "fg_host.cuh"
+#include "fg_internal.cuh"
+#include "fg_ptx.cuh"
+
+namespace fg {
+
+namespace {
+
+constexpr int kMaxExperts = 1024;
+constexpr int kSlabBytes = 16384;
+constexpr int kMinSlabs = 4;  // K steps a block of the cut line takes at least
+
+struct GroupedParams {
+  const uint8_t* b_img;
+  const uint8_t* b_sf;
+  const float* b_s;           // FP8_TENSOR
+  const void* a_scales;
+  const int32_t* offsets;     // [E + 1]
+  const int32_t* rows;        // [R] or null
+  __nv_bfloat16* y;           // [R][N]
+  float* part;                // [blocks][2][TT][128] partials (cut line)
+  unsigned long long* tickets;  // [blocks] arrivals at the unit that begins last in the block
+  unsigned long long epoch;
+  uint32_t* err;
+  uint64_t timeout_ns;
+  int T, R, E, N, K, KB;
+  int debug_stall;
+};
+
+template <int MODE, int TT>
+struct GCfg {
+  static constexpr int APS = MODE == kMXFP4 ? 2 : (is_mx(MODE) ? 1 : 0);
+  static constexpr bool CUT = TT == 32;           // the cut line of K steps
+  static constexpr int STAGES = 4;
+  static constexpr int TOK_BYTES = TT * 128;
+  static constexpr int TOK_ATOMS = (TT + 127) / 128;
+  static constexpr int SFW_BYTES = APS * 512;
+  static constexpr int SFT_BYTES = APS * TOK_ATOMS * 512;
+  static constexpr int STAGE_RAW = kSlabBytes + TOK_BYTES + SFW_BYTES + SFT_BYTES;
+  static constexpr int STAGE_BYTES = (STAGE_RAW + 1023) / 1024 * 1024;
+  static constexpr int SMEM = STAGES * STAGE_BYTES + 1024;
+  static constexpr int EPI_WARPS = TT == 32 ? 4 : 8;
+  static constexpr int THREADS = 128 + 32 * EPI_WARPS;
+  static constexpr int ACCS = TT <= 128 ? 2 : 1;  // accumulators
+  static constexpr int ACC_COLS = ACCS * TT;
+  static constexpr int SFW_COLS = APS * 4, SFT_COLS = APS * 4 * TOK_ATOMS;
+  static constexpr int TMEM_NEED = ACC_COLS + STAGES * (SFW_COLS + SFT_COLS);
+  static constexpr int TMEM_COLS =
+      TMEM_NEED <= 64 ? 64 : (TMEM_NEED <= 128 ? 128 : (TMEM_NEED <= 256 ? 256 : 512));
+  static constexpr int BLOCKS_PER_SM = TT == 32 ? 2 : 1;
+  static_assert(TMEM_NEED <= 512 && BLOCKS_PER_SM * TMEM_COLS <= 512, "TMEM budget");
+  static_assert(BLOCKS_PER_SM * (SMEM + 10240) <= 232448, "shared memory budget");
+};
+
+// The unit's rows and weight tile.
+struct Unit {
+  int e, row0, count, n16, nt;  // n16: rows rounded up to 16
+};
+
+// One block's share of a unit: K steps [k0, k1).
+struct Share {
+  long long u;
+  int k0, k1;
+};
+
+struct Schedule {
+  const int* offs;   // [E + 1] clamped offsets
+  const int* tiles;  // [E + 1] token tiles before expert e
+  long long units, W, lo, hi;
+  int E, NT, KB, blocks, c;
+};
+
+template <int TT>
+__device__ __forceinline__ Unit unit_at(const Schedule& s, long long u) {
+  int a = 0, b = s.E;  // the last e with tiles[e] * NT <= u
+  while (b - a > 1) {
+    const int m = (a + b) >> 1;
+    if (static_cast<long long>(s.tiles[m]) * s.NT <= u) a = m; else b = m;
+  }
+  const int r = static_cast<int>(u - static_cast<long long>(s.tiles[a]) * s.NT);
+  const int n = s.tiles[a + 1] - s.tiles[a];
+  const int rows = s.offs[a + 1] - s.offs[a];
+  const int per = ((rows + n - 1) / n + 15) & ~15;
+  Unit q;
+  q.e = a;
+  q.nt = r / n;
+  const int m = r - q.nt * n;
+  q.row0 = s.offs[a] + m * per;
+  q.count = min(per, rows - m * per);
+  q.n16 = (q.count + 15) & ~15;
+  return q;
+}
+
+// Cut c of the line of W steps over `blocks` blocks, and the block that holds step x.
+__device__ __forceinline__ long long cut_at(const Schedule& s, int c) { return s.W * c / s.blocks; }
+__device__ __forceinline__ int holder_of(const Schedule& s, long long x) {
+  return static_cast<int>(((x + 1) * s.blocks + s.W - 1) / s.W) - 1;
+}
+
+template <bool CUT>
+__device__ __forceinline__ int share_count(const Schedule& s) {
+  if (!CUT) return s.c < s.units ? static_cast<int>((s.units - s.c + s.blocks - 1) / s.blocks) : 0;
+  return s.hi > s.lo ? static_cast<int>((s.hi - 1) / s.KB - s.lo / s.KB + 1) : 0;
+}
+
+template <bool CUT>
+__device__ __forceinline__ Share share_at(const Schedule& s, int i) {
+  Share h;
+  if (!CUT) {
+    h.u = s.c + static_cast<long long>(i) * s.blocks;
+    h.k0 = 0;
+    h.k1 = s.KB;
+    return h;
+  }
+  h.u = s.lo / s.KB + i;
+  const long long first = h.u * s.KB;
+  h.k0 = i == 0 ? static_cast<int>(s.lo - first) : 0;
+  h.k1 = static_cast<int>(min(static_cast<long long>(s.KB), s.hi - first));
+  return h;
+}
+
+template <int MODE>
+__device__ __forceinline__ void mma_step(uint32_t d, uint64_t a, uint64_t b, int n, int j, int kb, uint32_t sfw,
+                                         uint32_t sft, int tok_atoms, uint32_t accum) {
+  if (MODE == kBF16) {
+    mma_f16(d, a, b, idesc_bf16(128, n), accum);
+  } else if (MODE == kTensor) {
+    mma_f8f6f4(d, a, b, idesc_e4m3(128, n), accum);
+  } else if (MODE == kMXFP8) {  // the weight's byte of its four-slab atom; the token atoms repeat theirs
+    mma_mxf8f6f4(d, a, b, idesc_mx(128, n, kF8f6f4E4M3, kb & 3, j), sfw, sft, accum);
+  } else if (MODE == kMXFP8B32) {
+    mma_mxf8f6f4(d, a, b, idesc_mx(128, n, kF8f6f4E4M3, j, j), sfw, sft, accum);
+  } else if (MODE == kMXFP4FP8A) {
+    mma_mxf8f6f4(d, a, b, idesc_mx_ab(128, n, kF8f6f4E2M1, kF8f6f4E4M3, j, j), sfw, sft, accum);
+  } else {
+    const int g = j >> 1, id = 2 * (j & 1);
+    mma_mxf4(d, a, b, idesc_mx(128, n, kMxf4E2M1, id, id), sfw + 4 * g, sft + 4 * tok_atoms * g, accum);
+  }
+}
+
+// tmap_a: A as rows of bytes, boxes of 128 bytes x 16 rows (GATHER: x 1 row);
+// tmap_b: fp8 x fp4 only, the weight image's blocks.
+template <int MODE, int TT, bool GATHER>
+__global__ void __launch_bounds__(GCfg<MODE, TT>::THREADS, GCfg<MODE, TT>::BLOCKS_PER_SM)
+    grouped_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
+                   const GroupedParams p) {
+  using C = GCfg<MODE, TT>;
+  constexpr int ST = C::STAGES;
+  constexpr bool CUT = C::CUT;
+  extern __shared__ uint8_t dsmem[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsmem) + 1023) & ~uintptr_t(1023));
+  __shared__ __align__(8) uint64_t full_bar[ST], empty_bar[ST];
+  __shared__ __align__(8) uint64_t accf_bar[C::ACCS], acce_bar[C::ACCS];
+  __shared__ __align__(8) uint64_t stall_bar, drain_bar;
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ int abort_sh, issued_sh, consumed_sh, mma_any_sh, last_sh;
+  __shared__ int offs_sh[kMaxExperts + 1], tiles_sh[kMaxExperts + 1];
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint64_t T = p.timeout_ns;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&full_bar[i], C::APS ? 3 : 1);  // MX: + one arrival per scale warp
+      mbar_init(&empty_bar[i], 1);
+    }
+    for (int i = 0; i < C::ACCS; ++i) {
+      mbar_init(&accf_bar[i], 1);
+      mbar_init(&acce_bar[i], C::EPI_WARPS);
+    }
+    mbar_init(&stall_bar, 1);
+    mbar_init(&drain_bar, 1);
+    abort_sh = 0;
+    issued_sh = 0;
+    consumed_sh = 0;
+    mma_any_sh = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&tmem_base_sh, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  if (threadIdx.x == 0) pdl_launch_dependents();
+  // offsets, clamped into 0..R and to counts of at least zero, and the token
+  // tiles before each expert
+  for (int e = threadIdx.x; e <= p.E; e += C::THREADS) offs_sh[e] = min(max(__ldg(p.offsets + e), 0), p.R);
+  __syncthreads();
+  if (warp == 0) {
+    prefetch_tmap(&tmap_a);
+    if (MODE == kMXFP4FP8A) prefetch_tmap(&tmap_b);
+    int carry = 0;
+    for (int e0 = 0; e0 < p.E; e0 += 32) {
+      const int e = e0 + lane;
+      const int t = e < p.E ? (max(0, offs_sh[e + 1] - offs_sh[e]) + TT - 1) / TT : 0;
+      int sum = t;
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const int o = __shfl_up_sync(0xffffffffu, sum, d);
+        if (lane >= d) sum += o;
+      }
+      if (e < p.E) tiles_sh[e] = carry + sum - t;
+      carry += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    if (lane == 0) tiles_sh[p.E] = carry;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base_sh;
+
+  Schedule s;
+  s.offs = offs_sh;
+  s.tiles = tiles_sh;
+  s.E = p.E;
+  s.NT = p.N / 128;
+  s.KB = p.KB;
+  s.units = static_cast<long long>(tiles_sh[p.E]) * s.NT;
+  s.W = s.units * s.KB;
+  s.c = blockIdx.x;
+  s.blocks = gridDim.x;
+  if (CUT) {
+    const long long most = (s.W + kMinSlabs - 1) / kMinSlabs;
+    s.blocks = static_cast<int>(min(static_cast<long long>(gridDim.x), max(most, 1ll)));
+    s.lo = s.c < s.blocks ? cut_at(s, s.c) : 0;
+    s.hi = s.c < s.blocks ? cut_at(s, s.c + 1) : 0;
+  }
+  const int shares = share_count<CUT>(s);
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- copies
+    int it = 0;
+    bool ok = true;
+    for (int i = 0; ok && i < shares; ++i) {
+      const Share h = share_at<CUT>(s, i);
+      const Unit q = unit_at<TT>(s, h.u);
+      // gathered: this lane's groups of four rows; rows past the tile's end
+      // repeat its last one, indexes are clamped into A
+      constexpr int G4 = GATHER ? (TT + 127) / 128 : 1;
+      int idx[G4][4];
+      if (GATHER) {
+#pragma unroll
+        for (int g = 0; g < G4; ++g)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int m = min((g * 32 + lane) * 4 + j, q.count - 1);
+            idx[g][j] = min(max(__ldg(p.rows + q.row0 + m), 0), p.T - 1);
+          }
+      }
+      const long long wt = static_cast<long long>(q.e) * s.NT + q.nt;  // weight tile of the stacked image
+      for (int kb = h.k0; kb < h.k1; ++kb, ++it) {
+        const int slot = it % ST;
+        const bool w = mbar_wait(&empty_bar[slot], ((it / ST) & 1) ^ 1u, T, p.err, 61);
+        if (!__all_sync(0xffffffffu, w)) {
+          ok = false;
+          break;
+        }
+        uint8_t* st = smem + slot * C::STAGE_BYTES;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&full_bar[slot],
+                                (MODE == kMXFP4FP8A ? kSlabBytes / 2 : kSlabBytes) + q.n16 * 128 + C::SFW_BYTES);
+          const long long slab = wt * s.KB + kb;
+          if (MODE == kMXFP4FP8A)
+            tma_load_3d(st, &tmap_b, 0, 0, static_cast<int32_t>(slab), &full_bar[slot]);
+          else
+            bulk_g2s(st, p.b_img + slab * kSlabBytes, kSlabBytes, &full_bar[slot]);
+          if (C::APS) {
+            const long long atom = MODE == kMXFP8 ? wt * ((s.KB + 3) / 4) + kb / 4 : slab * C::APS;
+            bulk_g2s(st + kSlabBytes + C::TOK_BYTES, p.b_sf + atom * 512, C::SFW_BYTES, &full_bar[slot]);
+          }
+        }
+        __syncwarp();
+        uint8_t* tok = st + kSlabBytes;
+        if (GATHER) {
+#pragma unroll
+          for (int g = 0; g < G4; ++g) {
+            const int m = (g * 32 + lane) * 4;
+            if (m < q.n16) tma_gather4(tok + m * 128, &tmap_a, kb * 128, idx[g], &full_bar[slot]);
+          }
+        } else if (lane * 16 < q.n16) {
+          tma_load_2d(tok + lane * 2048, &tmap_a, kb * 128, q.row0 + lane * 16, &full_bar[slot]);
+        }
+      }
+    }
+    if (lane == 0) {
+      issued_sh = it;
+      if (!ok) abort_sh = 1;
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMAs
+    if (lane == 0) {
+      bool ok = true;
+      if (p.debug_stall) ok = mbar_wait(&stall_bar, 0, T, p.err, 62);
+      int it = 0;
+      for (int i = 0; ok && i < shares; ++i) {
+        const Share h = share_at<CUT>(s, i);
+        const Unit q = unit_at<TT>(s, h.u);
+        const int acc = i % C::ACCS;
+        if (!mbar_wait(&acce_bar[acc], ((i / C::ACCS) & 1) ^ 1u, T, p.err, 63)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + acc * TT;
+        for (int kb = h.k0; kb < h.k1; ++kb, ++it) {
+          const int slot = it % ST;
+          if (!mbar_wait(&full_bar[slot], (it / ST) & 1, T, p.err, 64)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          mma_any_sh = 1;
+          uint8_t* st = smem + slot * C::STAGE_BYTES;
+          const uint32_t sfw = tmem + C::ACC_COLS + slot * (C::SFW_COLS + C::SFT_COLS);
+          const uint32_t sft = sfw + C::SFW_COLS;
+          if (C::APS) {
+            const uint32_t sw = smem_u32(st + kSlabBytes + C::TOK_BYTES);
+            const uint32_t stk = sw + C::SFW_BYTES;
+#pragma unroll
+            for (int g = 0; g < C::APS; ++g) {
+              tc_cp_32x128b_warpx4(sfw + 4 * g, sdesc_plain_rows16(sw + 512 * g));
+#pragma unroll
+              for (int a = 0; a < C::TOK_ATOMS; ++a)
+                if (a == 0 || q.n16 > a * 128)
+                  tc_cp_32x128b_warpx4(sft + 4 * (g * C::TOK_ATOMS + a),
+                                       sdesc_plain_rows16(stk + 512 * (g * C::TOK_ATOMS + a)));
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            mma_step<MODE>(d, sdesc_sw128(smem_u32(st + j * 32)), sdesc_sw128(smem_u32(st + kSlabBytes + j * 32)), q.n16, j,
+                           kb, sfw, sft, C::TOK_ATOMS, (kb > h.k0 || j > 0) ? 1u : 0u);
+          tc_commit(&empty_bar[slot]);
+        }
+        if (!ok) {
+          ++it;
+          break;
+        }
+        tc_commit(&accf_bar[acc]);
+      }
+      consumed_sh = it;
+      if (!ok) abort_sh = 1;
+      if (mma_any_sh) {
+        tc_commit(&drain_bar);
+        mbar_wait(&drain_bar, 0, T, p.err, 65);
+      }
+    }
+  } else if (warp < 4) {
+    // ----------------------------------------------------- token scale atoms
+    if (C::APS) {
+      constexpr int PT = (TT + 63) / 64;  // rows of the tile per thread
+      const int st_id = threadIdx.x - 64;
+      const uint8_t* asf = static_cast<const uint8_t*>(p.a_scales);
+      const int cols = MODE == kMXFP8 ? p.K / 128 : p.K / 32;
+      const bool words = (reinterpret_cast<uintptr_t>(asf) & 3u) == 0;
+      int it = 0;
+      bool ok = true;
+      for (int i = 0; ok && i < shares; ++i) {
+        const Share h = share_at<CUT>(s, i);
+        const Unit q = unit_at<TT>(s, h.u);
+        const uint8_t* src[PT];
+#pragma unroll
+        for (int j = 0; j < PT; ++j) {
+          const int m = st_id + 64 * j;
+          int row = q.row0 + min(m, q.count - 1);
+          if (GATHER) row = min(max(__ldg(p.rows + row), 0), p.T - 1);
+          src[j] = asf + static_cast<size_t>(row) * cols;
+        }
+        // the four E8M0 bytes of atom g of K step kb
+        auto word = [&](int j, int kb, int g) -> uint32_t {
+          if (MODE == kMXFP8) return static_cast<uint32_t>(__ldg(src[j] + kb)) * 0x01010101u;
+          const uint8_t* b = src[j] + (kb * C::APS + g) * 4;
+          if (words) return __ldg(reinterpret_cast<const uint32_t*>(b));
+          return b[0] | (static_cast<uint32_t>(b[1]) << 8) | (static_cast<uint32_t>(b[2]) << 16) |
+                 (static_cast<uint32_t>(b[3]) << 24);
+        };
+        uint32_t next[PT][C::APS ? C::APS : 1];
+        auto fetch = [&](int kb) {
+#pragma unroll
+          for (int j = 0; j < PT; ++j)
+#pragma unroll
+            for (int g = 0; g < C::APS; ++g)
+              if (st_id + 64 * j < q.n16) next[j][g] = word(j, kb, g);
+        };
+        fetch(h.k0);
+        for (int kb = h.k0; kb < h.k1; ++kb, ++it) {
+          const int slot = it % ST;
+          const bool w = mbar_wait(&empty_bar[slot], ((it / ST) & 1) ^ 1u, T, p.err, 66);
+          if (!__all_sync(0xffffffffu, w)) {
+            ok = false;
+            break;
+          }
+          uint8_t* sft = smem + slot * C::STAGE_BYTES + kSlabBytes + C::TOK_BYTES + C::SFW_BYTES;
+#pragma unroll
+          for (int j = 0; j < PT; ++j) {
+            const int m = st_id + 64 * j;
+            if (m < q.n16) {
+#pragma unroll
+              for (int g = 0; g < C::APS; ++g)
+                *reinterpret_cast<uint32_t*>(sft + (g * C::TOK_ATOMS + (m >> 7)) * 512 + (m & 31) * 16 +
+                                             ((m & 127) >> 5) * 4) = next[j][g];
+            }
+          }
+          if (kb + 1 < h.k1) fetch(kb + 1);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full_bar[slot]);
+        }
+      }
+      if (!ok && lane == 0) abort_sh = 1;
+    }
+  } else {
+    // -------------------------------------------------------------- results
+    const int qd = warp & 3;
+    const int half = (warp - 4) >> 2;  // TT = 256: columns 0..127 or 128..255
+    constexpr int COLS = TT == 32 ? 32 : 128;  // columns (rows of Y) per warp
+    const float scale = MODE == kTensor ? __ldg(static_cast<const float*>(p.a_scales)) * __ldg(p.b_s) : 1.f;
+    bool ok = true;
+    for (int i = 0; i < shares; ++i) {
+      const Share h = share_at<CUT>(s, i);
+      const Unit q = unit_at<TT>(s, h.u);
+      const int acc = i % C::ACCS;
+      // a warp that gave up waits for nothing more, but still meets the others
+      // at the barriers of the shared units
+      if (ok) {
+        const bool w = mbar_wait(&accf_bar[acc], (i / C::ACCS) & 1, T, p.err, 67);
+        ok = __all_sync(0xffffffffu, w);
+        if (!ok && lane == 0) abort_sh = 1;
+      }
+      const bool shared_unit = CUT && (h.k0 > 0 || h.k1 < s.KB);
+      if (!ok) {
+        if (shared_unit) {
+          bar_sync_named(1, 32 * C::EPI_WARPS);
+          bar_sync_named(1, 32 * C::EPI_WARPS);
+        }
+        continue;
+      }
+      tc_fence_after();
+      uint32_t v[COLS];
+      const uint32_t taddr = tmem + acc * TT + half * COLS + (static_cast<uint32_t>(qd * 32) << 16);
+#pragma unroll
+      for (int c = 0; c < COLS; c += 32) tmem_ld32(taddr + c, *reinterpret_cast<uint32_t(*)[32]>(&v[c]));
+      tmem_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&acce_bar[acc]);
+      const int n = qd * 32 + lane;  // row of the weight tile
+      const int m0 = half * COLS;
+      if (shared_unit) {
+        // a shared unit: leave the partial, and let the last to arrive add up
+        const long long first = h.u * s.KB;
+        const int c0 = holder_of(s, first), c1 = holder_of(s, first + s.KB - 1);
+        const size_t tile = static_cast<size_t>(TT) * 128;
+        // a block's share that begins inside a unit is its first, slot 0; one
+        // that begins with the unit and ends inside it is its last, slot 1
+        float* mine = p.part + (2 * static_cast<size_t>(s.c) + (h.k0 > 0 ? 0 : 1)) * tile;
+#pragma unroll
+        for (int m = 0; m < COLS; ++m)
+          if (m < q.count) __stcg(mine + m * 128 + n, __uint_as_float(v[m]));
+        __threadfence();
+        bar_sync_named(1, 32 * C::EPI_WARPS);
+        if (threadIdx.x == 128) last_sh = 0;
+        if (threadIdx.x == 128 && *reinterpret_cast<volatile int*>(&abort_sh) == 0) {
+          // tickets hold the call's tag and the arrivals; a word of another
+          // call (or of nothing) counts as none
+          unsigned long long* t = p.tickets + c0;
+          unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(t), seen;
+          int arrived;
+          do {
+            seen = old;
+            arrived = (seen >> 16) == p.epoch ? static_cast<int>(seen & 0xffffu) : 0;
+            const bool last = arrived == c1 - c0;  // the others are in: leave the word clear
+            old = atomicCAS(t, seen, last ? 0ull : (p.epoch << 16) | static_cast<unsigned long long>(arrived + 1));
+          } while (old != seen);
+          __threadfence();
+          last_sh = arrived == c1 - c0;
+        }
+        bar_sync_named(1, 32 * C::EPI_WARPS);
+        const bool last = last_sh != 0;
+        if (!last) continue;
+#pragma unroll
+        for (int m = 0; m < COLS; ++m) {
+          if (m < q.count) {
+            float sum = __ldcg(p.part + (2 * static_cast<size_t>(c0) + 1) * tile + m * 128 + n);
+            for (int c = c0 + 1; c <= c1; ++c) sum += __ldcg(p.part + 2 * static_cast<size_t>(c) * tile + m * 128 + n);
+            v[m] = __float_as_uint(sum);
+          }
+        }
+      }
+      __nv_bfloat16* out = p.y + static_cast<size_t>(q.row0 + m0) * p.N + q.nt * 128 + n;
+#pragma unroll
+      for (int m = 0; m < COLS; ++m)
+        if (m0 + m < q.count) out[static_cast<size_t>(m) * p.N] = __float2bfloat16_rn(__uint_as_float(v[m]) * scale);
+    }
+  }
+
+  // --------------------------------------------------------------- teardown
+  tc_fence_before();
+  __syncthreads();
+  if (abort_sh && threadIdx.x == 0) {
+    for (int it = consumed_sh; it < issued_sh; ++it)
+      mbar_wait(&full_bar[it % ST], (it / ST) & 1, T, nullptr, 0);
+  }
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
+}
+
+template <int MODE, int TT, bool GATHER>
+cudaError_t launch_one(const CUtensorMap& tmap_a, const CUtensorMap& tmap_b, const GroupedParams& p, int blocks,
+                       cudaStream_t stream) {
+  using C = GCfg<MODE, TT>;
+  auto* kernel = &grouped_kernel<MODE, TT, GATHER>;
+  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), C::SMEM);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = pdl_enabled() ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, tmap_a, tmap_b, p);
+}
+
+template <int MODE>
+cudaError_t launch_mode(const CUtensorMap& tmap_a, const CUtensorMap& tmap_b, const GroupedParams& p, int tt, int blocks,
+                        cudaStream_t stream) {
+  if (tt == 32)
+    return p.rows ? launch_one<MODE, 32, true>(tmap_a, tmap_b, p, blocks, stream)
+                  : launch_one<MODE, 32, false>(tmap_a, tmap_b, p, blocks, stream);
+  return p.rows ? launch_one<MODE, 256, true>(tmap_a, tmap_b, p, blocks, stream)
+                : launch_one<MODE, 256, false>(tmap_a, tmap_b, p, blocks, stream);
+}
+
+// Token tile and blocks of a call.
+struct GroupedPlan {
+  int tt, blocks;
+  uint64_t part_bytes, ticket_bytes;
+};
+
+GroupedPlan grouped_plan(int64_t R, int64_t E, int64_t N, int64_t KB) {
+  GroupedPlan g;
+  g.tt = R <= 16 * E ? 32 : 256;
+  const int64_t most = g.tt == 32 ? 2 * static_cast<int64_t>(sm_count()) : sm_count();
+  // no more token tiles than this, however the rows fall
+  const int64_t units = (R / g.tt + (E < R ? E : R)) * (N / 128);
+  const int64_t want = g.tt == 32 ? (units * KB + kMinSlabs - 1) / kMinSlabs : units;
+  g.blocks = static_cast<int>(want < most ? want : most);
+  g.part_bytes = g.tt == 32 ? static_cast<uint64_t>(g.blocks) * 2 * g.tt * 128 * 4 : 0;
+  g.ticket_bytes = g.tt == 32 ? static_cast<uint64_t>(g.blocks) * 8 : 0;
+  return g;
+}
+
+fg_status check_grouped(int mode, int64_t R, int E, int64_t N, int64_t K) {
+  const char* what = "fg_grouped_gemm";
+  if (!mode_ok(mode)) return fail(FG_ERR_INVALID_ARG, "%s: bad mode %d", what, mode);
+  if (mode == FG_FP8_BLOCK128)
+    return fail(FG_ERR_INVALID_ARG, "%s: not built for fp8_block128 (fp32 block scales); use an MX mode", what);
+  if (E < 1 || E > kMaxExperts) return fail(FG_ERR_SHAPE, "%s: E=%d outside 1..%d", what, E, kMaxExperts);
+  if (R < 0 || R > (int64_t(1) << 24)) return fail(FG_ERR_SHAPE, "%s: R=%lld", what, (long long)R);
+  if (N <= 0 || N % 128) return fail(FG_ERR_SHAPE, "%s: N=%lld per expert must be a multiple of 128", what, (long long)N);
+  return check_nk(mode, N * E, K);
+}
+
+}  // namespace
+
+}  // namespace fg
+
+using namespace fg;
+
+extern "C" {
+
+fg_status fg_grouped_gemm_workspace_size(int mode, int64_t R, int E, int64_t N, int64_t K, uint64_t* bytes) {
+  if (!bytes) return fail(FG_ERR_INVALID_ARG, "null output");
+  fg_status s = check_grouped(mode, R, E, N, K);
+  if (s != FG_OK) return s;
+  const GroupedPlan g = grouped_plan(R, E, N, row_bytes(mode, K) / 128);
+  *bytes = R == 0 ? 0 : g.part_bytes + g.ticket_bytes;
+  return FG_OK;
+}
+
+fg_status fg_grouped_gemm(const void* A, const void* a_scales, int64_t T, const int32_t* rows, int64_t R,
+                          const int32_t* offsets, int E, const fg_bshuf* b, int mode, void* Y, void* workspace,
+                          uint64_t workspace_bytes, uint32_t flags, void* stream) {
+  const char* what = "fg_grouped_gemm";
+  fg_status s = check_desc(b);
+  if (s != FG_OK) return s;
+  if (b->mode != mode)
+    return fail(FG_ERR_LAYOUT, "%s: weight was preshuffled for %s, call asks for %s", what, mode_name(b->mode), mode_name(mode));
+  if (flags & ~FG_FLAG_DEBUG_STALL) return fail(FG_ERR_INVALID_ARG, "%s: unknown flags 0x%x", what, flags);
+  if (E < 1 || b->N % E)
+    return fail(FG_ERR_SHAPE, "%s: the stacked weight's %lld rows do not divide over E=%d experts", what, (long long)b->N, E);
+  const int64_t N = b->N / E, K = b->K;
+  if ((s = check_grouped(mode, R, E, N, K)) != FG_OK) return s;
+  if (T < 0 || T > (int64_t(1) << 24)) return fail(FG_ERR_SHAPE, "%s: T=%lld", what, (long long)T);
+  if (!rows && T < R) return fail(FG_ERR_SHAPE, "%s: A has %lld rows, fewer than R=%lld", what, (long long)T, (long long)R);
+  if (R == 0) return FG_OK;
+  if (T == 0) return fail(FG_ERR_SHAPE, "%s: no rows of A to gather from", what);
+  if (!A || !Y || !offsets) return fail(FG_ERR_INVALID_ARG, "%s: null A, Y or offsets", what);
+  if (mode != FG_BF16 && !a_scales) return fail(FG_ERR_INVALID_ARG, "%s: %s needs A scales", what, mode_name(mode));
+  if (!aligned(A, 16) || !aligned(Y, 16)) return fail(FG_ERR_ALIGN, "%s: A and Y must be 16-byte aligned", what);
+  if (!aligned(offsets, 4) || !aligned(rows, 4) || (mode == FG_FP8_TENSOR && !aligned(a_scales, 4)))
+    return fail(FG_ERR_ALIGN, "%s: offsets, rows and fp32 scales must be 4-byte aligned", what);
+  const int64_t rb = row_bytes(mode, K);
+  const GroupedPlan g = grouped_plan(R, E, N, rb / 128);
+  const uint64_t need = g.part_bytes + g.ticket_bytes;
+  if (need) {
+    if (!workspace || workspace_bytes < need)
+      return fail(FG_ERR_WORKSPACE, "%s: needs a %llu-byte workspace", what, (unsigned long long)need);
+    if (!aligned(workspace, 16)) return fail(FG_ERR_ALIGN, "%s: workspace must be 16-byte aligned", what);
+  }
+  if ((s = check_arch()) != FG_OK) return s;
+  GroupedParams p;
+  memset(&p, 0, sizeof p);
+  p.err = dev_error_ptr();
+  if (!p.err) return fail(FG_ERR_CUDA, "device error word unavailable");
+  CUtensorMap tmap_a, tmap_b;
+  memset(&tmap_b, 0, sizeof tmap_b);
+  if ((s = make_tmap(&tmap_a, A, T, rb, rows ? 1 : 16)) != FG_OK) return s;
+  if (mode == FG_MXFP4_FP8A && (s = make_tmap_fp4w(&tmap_b, b->data, b->N, K)) != FG_OK) return s;
+  p.b_img = static_cast<const uint8_t*>(b->data);
+  p.b_sf = static_cast<const uint8_t*>(b->sf);
+  p.b_s = static_cast<const float*>(b->sf);
+  p.a_scales = a_scales;
+  p.offsets = offsets;
+  p.rows = rows;
+  p.y = static_cast<__nv_bfloat16*>(Y);
+  p.part = static_cast<float*>(workspace);
+  p.tickets = reinterpret_cast<unsigned long long*>(static_cast<uint8_t*>(workspace) + g.part_bytes);
+  p.epoch = next_epoch() & ((1ull << 48) - 1);
+  p.timeout_ns = wait_timeout_ns();
+  p.T = static_cast<int>(T);
+  p.R = static_cast<int>(R);
+  p.E = E;
+  p.N = static_cast<int>(N);
+  p.K = static_cast<int>(K);
+  p.KB = static_cast<int>(rb / 128);
+  p.debug_stall = (flags & FG_FLAG_DEBUG_STALL) ? 1 : 0;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaErrorInvalidValue;
+  switch (mode) {
+    case FG_BF16: e = launch_mode<kBF16>(tmap_a, tmap_b, p, g.tt, g.blocks, st); break;
+    case FG_FP8_TENSOR: e = launch_mode<kTensor>(tmap_a, tmap_b, p, g.tt, g.blocks, st); break;
+    case FG_MXFP8: e = launch_mode<kMXFP8>(tmap_a, tmap_b, p, g.tt, g.blocks, st); break;
+    case FG_MXFP4: e = launch_mode<kMXFP4>(tmap_a, tmap_b, p, g.tt, g.blocks, st); break;
+    case FG_MXFP8_B32: e = launch_mode<kMXFP8B32>(tmap_a, tmap_b, p, g.tt, g.blocks, st); break;
+    case FG_MXFP4_FP8A: e = launch_mode<kMXFP4FP8A>(tmap_a, tmap_b, p, g.tt, g.blocks, st); break;
+  }
+  return e == cudaSuccess ? FG_OK : cuda_fail(e, "grouped product launch");
+}
+
+}  // extern "C"

@@ -116,6 +116,18 @@ __device__ __forceinline__ void tma_load_2d(void* smem_dst, const CUtensorMap* m
       : "memory");
 }
 
+// Four rows y[0..3] of a 2-D tensor map whose box is one row, global -> shared:
+// they land one after the other, swizzled by their place in shared memory (x
+// as for tma_load_2d).
+__device__ __forceinline__ void tma_gather4(void* smem_dst, const CUtensorMap* map, int32_t x, const int (&y)[4],
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
+      "%5, %6}], [%7];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]), "r"(smem_u32(bar))
+      : "memory");
+}
+
 // 3-D tiled tensor copy (TMA) global -> shared (x as for tma_load_2d).
 __device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
                                             uint64_t* bar) {

@@ -170,6 +170,57 @@ def moe_route(logits, top_k, renormalize=True, stream=None):
     return Routing(weights, experts, offsets, rows, slots)
 
 
+def grouped_gemm_workspace_size(mode, rows, experts, n, k):
+    b = ctypes.c_uint64()
+    _fg._check(_fg.lib().fg_grouped_gemm_workspace_size(_fg._mode(mode), rows, experts, n, k, ctypes.byref(b)))
+    return b.value
+
+
+def grouped_gemm(A, pb, offsets, a_scales=None, rows=None, Y=None, workspace=None, flags=0, stream=None):
+    """Y[i] = dequant(A[rows[i]]) . dequant(B_e)^T (bf16 [R][N]) for the rows i of
+    expert e, offsets[e] <= i < offsets[e+1].
+
+    pb is the preshuffled stack of the experts' weights, [E * N][K]; offsets is
+    int32 [E + 1] on the device; A holds codes [T][K] as for gemm().  rows (int32
+    [R]) names the row of A for each row of Y; without it they are the same.
+    Rows of Y that no expert holds are left as they are.
+    """
+    mode, n_all, k = pb.mode, pb.N, pb.K
+    device = pb.data.device
+    _fg._require(A, "A", _fg._a_dtypes(mode), device)
+    if A.dim() != 2 or _fg._row_bytes_of(A) != _fg._a_row_bytes(mode, k):
+        raise ValueError("A must be [T][K] codes of the mode (%d bytes per row for K=%d), got shape %s dtype %s"
+                         % (_fg._a_row_bytes(mode, k), k, tuple(A.shape), A.dtype))
+    t = A.shape[0]
+    _fg._require(offsets, "offsets", (torch.int32,), device)
+    e = offsets.numel() - 1
+    if e < 1 or n_all % e:
+        raise ValueError("offsets must hold E + 1 values, E a divisor of the stacked weight's %d rows" % n_all)
+    n = n_all // e
+    if a_scales is not None and mode != _fg.FG_BF16:
+        dts, count = _fg._scale_spec(mode, t, k, False)
+        _fg._require(a_scales, "a_scales", dts, device, numel=count)
+    if rows is not None:
+        _fg._require(rows, "rows", (torch.int32,), device)
+    r = t if rows is None else rows.numel()
+    if Y is None:
+        Y = torch.empty((r, n), dtype=torch.bfloat16, device=device)
+    else:
+        _fg._require(Y, "Y", _fg._dtypes("bfloat16", "int16"), device, shape=(r, n))
+    need = 0
+    if workspace is None:
+        need = grouped_gemm_workspace_size(mode, r, e, n, k)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    else:
+        _fg._require(workspace, "workspace", device=device)
+        need = workspace.numel() * workspace.element_size()
+    _fg._check(_fg.lib().fg_grouped_gemm(A.data_ptr(), _p(a_scales), t, _p(rows), r, offsets.data_ptr(), e,
+                                         ctypes.byref(pb.desc), mode, Y.data_ptr(), _p(workspace), need, flags,
+                                         _on(device, stream, Y, workspace)))
+    return Y
+
+
 def moe_combine(Y, slots, weights, residual=None, stream=None):
     """out[t] = residual[t] + sum_j weights[t][j] * Y[slots[t][j]] (bf16 [T][N])
     for the experts' rows Y [R][N]; a slot of -1 is no choice."""
