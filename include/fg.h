@@ -363,12 +363,13 @@ FG_API fg_status fg_moe_route(const void* logits, int type, int64_t T, int E, in
  *           0..T-1; NULL: row i itself (T >= R).
  *  offsets  device int32 [E + 1], not decreasing, clamped into 0..R.  Rows of Y
  *           before offsets[0] and from offsets[E] on are not written.
- *  workspace  fg_grouped_gemm_workspace_size bytes; any contents.  Calls that
+ *  workspace  fg_grouped_gemm_workspace_size bytes (gather: rows given); any contents.  Calls that
  *           overlap on the GPU need a workspace each.
  * All modes but FP8_BLOCK128; E <= 1024; R, T <= 2^24.
  * Errors: INVALID_ARG, SHAPE, ALIGN, LAYOUT, WORKSPACE, UNSUPPORTED_ARCH, CUDA.
  */
-FG_API fg_status fg_grouped_gemm_workspace_size(int mode, int64_t R, int E, int64_t N, int64_t K, uint64_t* bytes);
+FG_API fg_status fg_grouped_gemm_workspace_size(int mode, int64_t R, int E, int64_t N, int64_t K, int gather,
+                                                uint64_t* bytes);
 FG_API fg_status fg_grouped_gemm(const void* A, const void* a_scales, int64_t T, const int32_t* rows, int64_t R,
                                  const int32_t* offsets, int E, const fg_bshuf* b, int mode, void* Y, void* workspace,
                                  uint64_t workspace_bytes, uint32_t flags, void* stream);

@@ -72,7 +72,7 @@ def lib():
         "fg_moe_route_workspace_size": ([i64, i32, ctypes.POINTER(u64)], i32),
         "fg_moe_route": ([vp, i32, i64, i32, i64, i32, u32, vp, vp, vp, vp, vp, vp, u64, vp], i32),
         "fg_moe_combine": ([vp, i64, vp, vp, vp, i64, i32, i64, vp, vp], i32),
-        "fg_grouped_gemm_workspace_size": ([i32, i64, i32, i64, i64, ctypes.POINTER(u64)], i32),
+        "fg_grouped_gemm_workspace_size": ([i32, i64, i32, i64, i64, i32, ctypes.POINTER(u64)], i32),
         "fg_grouped_gemm": ([vp, vp, i64, vp, i64, vp, i32, ctypes.POINTER(BShuf), i32, vp, vp, u64, u32, vp], i32),
         "fg_get_error": ([], i32),
         "fg_set_wait_timeout_ns": ([u64], None),

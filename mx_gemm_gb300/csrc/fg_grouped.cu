@@ -17,7 +17,11 @@
 // back to the host.
 //
 //  - TT = 256 (many rows an expert): units are dealt out whole.  Bound by the
-//    tensor cores and the stream from L2.
+//    tensor cores and the stream from L2.  A first kernel lays out what every
+//    weight tile reads again: the gathered rows one after the other (tensor
+//    copies of four indexed rows each took three times as long as the product
+//    itself: 1797 us against 624 us for 32768 mxfp4 rows, 4096 x 7168), and the
+//    token scales as the atoms the tensor core reads.
 //  - TT = 32 (decoding): bound by the weights' bytes from HBM, whatever the
 //    rows.  The K steps of all units form one line that is cut evenly over the
 //    blocks, wherever the cuts fall, so that all SMs stream to the end.  Blocks
@@ -53,6 +57,7 @@ struct GroupedParams {
   const int32_t* offsets;     // [E + 1]
   const int32_t* rows;        // [R] or null
   __nv_bfloat16* y;           // [R][N]
+  const uint8_t* a_sf;        // TT = 256, MX: token scale atoms [tile][K step][atom][2][512]
   float* part;                // [blocks][2][TT][128] partials (cut line)
   unsigned long long* tickets;  // [blocks] arrivals at the unit that begins last in the block
   unsigned long long epoch;
@@ -71,6 +76,7 @@ struct GCfg {
   static constexpr int TOK_ATOMS = (TT + 127) / 128;
   static constexpr int SFW_BYTES = APS * 512;
   static constexpr int SFT_BYTES = APS * TOK_ATOMS * 512;
+  static constexpr bool SCALE_WARPS = APS > 0 && TT == 32;  // else the atoms come by bulk copy
   static constexpr int STAGE_RAW = kSlabBytes + TOK_BYTES + SFW_BYTES + SFT_BYTES;
   static constexpr int STAGE_BYTES = (STAGE_RAW + 1023) / 1024 * 1024;
   static constexpr int SMEM = STAGES * STAGE_BYTES + 1024;
@@ -90,6 +96,7 @@ struct GCfg {
 // The unit's rows and weight tile.
 struct Unit {
   int e, row0, count, n16, nt;  // n16: rows rounded up to 16
+  int tile;                     // token tile, over all experts
 };
 
 // One block's share of a unit: K steps [k0, k1).
@@ -120,6 +127,7 @@ __device__ __forceinline__ Unit unit_at(const Schedule& s, long long u) {
   q.e = a;
   q.nt = r / n;
   const int m = r - q.nt * n;
+  q.tile = s.tiles[a] + m;
   q.row0 = s.offs[a] + m * per;
   q.count = min(per, rows - m * per);
   q.n16 = (q.count + 15) & ~15;
@@ -154,6 +162,32 @@ __device__ __forceinline__ Share share_at(const Schedule& s, int i) {
   return h;
 }
 
+// The offsets, clamped into 0..R, and the token tiles before each expert, by
+// the whole block (any count of warps); ends with the block in step.
+template <int TT>
+__device__ __forceinline__ void read_offsets(const int32_t* offsets, int R, int E, int* offs, int* tiles) {
+  for (int e = threadIdx.x; e <= E; e += blockDim.x) offs[e] = min(max(__ldg(offsets + e), 0), R);
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    int carry = 0;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+      const int e = e0 + lane;
+      const int t = e < E ? (max(0, offs[e + 1] - offs[e]) + TT - 1) / TT : 0;
+      int sum = t;
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const int o = __shfl_up_sync(0xffffffffu, sum, d);
+        if (lane >= d) sum += o;
+      }
+      if (e < E) tiles[e] = carry + sum - t;
+      carry += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    if (lane == 0) tiles[E] = carry;
+  }
+  __syncthreads();
+}
+
 template <int MODE>
 __device__ __forceinline__ void mma_step(uint32_t d, uint64_t a, uint64_t b, int n, int j, int kb, uint32_t sfw,
                                          uint32_t sft, int tok_atoms, uint32_t accum) {
@@ -161,8 +195,10 @@ __device__ __forceinline__ void mma_step(uint32_t d, uint64_t a, uint64_t b, int
     mma_f16(d, a, b, idesc_bf16(128, n), accum);
   } else if (MODE == kTensor) {
     mma_f8f6f4(d, a, b, idesc_e4m3(128, n), accum);
-  } else if (MODE == kMXFP8) {  // the weight's byte of its four-slab atom; the token atoms repeat theirs
-    mma_mxf8f6f4(d, a, b, idesc_mx(128, n, kF8f6f4E4M3, kb & 3, j), sfw, sft, accum);
+  } else if (MODE == kMXFP8) {
+    // the weight's byte of its four-slab atom; the token atoms likewise, or
+    // (TT = 32) with the slab's scale in all four bytes
+    mma_mxf8f6f4(d, a, b, idesc_mx(128, n, kF8f6f4E4M3, kb & 3, kb & 3), sfw, sft, accum);
   } else if (MODE == kMXFP8B32) {
     mma_mxf8f6f4(d, a, b, idesc_mx(128, n, kF8f6f4E4M3, j, j), sfw, sft, accum);
   } else if (MODE == kMXFP4FP8A) {
@@ -173,11 +209,18 @@ __device__ __forceinline__ void mma_step(uint32_t d, uint64_t a, uint64_t b, int
   }
 }
 
-// tmap_a: A as rows of bytes, boxes of 128 bytes x 16 rows (GATHER: x 1 row);
+// A as rows of bytes: boxes of 128 bytes x 16, 32, 64, 128 rows, so that a tile
+// of up to 256 rows takes few copies and moves only its own rows (a copy costs
+// its issuing thread tens of cycles: 16 boxes of 16 rows a K step held the
+// whole kernel back).  TT = 32 uses the first; GATHER: 1 row.
+struct AMaps {
+  CUtensorMap rows[4];
+};
+
 // tmap_b: fp8 x fp4 only, the weight image's blocks.
 template <int MODE, int TT, bool GATHER>
 __global__ void __launch_bounds__(GCfg<MODE, TT>::THREADS, GCfg<MODE, TT>::BLOCKS_PER_SM)
-    grouped_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
+    grouped_kernel(const __grid_constant__ AMaps a_maps, const __grid_constant__ CUtensorMap tmap_b,
                    const GroupedParams p) {
   using C = GCfg<MODE, TT>;
   constexpr int ST = C::STAGES;
@@ -188,7 +231,7 @@ __global__ void __launch_bounds__(GCfg<MODE, TT>::THREADS, GCfg<MODE, TT>::BLOCK
   __shared__ __align__(8) uint64_t accf_bar[C::ACCS], acce_bar[C::ACCS];
   __shared__ __align__(8) uint64_t stall_bar, drain_bar;
   __shared__ uint32_t tmem_base_sh;
-  __shared__ int abort_sh, issued_sh, consumed_sh, mma_any_sh, last_sh;
+  __shared__ int abort_sh, issued_sh, consumed_sh, last_sh;
   __shared__ int offs_sh[kMaxExperts + 1], tiles_sh[kMaxExperts + 1];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -196,7 +239,7 @@ __global__ void __launch_bounds__(GCfg<MODE, TT>::THREADS, GCfg<MODE, TT>::BLOCK
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < ST; ++i) {
-      mbar_init(&full_bar[i], C::APS ? 3 : 1);  // MX: + one arrival per scale warp
+      mbar_init(&full_bar[i], C::SCALE_WARPS ? 3 : 1);  // + one arrival per scale warp
       mbar_init(&empty_bar[i], 1);
     }
     for (int i = 0; i < C::ACCS; ++i) {
@@ -208,7 +251,6 @@ __global__ void __launch_bounds__(GCfg<MODE, TT>::THREADS, GCfg<MODE, TT>::BLOCK
     abort_sh = 0;
     issued_sh = 0;
     consumed_sh = 0;
-    mma_any_sh = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -217,28 +259,11 @@ __global__ void __launch_bounds__(GCfg<MODE, TT>::THREADS, GCfg<MODE, TT>::BLOCK
   }
   pdl_wait();
   if (threadIdx.x == 0) pdl_launch_dependents();
-  // offsets, clamped into 0..R and to counts of at least zero, and the token
-  // tiles before each expert
-  for (int e = threadIdx.x; e <= p.E; e += C::THREADS) offs_sh[e] = min(max(__ldg(p.offsets + e), 0), p.R);
-  __syncthreads();
   if (warp == 0) {
-    prefetch_tmap(&tmap_a);
+    prefetch_tmap(&a_maps.rows[0]);
     if (MODE == kMXFP4FP8A) prefetch_tmap(&tmap_b);
-    int carry = 0;
-    for (int e0 = 0; e0 < p.E; e0 += 32) {
-      const int e = e0 + lane;
-      const int t = e < p.E ? (max(0, offs_sh[e + 1] - offs_sh[e]) + TT - 1) / TT : 0;
-      int sum = t;
-#pragma unroll
-      for (int d = 1; d < 32; d *= 2) {
-        const int o = __shfl_up_sync(0xffffffffu, sum, d);
-        if (lane >= d) sum += o;
-      }
-      if (e < p.E) tiles_sh[e] = carry + sum - t;
-      carry += __shfl_sync(0xffffffffu, sum, 31);
-    }
-    if (lane == 0) tiles_sh[p.E] = carry;
   }
+  read_offsets<TT>(p.offsets, p.R, p.E, offs_sh, tiles_sh);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -271,49 +296,59 @@ __global__ void __launch_bounds__(GCfg<MODE, TT>::THREADS, GCfg<MODE, TT>::BLOCK
       const Unit q = unit_at<TT>(s, h.u);
       // gathered: this lane's groups of four rows; rows past the tile's end
       // repeat its last one, indexes are clamped into A
-      constexpr int G4 = GATHER ? (TT + 127) / 128 : 1;
-      int idx[G4][4];
+      int idx[4];
       if (GATHER) {
 #pragma unroll
-        for (int g = 0; g < G4; ++g)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int m = min((g * 32 + lane) * 4 + j, q.count - 1);
-            idx[g][j] = min(max(__ldg(p.rows + q.row0 + m), 0), p.T - 1);
-          }
+        for (int j = 0; j < 4; ++j)
+          idx[j] = min(max(__ldg(p.rows + q.row0 + min(lane * 4 + j, q.count - 1)), 0), p.T - 1);
       }
       const long long wt = static_cast<long long>(q.e) * s.NT + q.nt;  // weight tile of the stacked image
       for (int kb = h.k0; kb < h.k1; ++kb, ++it) {
         const int slot = it % ST;
-        const bool w = mbar_wait(&empty_bar[slot], ((it / ST) & 1) ^ 1u, T, p.err, 61);
-        if (!__all_sync(0xffffffffu, w)) {
-          ok = false;
-          break;
-        }
+        ok = __all_sync(0xffffffffu, mbar_wait(&empty_bar[slot], ((it / ST) & 1) ^ 1u, T, p.err, 61));
+        if (!ok) break;
         uint8_t* st = smem + slot * C::STAGE_BYTES;
-        if (lane == 0) {
+        uint8_t* tok = st + kSlabBytes;
+        // rows that are copied; the accumulator's columns past them hold what
+        // the rows of an earlier step left and are not stored
+        const int copied = GATHER ? (q.count + 3) & ~3 : q.n16;
+        if (elect_one()) {
           mbar_arrive_expect_tx(&full_bar[slot],
-                                (MODE == kMXFP4FP8A ? kSlabBytes / 2 : kSlabBytes) + q.n16 * 128 + C::SFW_BYTES);
+                                (MODE == kMXFP4FP8A ? kSlabBytes / 2 : kSlabBytes) + copied * 128 + C::SFW_BYTES +
+                                    (C::SCALE_WARPS ? 0 : C::SFT_BYTES));
           const long long slab = wt * s.KB + kb;
           if (MODE == kMXFP4FP8A)
             tma_load_3d(st, &tmap_b, 0, 0, static_cast<int32_t>(slab), &full_bar[slot]);
           else
             bulk_g2s(st, p.b_img + slab * kSlabBytes, kSlabBytes, &full_bar[slot]);
+          if (!GATHER) {
+            int m = 0;
+            if (TT == 256 && q.n16 == 256) {
+              tma_load_2d(tok, &a_maps.rows[3], kb * 128, q.row0, &full_bar[slot]);
+              m = 128;
+            }
+#pragma unroll
+            for (int b = TT == 256 ? 3 : 1; b >= 0; --b) {
+              if (q.n16 - m >= 16 << b) {
+                tma_load_2d(tok + m * 128, &a_maps.rows[b], kb * 128, q.row0 + m, &full_bar[slot]);
+                m += 16 << b;
+              }
+            }
+          }
           if (C::APS) {
             const long long atom = MODE == kMXFP8 ? wt * ((s.KB + 3) / 4) + kb / 4 : slab * C::APS;
             bulk_g2s(st + kSlabBytes + C::TOK_BYTES, p.b_sf + atom * 512, C::SFW_BYTES, &full_bar[slot]);
+            if (!C::SCALE_WARPS) {
+              const long long step = MODE == kMXFP8 ? static_cast<long long>(q.tile) * ((s.KB + 3) / 4) + kb / 4
+                                                    : static_cast<long long>(q.tile) * s.KB + kb;
+              bulk_g2s(st + kSlabBytes + C::TOK_BYTES + C::SFW_BYTES, p.a_sf + step * C::SFT_BYTES, C::SFT_BYTES,
+                       &full_bar[slot]);
+            }
           }
         }
         __syncwarp();
-        uint8_t* tok = st + kSlabBytes;
         if (GATHER) {
-#pragma unroll
-          for (int g = 0; g < G4; ++g) {
-            const int m = (g * 32 + lane) * 4;
-            if (m < q.n16) tma_gather4(tok + m * 128, &tmap_a, kb * 128, idx[g], &full_bar[slot]);
-          }
-        } else if (lane * 16 < q.n16) {
-          tma_load_2d(tok + lane * 2048, &tmap_a, kb * 128, q.row0 + lane * 16, &full_bar[slot]);
+          if (lane * 4 < copied) tma_gather4(tok + lane * 512, &a_maps.rows[0], kb * 128, idx, &full_bar[slot]);
         }
       }
     }
@@ -323,33 +358,28 @@ __global__ void __launch_bounds__(GCfg<MODE, TT>::THREADS, GCfg<MODE, TT>::BLOCK
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMAs
-    if (lane == 0) {
-      bool ok = true;
-      if (p.debug_stall) ok = mbar_wait(&stall_bar, 0, T, p.err, 62);
-      int it = 0;
-      for (int i = 0; ok && i < shares; ++i) {
-        const Share h = share_at<CUT>(s, i);
-        const Unit q = unit_at<TT>(s, h.u);
-        const int acc = i % C::ACCS;
-        if (!mbar_wait(&acce_bar[acc], ((i / C::ACCS) & 1) ^ 1u, T, p.err, 63)) {
-          ok = false;
-          break;
-        }
+    bool ok = true;
+    if (p.debug_stall) ok = __all_sync(0xffffffffu, mbar_wait(&stall_bar, 0, T, p.err, 62));
+    int it = 0;
+    for (int i = 0; ok && i < shares; ++i) {
+      const Share h = share_at<CUT>(s, i);
+      const Unit q = unit_at<TT>(s, h.u);
+      const int acc = i % C::ACCS;
+      ok = __all_sync(0xffffffffu, mbar_wait(&acce_bar[acc], ((i / C::ACCS) & 1) ^ 1u, T, p.err, 63));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t d = tmem + acc * TT;
+      for (int kb = h.k0; kb < h.k1; ++kb, ++it) {
+        const int slot = it % ST;
+        ok = __all_sync(0xffffffffu, mbar_wait(&full_bar[slot], (it / ST) & 1, T, p.err, 64));
+        if (!ok) break;
         tc_fence_after();
-        const uint32_t d = tmem + acc * TT;
-        for (int kb = h.k0; kb < h.k1; ++kb, ++it) {
-          const int slot = it % ST;
-          if (!mbar_wait(&full_bar[slot], (it / ST) & 1, T, p.err, 64)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          mma_any_sh = 1;
-          uint8_t* st = smem + slot * C::STAGE_BYTES;
-          const uint32_t sfw = tmem + C::ACC_COLS + slot * (C::SFW_COLS + C::SFT_COLS);
-          const uint32_t sft = sfw + C::SFW_COLS;
+        const uint32_t st = smem_u32(smem) + slot * C::STAGE_BYTES;
+        const uint32_t sfw = tmem + C::ACC_COLS + slot * (C::SFW_COLS + C::SFT_COLS);
+        const uint32_t sft = sfw + C::SFW_COLS;
+        if (elect_one()) {
           if (C::APS) {
-            const uint32_t sw = smem_u32(st + kSlabBytes + C::TOK_BYTES);
+            const uint32_t sw = st + kSlabBytes + C::TOK_BYTES;
             const uint32_t stk = sw + C::SFW_BYTES;
 #pragma unroll
             for (int g = 0; g < C::APS; ++g) {
@@ -363,26 +393,29 @@ __global__ void __launch_bounds__(GCfg<MODE, TT>::THREADS, GCfg<MODE, TT>::BLOCK
           }
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            mma_step<MODE>(d, sdesc_sw128(smem_u32(st + j * 32)), sdesc_sw128(smem_u32(st + kSlabBytes + j * 32)), q.n16, j,
-                           kb, sfw, sft, C::TOK_ATOMS, (kb > h.k0 || j > 0) ? 1u : 0u);
+            mma_step<MODE>(d, sdesc_sw128(st + j * 32), sdesc_sw128(st + kSlabBytes + j * 32), q.n16, j, kb, sfw, sft,
+                           C::TOK_ATOMS, (kb > h.k0 || j > 0) ? 1u : 0u);
           tc_commit(&empty_bar[slot]);
         }
-        if (!ok) {
-          ++it;
-          break;
-        }
-        tc_commit(&accf_bar[acc]);
+        __syncwarp();
       }
+      if (!ok) break;
+      if (elect_one()) tc_commit(&accf_bar[acc]);
+      __syncwarp();
+    }
+    if (lane == 0) {
+      // a step whose wait gave up was not consumed; the teardown waits for it
       consumed_sh = it;
       if (!ok) abort_sh = 1;
-      if (mma_any_sh) {
-        tc_commit(&drain_bar);
-        mbar_wait(&drain_bar, 0, T, p.err, 65);
-      }
+    }
+    if (it > 0) {  // every MMA and commit has landed before the block lets go of its memory
+      if (elect_one()) tc_commit(&drain_bar);
+      __syncwarp();
+      mbar_wait(&drain_bar, 0, T, p.err, 65);
     }
   } else if (warp < 4) {
     // ----------------------------------------------------- token scale atoms
-    if (C::APS) {
+    if (C::SCALE_WARPS) {
       constexpr int PT = (TT + 63) / 64;  // rows of the tile per thread
       const int st_id = threadIdx.x - 64;
       const uint8_t* asf = static_cast<const uint8_t*>(p.a_scales);
@@ -541,8 +574,92 @@ __global__ void __launch_bounds__(GCfg<MODE, TT>::THREADS, GCfg<MODE, TT>::BLOCK
   if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
 }
 
+// What TT = 256 lays out first: the gathered rows of A (a_rows) and the token
+// scale atoms (a_sf), each where wanted.
+struct PrepParams {
+  const uint8_t* a;
+  const uint8_t* scales;
+  const int32_t* offsets;
+  const int32_t* rows;
+  uint8_t* a_rows;  // [R][rb] or null
+  uint8_t* a_sf;    // [tile][NA][2][512], NA atoms a 128-row block (null: no MX scales)
+  int T, R, E;
+  int rb;           // bytes of a row of A
+  int sb;           // scale bytes of a row
+  int NA;           // atoms of a 128-row block: four scale bytes of each row to an atom
+};
+
+__global__ void __launch_bounds__(256) grouped_prep_kernel(const PrepParams p) {
+  __shared__ int offs_sh[kMaxExperts + 1], tiles_sh[kMaxExperts + 1];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t threads = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  const int64_t tid = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  if (p.a_rows) {
+    // a warp per row, 16 bytes a lane
+    const int lane = threadIdx.x & 31;
+    for (int64_t i = tid >> 5; i < p.R; i += threads >> 5) {
+      const int row = min(max(__ldg(p.rows + i), 0), p.T - 1);
+      const uint4* src = reinterpret_cast<const uint4*>(p.a + static_cast<size_t>(row) * p.rb);
+      uint4* dst = reinterpret_cast<uint4*>(p.a_rows + static_cast<size_t>(i) * p.rb);
+      for (int c0 = 0; c0 < p.rb / 16; c0 += 128) {
+        uint4 v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (c0 + j * 32 + lane < p.rb / 16) v[j] = __ldg(src + c0 + j * 32 + lane);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (c0 + j * 32 + lane < p.rb / 16) dst[c0 + j * 32 + lane] = v[j];
+      }
+    }
+  }
+  if (!p.a_sf) return;
+  read_offsets<256>(p.offsets, p.R, p.E, offs_sh, tiles_sh);
+  Schedule s;
+  s.offs = offs_sh;
+  s.tiles = tiles_sh;
+  s.E = p.E;
+  s.NT = 1;
+  // A thread takes four atoms in a row of one line: byte 16 * line + 4 * b + j
+  // of an atom belongs to row 32 * b + line of its 128, scale byte 4 * atom + j.
+  const int quads = (p.NA + 3) / 4;
+  const int64_t total = static_cast<int64_t>(tiles_sh[p.E]) * quads * 64;
+  for (int64_t i = tid; i < total; i += threads) {
+    const int line = static_cast<int>(i & 31), half = static_cast<int>(i >> 5) & 1;
+    const int64_t tq = i >> 6;
+    const int tile = static_cast<int>(tq / quads), quad = static_cast<int>(tq - static_cast<int64_t>(tile) * quads);
+    const Unit q = unit_at<256>(s, tile);
+    if (half * 128 >= q.n16) continue;
+    uint32_t w[4][4];  // [atom][block of 32 rows]
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const int m = min(half * 128 + b * 32 + line, q.count - 1);
+      int row = q.row0 + m;
+      if (p.rows) row = min(max(__ldg(p.rows + row), 0), p.T - 1);
+      const uint8_t* src = p.scales + static_cast<size_t>(row) * p.sb;
+#pragma unroll
+      for (int a = 0; a < 4; ++a) {
+        uint32_t v = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int c = (quad * 4 + a) * 4 + j;
+          if (c < p.sb) v |= static_cast<uint32_t>(__ldg(src + c)) << (8 * j);
+        }
+        w[a][b] = v;
+      }
+    }
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      const int atom = quad * 4 + a;
+      if (atom < p.NA)
+        *reinterpret_cast<uint4*>(p.a_sf + ((static_cast<size_t>(tile) * p.NA + atom) * 2 + half) * 512 + line * 16) =
+            make_uint4(w[a][0], w[a][1], w[a][2], w[a][3]);
+    }
+  }
+}
+
 template <int MODE, int TT, bool GATHER>
-cudaError_t launch_one(const CUtensorMap& tmap_a, const CUtensorMap& tmap_b, const GroupedParams& p, int blocks,
+cudaError_t launch_one(const AMaps& a_maps, const CUtensorMap& tmap_b, const GroupedParams& p, int blocks,
                        cudaStream_t stream) {
   using C = GCfg<MODE, TT>;
   auto* kernel = &grouped_kernel<MODE, TT, GATHER>;
@@ -558,35 +675,62 @@ cudaError_t launch_one(const CUtensorMap& tmap_a, const CUtensorMap& tmap_b, con
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = pdl_enabled() ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, tmap_a, tmap_b, p);
+  return cudaLaunchKernelEx(&cfg, kernel, a_maps, tmap_b, p);
 }
 
 template <int MODE>
-cudaError_t launch_mode(const CUtensorMap& tmap_a, const CUtensorMap& tmap_b, const GroupedParams& p, int tt, int blocks,
+cudaError_t launch_mode(const AMaps& a_maps, const CUtensorMap& tmap_b, const GroupedParams& p, int tt, int blocks,
                         cudaStream_t stream) {
   if (tt == 32)
-    return p.rows ? launch_one<MODE, 32, true>(tmap_a, tmap_b, p, blocks, stream)
-                  : launch_one<MODE, 32, false>(tmap_a, tmap_b, p, blocks, stream);
-  return p.rows ? launch_one<MODE, 256, true>(tmap_a, tmap_b, p, blocks, stream)
-                : launch_one<MODE, 256, false>(tmap_a, tmap_b, p, blocks, stream);
+    return p.rows ? launch_one<MODE, 32, true>(a_maps, tmap_b, p, blocks, stream)
+                  : launch_one<MODE, 32, false>(a_maps, tmap_b, p, blocks, stream);
+  return launch_one<MODE, 256, false>(a_maps, tmap_b, p, blocks, stream);
 }
 
-// Token tile and blocks of a call.
+cudaError_t launch_prep(const PrepParams& p, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(sm_count() * 8);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = pdl_enabled() ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, grouped_prep_kernel, p);
+}
+
+// Token tile, blocks and workspace of a call: partials and tickets (tt 32), or
+// scale atoms and gathered rows (tt 256), in this order.
 struct GroupedPlan {
   int tt, blocks;
-  uint64_t part_bytes, ticket_bytes;
+  int atoms;  // scale atoms of a 128-row block
+  uint64_t part_bytes, ticket_bytes, sf_bytes, rows_bytes;
+  uint64_t total() const { return part_bytes + ticket_bytes + sf_bytes + rows_bytes; }
 };
 
-GroupedPlan grouped_plan(int64_t R, int64_t E, int64_t N, int64_t KB) {
+GroupedPlan grouped_plan(int mode, int64_t R, int64_t E, int64_t N, int64_t K, bool gather) {
   GroupedPlan g;
+  memset(&g, 0, sizeof g);
+  if (R == 0) return g;
+  const int64_t KB = row_bytes(mode, K) / 128;
   g.tt = R <= 16 * E ? 32 : 256;
   const int64_t most = g.tt == 32 ? 2 * static_cast<int64_t>(sm_count()) : sm_count();
   // no more token tiles than this, however the rows fall
-  const int64_t units = (R / g.tt + (E < R ? E : R)) * (N / 128);
+  const int64_t tiles = R / g.tt + (E < R ? E : R);
+  const int64_t units = tiles * (N / 128);
   const int64_t want = g.tt == 32 ? (units * KB + kMinSlabs - 1) / kMinSlabs : units;
   g.blocks = static_cast<int>(want < most ? want : most);
-  g.part_bytes = g.tt == 32 ? static_cast<uint64_t>(g.blocks) * 2 * g.tt * 128 * 4 : 0;
-  g.ticket_bytes = g.tt == 32 ? static_cast<uint64_t>(g.blocks) * 8 : 0;
+  if (g.tt == 32) {
+    g.part_bytes = static_cast<uint64_t>(g.blocks) * 2 * g.tt * 128 * 4;
+    g.ticket_bytes = static_cast<uint64_t>(g.blocks) * 8;
+  } else {
+    if (is_mx(mode)) {
+      g.atoms = static_cast<int>((mx_sf_cols(mode, K) + 3) / 4);
+      g.sf_bytes = static_cast<uint64_t>(tiles) * g.atoms * 1024;
+    }
+    if (gather) g.rows_bytes = static_cast<uint64_t>(R) * row_bytes(mode, K);
+  }
   return g;
 }
 
@@ -609,12 +753,12 @@ using namespace fg;
 
 extern "C" {
 
-fg_status fg_grouped_gemm_workspace_size(int mode, int64_t R, int E, int64_t N, int64_t K, uint64_t* bytes) {
+fg_status fg_grouped_gemm_workspace_size(int mode, int64_t R, int E, int64_t N, int64_t K, int gather,
+                                         uint64_t* bytes) {
   if (!bytes) return fail(FG_ERR_INVALID_ARG, "null output");
   fg_status s = check_grouped(mode, R, E, N, K);
   if (s != FG_OK) return s;
-  const GroupedPlan g = grouped_plan(R, E, N, row_bytes(mode, K) / 128);
-  *bytes = R == 0 ? 0 : g.part_bytes + g.ticket_bytes;
+  *bytes = grouped_plan(mode, R, E, N, K, gather != 0).total();
   return FG_OK;
 }
 
@@ -641,8 +785,8 @@ fg_status fg_grouped_gemm(const void* A, const void* a_scales, int64_t T, const 
   if (!aligned(offsets, 4) || !aligned(rows, 4) || (mode == FG_FP8_TENSOR && !aligned(a_scales, 4)))
     return fail(FG_ERR_ALIGN, "%s: offsets, rows and fp32 scales must be 4-byte aligned", what);
   const int64_t rb = row_bytes(mode, K);
-  const GroupedPlan g = grouped_plan(R, E, N, rb / 128);
-  const uint64_t need = g.part_bytes + g.ticket_bytes;
+  const GroupedPlan g = grouped_plan(mode, R, E, N, K, rows != nullptr);
+  const uint64_t need = g.total();
   if (need) {
     if (!workspace || workspace_bytes < need)
       return fail(FG_ERR_WORKSPACE, "%s: needs a %llu-byte workspace", what, (unsigned long long)need);
@@ -653,9 +797,15 @@ fg_status fg_grouped_gemm(const void* A, const void* a_scales, int64_t T, const 
   memset(&p, 0, sizeof p);
   p.err = dev_error_ptr();
   if (!p.err) return fail(FG_ERR_CUDA, "device error word unavailable");
-  CUtensorMap tmap_a, tmap_b;
+  AMaps a_maps;
+  CUtensorMap tmap_b;
+  memset(&a_maps, 0, sizeof a_maps);
   memset(&tmap_b, 0, sizeof tmap_b);
-  if ((s = make_tmap(&tmap_a, A, T, rb, rows ? 1 : 16)) != FG_OK) return s;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  uint8_t* a_rows = g.rows_bytes ? ws + g.sf_bytes : nullptr;  // A's rows in the order of Y's
+  const bool indexed = rows && !a_rows;
+  for (int i = 0; i < (indexed ? 1 : (g.tt == 32 ? 2 : 4)); ++i)
+    if ((s = make_tmap(&a_maps.rows[i], a_rows ? a_rows : A, a_rows ? R : T, rb, indexed ? 1 : 16u << i)) != FG_OK) return s;
   if (mode == FG_MXFP4_FP8A && (s = make_tmap_fp4w(&tmap_b, b->data, b->N, K)) != FG_OK) return s;
   p.b_img = static_cast<const uint8_t*>(b->data);
   p.b_sf = static_cast<const uint8_t*>(b->sf);
@@ -664,8 +814,9 @@ fg_status fg_grouped_gemm(const void* A, const void* a_scales, int64_t T, const 
   p.offsets = offsets;
   p.rows = rows;
   p.y = static_cast<__nv_bfloat16*>(Y);
-  p.part = static_cast<float*>(workspace);
-  p.tickets = reinterpret_cast<unsigned long long*>(static_cast<uint8_t*>(workspace) + g.part_bytes);
+  p.a_sf = ws;
+  p.part = reinterpret_cast<float*>(ws);
+  p.tickets = reinterpret_cast<unsigned long long*>(ws + g.part_bytes);
   p.epoch = next_epoch() & ((1ull << 48) - 1);
   p.timeout_ns = wait_timeout_ns();
   p.T = static_cast<int>(T);
@@ -677,13 +828,19 @@ fg_status fg_grouped_gemm(const void* A, const void* a_scales, int64_t T, const 
   p.debug_stall = (flags & FG_FLAG_DEBUG_STALL) ? 1 : 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaErrorInvalidValue;
+  if (g.sf_bytes || g.rows_bytes) {
+    PrepParams q{static_cast<const uint8_t*>(A), static_cast<const uint8_t*>(a_scales), offsets, rows, a_rows,
+                 g.sf_bytes ? ws : nullptr, p.T, p.R, E, static_cast<int>(rb),
+                 is_mx(mode) ? static_cast<int>(mx_sf_cols(mode, K)) : 0, g.atoms};
+    if ((e = launch_prep(q, st)) != cudaSuccess) return cuda_fail(e, "grouped product's layout launch");
+  }
   switch (mode) {
-    case FG_BF16: e = launch_mode<kBF16>(tmap_a, tmap_b, p, g.tt, g.blocks, st); break;
-    case FG_FP8_TENSOR: e = launch_mode<kTensor>(tmap_a, tmap_b, p, g.tt, g.blocks, st); break;
-    case FG_MXFP8: e = launch_mode<kMXFP8>(tmap_a, tmap_b, p, g.tt, g.blocks, st); break;
-    case FG_MXFP4: e = launch_mode<kMXFP4>(tmap_a, tmap_b, p, g.tt, g.blocks, st); break;
-    case FG_MXFP8_B32: e = launch_mode<kMXFP8B32>(tmap_a, tmap_b, p, g.tt, g.blocks, st); break;
-    case FG_MXFP4_FP8A: e = launch_mode<kMXFP4FP8A>(tmap_a, tmap_b, p, g.tt, g.blocks, st); break;
+    case FG_BF16: e = launch_mode<kBF16>(a_maps, tmap_b, p, g.tt, g.blocks, st); break;
+    case FG_FP8_TENSOR: e = launch_mode<kTensor>(a_maps, tmap_b, p, g.tt, g.blocks, st); break;
+    case FG_MXFP8: e = launch_mode<kMXFP8>(a_maps, tmap_b, p, g.tt, g.blocks, st); break;
+    case FG_MXFP4: e = launch_mode<kMXFP4>(a_maps, tmap_b, p, g.tt, g.blocks, st); break;
+    case FG_MXFP8_B32: e = launch_mode<kMXFP8B32>(a_maps, tmap_b, p, g.tt, g.blocks, st); break;
+    case FG_MXFP4_FP8A: e = launch_mode<kMXFP4FP8A>(a_maps, tmap_b, p, g.tt, g.blocks, st); break;
   }
   return e == cudaSuccess ? FG_OK : cuda_fail(e, "grouped product launch");
 }

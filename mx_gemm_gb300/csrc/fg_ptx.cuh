@@ -24,6 +24,17 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
   return t;
 }
 
+// True in one lane of a converged warp, the same one each time.  Copies and
+// MMAs that a whole warp reaches and one lane issues under this predicate cost
+// the issuing warp far less than in a loop that one lane runs alone (measured:
+// eight copies and their barrier 380 against 690 cycles): the operands stay
+// uniform over the warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+
 // ------------------------------------------------------------------ mbarrier
 
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {

@@ -170,9 +170,10 @@ def moe_route(logits, top_k, renormalize=True, stream=None):
     return Routing(weights, experts, offsets, rows, slots)
 
 
-def grouped_gemm_workspace_size(mode, rows, experts, n, k):
+def grouped_gemm_workspace_size(mode, rows, experts, n, k, gather=False):
+    """Workspace bytes of grouped_gemm for `rows` rows of Y (gather: with row indexes)."""
     b = ctypes.c_uint64()
-    _fg._check(_fg.lib().fg_grouped_gemm_workspace_size(_fg._mode(mode), rows, experts, n, k, ctypes.byref(b)))
+    _fg._check(_fg.lib().fg_grouped_gemm_workspace_size(_fg._mode(mode), rows, experts, n, k, int(gather), ctypes.byref(b)))
     return b.value
 
 
@@ -209,7 +210,7 @@ def grouped_gemm(A, pb, offsets, a_scales=None, rows=None, Y=None, workspace=Non
         _fg._require(Y, "Y", _fg._dtypes("bfloat16", "int16"), device, shape=(r, n))
     need = 0
     if workspace is None:
-        need = grouped_gemm_workspace_size(mode, r, e, n, k)
+        need = grouped_gemm_workspace_size(mode, r, e, n, k, rows is not None)
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=device)
     else:
