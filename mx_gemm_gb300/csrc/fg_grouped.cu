@@ -47,7 +47,8 @@ namespace {
 
 constexpr int kMaxExperts = 1024;
 constexpr int kSlabBytes = 16384;
-constexpr int kMinSlabs = 4;  // K steps a block of the cut line takes at least
+constexpr int kMinSlabs = 4;    // K steps a block of the cut line takes at least
+constexpr int kShareSteps = 8;  // see the schedule
 
 struct GroupedParams {
   const uint8_t* b_img;
@@ -71,7 +72,9 @@ template <int MODE, int TT>
 struct GCfg {
   static constexpr int APS = MODE == kMXFP4 ? 2 : (is_mx(MODE) ? 1 : 0);
   static constexpr bool CUT = TT == 32;           // the cut line of K steps
-  static constexpr int STAGES = 4;
+  // fp8 x fp4 moves half a stage's bytes from HBM: one stage more (28.5 -> 28.2 us
+  // for one token, 103 -> 100 us for eight); the 8-bit modes lost 2-4 % with it
+  static constexpr int STAGES = TT == 32 && MODE == kMXFP4FP8A ? 5 : 4;
   static constexpr int TOK_BYTES = TT * 128;
   static constexpr int TOK_ATOMS = (TT + 127) / 128;
   static constexpr int SFW_BYTES = APS * 512;
@@ -90,7 +93,10 @@ struct GCfg {
       TMEM_NEED <= 64 ? 64 : (TMEM_NEED <= 128 ? 128 : (TMEM_NEED <= 256 ? 256 : 512));
   static constexpr int BLOCKS_PER_SM = TT == 32 ? 2 : 1;
   static_assert(TMEM_NEED <= 512 && BLOCKS_PER_SM * TMEM_COLS <= 512, "TMEM budget");
-  static_assert(BLOCKS_PER_SM * (SMEM + 10240) <= 232448, "shared memory budget");
+  // with the schedule of E experts: two blocks an SM up to 500 experts at TT = 32
+  static constexpr int smem(int E) { return SMEM + 8 * (E + 1); }
+  static_assert(SMEM + 8 * (kMaxExperts + 1) <= 232448 - 1024 && BLOCKS_PER_SM * (SMEM + 8 * 500 + 1536) <= 233472,
+                "shared memory budget");
 };
 
 // The unit's rows and weight tile.
@@ -110,6 +116,7 @@ struct Schedule {
   const int* tiles;  // [E + 1] token tiles before expert e
   long long units, W, lo, hi;
   int E, NT, KB, blocks, c;
+  bool cut;  // the line of all K steps is cut evenly; else units are dealt out whole
 };
 
 template <int TT>
@@ -140,16 +147,14 @@ __device__ __forceinline__ int holder_of(const Schedule& s, long long x) {
   return static_cast<int>(((x + 1) * s.blocks + s.W - 1) / s.W) - 1;
 }
 
-template <bool CUT>
 __device__ __forceinline__ int share_count(const Schedule& s) {
-  if (!CUT) return s.c < s.units ? static_cast<int>((s.units - s.c + s.blocks - 1) / s.blocks) : 0;
+  if (!s.cut) return s.c < s.units ? static_cast<int>((s.units - s.c + s.blocks - 1) / s.blocks) : 0;
   return s.hi > s.lo ? static_cast<int>((s.hi - 1) / s.KB - s.lo / s.KB + 1) : 0;
 }
 
-template <bool CUT>
 __device__ __forceinline__ Share share_at(const Schedule& s, int i) {
   Share h;
-  if (!CUT) {
+  if (!s.cut) {
     h.u = s.c + static_cast<long long>(i) * s.blocks;
     h.k0 = 0;
     h.k1 = s.KB;
@@ -232,7 +237,8 @@ __global__ void __launch_bounds__(GCfg<MODE, TT>::THREADS, GCfg<MODE, TT>::BLOCK
   __shared__ __align__(8) uint64_t stall_bar, drain_bar;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh, issued_sh, consumed_sh, last_sh;
-  __shared__ int offs_sh[kMaxExperts + 1], tiles_sh[kMaxExperts + 1];
+  int* offs_sh = reinterpret_cast<int*>(smem + ST * C::STAGE_BYTES);
+  int* tiles_sh = offs_sh + p.E + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint64_t T = p.timeout_ns;
@@ -279,48 +285,80 @@ __global__ void __launch_bounds__(GCfg<MODE, TT>::THREADS, GCfg<MODE, TT>::BLOCK
   s.W = s.units * s.KB;
   s.c = blockIdx.x;
   s.blocks = gridDim.x;
+  s.cut = false;
   if (CUT) {
+    // Sharing units costs a round of partials at the end, about as long as
+    // kShareSteps K steps of every block.  Units stay whole where dealing them
+    // out leaves less than that idle, and where there is at most one for each
+    // block but enough of them to keep the memory busy (a block alone has 64 KB
+    // in flight).  256 units on 304 blocks, 8-bit, K = 7168: see the table.
+    const long long G = gridDim.x;
+    const long long rounds = (s.units + G - 1) / G;
+    const bool one_each = s.units <= G && 10 * s.units >= 6 * G;
+    s.cut = !(one_each || (rounds * G - s.units) * s.KB <= kShareSteps * G);
+  }
+  if (s.cut) {
     const long long most = (s.W + kMinSlabs - 1) / kMinSlabs;
     s.blocks = static_cast<int>(min(static_cast<long long>(gridDim.x), max(most, 1ll)));
     s.lo = s.c < s.blocks ? cut_at(s, s.c) : 0;
     s.hi = s.c < s.blocks ? cut_at(s, s.c + 1) : 0;
   }
-  const int shares = share_count<CUT>(s);
+  const int shares = share_count(s);
 
   if (warp == 0) {
     // ---------------------------------------------------------------- copies
     int it = 0;
     bool ok = true;
     for (int i = 0; ok && i < shares; ++i) {
-      const Share h = share_at<CUT>(s, i);
+      const Share h = share_at(s, i);
       const Unit q = unit_at<TT>(s, h.u);
-      // gathered: this lane's groups of four rows; rows past the tile's end
-      // repeat its last one, indexes are clamped into A
+      const long long wt = static_cast<long long>(q.e) * s.NT + q.nt;  // weight tile of the stacked image
+      // rows that are copied; the accumulator's columns past them hold what
+      // the rows of an earlier step left and are not stored
+      const int copied = GATHER ? (q.count + 3) & ~3 : q.n16;
+      const uint32_t bytes = (MODE == kMXFP4FP8A ? kSlabBytes / 2 : kSlabBytes) + copied * 128 + C::SFW_BYTES +
+                             (C::SCALE_WARPS ? 0 : C::SFT_BYTES);
+      // the weight's part of a stage (one lane)
+      auto weights = [&](int kb, int slot) {
+        uint8_t* st = smem + slot * C::STAGE_BYTES;
+        mbar_arrive_expect_tx(&full_bar[slot], bytes);
+        const long long slab = wt * s.KB + kb;
+        if (MODE == kMXFP4FP8A)
+          tma_load_3d(st, &tmap_b, 0, 0, static_cast<int32_t>(slab), &full_bar[slot]);
+        else
+          bulk_g2s(st, p.b_img + slab * kSlabBytes, kSlabBytes, &full_bar[slot]);
+        if (C::APS) {
+          const long long atom = MODE == kMXFP8 ? wt * ((s.KB + 3) / 4) + kb / 4 : slab * C::APS;
+          bulk_g2s(st + kSlabBytes + C::TOK_BYTES, p.b_sf + atom * 512, C::SFW_BYTES, &full_bar[slot]);
+        }
+      };
+      // gathered: this lane's four rows; rows past the tile's end repeat its
+      // last one, indexes are clamped into A
       int idx[4];
       if (GATHER) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          idx[j] = min(max(__ldg(p.rows + q.row0 + min(lane * 4 + j, q.count - 1)), 0), p.T - 1);
+        for (int j = 0; j < 4; ++j) idx[j] = __ldg(p.rows + q.row0 + min(lane * 4 + j, q.count - 1));
       }
-      const long long wt = static_cast<long long>(q.e) * s.NT + q.nt;  // weight tile of the stacked image
+      // the first stages are empty: their weights go out while the row indexes come
+      const int early = GATHER && i == 0 ? min(ST, h.k1 - h.k0) : 0;
+      if (early > 0) {
+        if (elect_one()) {
+          for (int j = 0; j < early; ++j) weights(h.k0 + j, j);
+        }
+        __syncwarp();
+      }
+      if (GATHER) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) idx[j] = min(max(idx[j], 0), p.T - 1);
+      }
       for (int kb = h.k0; kb < h.k1; ++kb, ++it) {
         const int slot = it % ST;
         ok = __all_sync(0xffffffffu, mbar_wait(&empty_bar[slot], ((it / ST) & 1) ^ 1u, T, p.err, 61));
         if (!ok) break;
         uint8_t* st = smem + slot * C::STAGE_BYTES;
         uint8_t* tok = st + kSlabBytes;
-        // rows that are copied; the accumulator's columns past them hold what
-        // the rows of an earlier step left and are not stored
-        const int copied = GATHER ? (q.count + 3) & ~3 : q.n16;
         if (elect_one()) {
-          mbar_arrive_expect_tx(&full_bar[slot],
-                                (MODE == kMXFP4FP8A ? kSlabBytes / 2 : kSlabBytes) + copied * 128 + C::SFW_BYTES +
-                                    (C::SCALE_WARPS ? 0 : C::SFT_BYTES));
-          const long long slab = wt * s.KB + kb;
-          if (MODE == kMXFP4FP8A)
-            tma_load_3d(st, &tmap_b, 0, 0, static_cast<int32_t>(slab), &full_bar[slot]);
-          else
-            bulk_g2s(st, p.b_img + slab * kSlabBytes, kSlabBytes, &full_bar[slot]);
+          if (it >= early) weights(kb, slot);
           if (!GATHER) {
             int m = 0;
             if (TT == 256 && q.n16 == 256) {
@@ -335,15 +373,11 @@ __global__ void __launch_bounds__(GCfg<MODE, TT>::THREADS, GCfg<MODE, TT>::BLOCK
               }
             }
           }
-          if (C::APS) {
-            const long long atom = MODE == kMXFP8 ? wt * ((s.KB + 3) / 4) + kb / 4 : slab * C::APS;
-            bulk_g2s(st + kSlabBytes + C::TOK_BYTES, p.b_sf + atom * 512, C::SFW_BYTES, &full_bar[slot]);
-            if (!C::SCALE_WARPS) {
-              const long long step = MODE == kMXFP8 ? static_cast<long long>(q.tile) * ((s.KB + 3) / 4) + kb / 4
-                                                    : static_cast<long long>(q.tile) * s.KB + kb;
-              bulk_g2s(st + kSlabBytes + C::TOK_BYTES + C::SFW_BYTES, p.a_sf + step * C::SFT_BYTES, C::SFT_BYTES,
-                       &full_bar[slot]);
-            }
+          if (C::APS && !C::SCALE_WARPS) {
+            const long long step = MODE == kMXFP8 ? static_cast<long long>(q.tile) * ((s.KB + 3) / 4) + kb / 4
+                                                  : static_cast<long long>(q.tile) * s.KB + kb;
+            bulk_g2s(st + kSlabBytes + C::TOK_BYTES + C::SFW_BYTES, p.a_sf + step * C::SFT_BYTES, C::SFT_BYTES,
+                     &full_bar[slot]);
           }
         }
         __syncwarp();
@@ -362,7 +396,7 @@ __global__ void __launch_bounds__(GCfg<MODE, TT>::THREADS, GCfg<MODE, TT>::BLOCK
     if (p.debug_stall) ok = __all_sync(0xffffffffu, mbar_wait(&stall_bar, 0, T, p.err, 62));
     int it = 0;
     for (int i = 0; ok && i < shares; ++i) {
-      const Share h = share_at<CUT>(s, i);
+      const Share h = share_at(s, i);
       const Unit q = unit_at<TT>(s, h.u);
       const int acc = i % C::ACCS;
       ok = __all_sync(0xffffffffu, mbar_wait(&acce_bar[acc], ((i / C::ACCS) & 1) ^ 1u, T, p.err, 63));
@@ -424,7 +458,7 @@ __global__ void __launch_bounds__(GCfg<MODE, TT>::THREADS, GCfg<MODE, TT>::BLOCK
       int it = 0;
       bool ok = true;
       for (int i = 0; ok && i < shares; ++i) {
-        const Share h = share_at<CUT>(s, i);
+        const Share h = share_at(s, i);
         const Unit q = unit_at<TT>(s, h.u);
         const uint8_t* src[PT];
 #pragma unroll
@@ -485,7 +519,7 @@ __global__ void __launch_bounds__(GCfg<MODE, TT>::THREADS, GCfg<MODE, TT>::BLOCK
     const float scale = MODE == kTensor ? __ldg(static_cast<const float*>(p.a_scales)) * __ldg(p.b_s) : 1.f;
     bool ok = true;
     for (int i = 0; i < shares; ++i) {
-      const Share h = share_at<CUT>(s, i);
+      const Share h = share_at(s, i);
       const Unit q = unit_at<TT>(s, h.u);
       const int acc = i % C::ACCS;
       // a warp that gave up waits for nothing more, but still meets the others
@@ -495,7 +529,7 @@ __global__ void __launch_bounds__(GCfg<MODE, TT>::THREADS, GCfg<MODE, TT>::BLOCK
         ok = __all_sync(0xffffffffu, w);
         if (!ok && lane == 0) abort_sh = 1;
       }
-      const bool shared_unit = CUT && (h.k0 > 0 || h.k1 < s.KB);
+      const bool shared_unit = CUT && (h.k0 > 0 || h.k1 < s.KB);  // of a cut line
       if (!ok) {
         if (shared_unit) {
           bar_sync_named(1, 32 * C::EPI_WARPS);
@@ -525,14 +559,16 @@ __global__ void __launch_bounds__(GCfg<MODE, TT>::THREADS, GCfg<MODE, TT>::BLOCK
 #pragma unroll
         for (int m = 0; m < COLS; ++m)
           if (m < q.count) __stcg(mine + m * 128 + n, __uint_as_float(v[m]));
-        __threadfence();
         bar_sync_named(1, 32 * C::EPI_WARPS);
         if (threadIdx.x == 128) last_sh = 0;
         if (threadIdx.x == 128 && *reinterpret_cast<volatile int*>(&abort_sh) == 0) {
-          // tickets hold the call's tag and the arrivals; a word of another
-          // call (or of nothing) counts as none
+          // Tickets hold the call's tag and the arrivals; a word of another
+          // call (or of nothing) counts as none.  The barrier above put the
+          // block's partial before this thread, its fence puts it before the
+          // arrival.  First guess: the word is clear, as a finished unit leaves it.
+          __threadfence();
           unsigned long long* t = p.tickets + c0;
-          unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(t), seen;
+          unsigned long long old = 0ull, seen;
           int arrived;
           do {
             seen = old;
@@ -663,12 +699,12 @@ cudaError_t launch_one(const AMaps& a_maps, const CUtensorMap& tmap_b, const Gro
                        cudaStream_t stream) {
   using C = GCfg<MODE, TT>;
   auto* kernel = &grouped_kernel<MODE, TT, GATHER>;
-  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), C::SMEM);
+  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), C::smem(kMaxExperts));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(blocks);
   cfg.blockDim = dim3(C::THREADS);
-  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.dynamicSmemBytes = C::smem(p.E);
   cfg.stream = stream;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -6,8 +6,12 @@
 // the stable order of all (token, choice) pairs by expert: pair i = t * top_k +
 // j goes to slot offsets[e] + (pairs before i with the same expert e).  A warp
 // finds a token's choices in registers: logits as unsigned keys in the same
-// order, top_k times the largest key (one warp reduction) and the lowest
-// expert that has it (another).
+// order with the expert's complement below them, so that one comparison also
+// breaks ties.  Each lane sorts its own few keys once (Batcher's odd-even
+// merge; up to 256 experts); then top_k times the warp takes the largest head
+// (one reduction for 16-bit logits, two for 32-bit ones) and its lane moves up.  Against scanning
+// the lane's keys anew for each choice this took 16383 x 256 from 29 us to the
+// figure below; it is bound by instructions, not by the 8 MB it reads.
 //
 // The stable order needs no sort, because a token picks an expert at most
 // once: for 64 tokens at a time shared memory holds a 64-bit mask per expert,
@@ -38,105 +42,214 @@ struct RouteParams {
   int32_t* offsets;   // [E + 1]
   int32_t* rows;      // [T * k]
   int32_t* slots;     // [T][k]
-  uint32_t* counts;   // [blocks][E], more than one block only
+  uint32_t* counts;   // [blocks][E rounded up to 4], more than one block only
   int64_t T, ldl;
   int E, k, renormalize;
+  int whole;  // rows of logits are aligned to a lane's chunk
 };
 
-__device__ __forceinline__ float ld_logit(const float* p) { return __ldcs(p); }
-__device__ __forceinline__ float ld_logit(const __nv_bfloat16* p) {
-  const unsigned short u = __ldcs(reinterpret_cast<const unsigned short*>(p));
-  return __uint_as_float(static_cast<uint32_t>(u) << 16);
-}
+// Sortable form of a logit and its expert: the larger comes first, among equal
+// logits the lower expert; 0 for -infinity and NaN, which are never picked.
+// Both zeros have one key.
+template <typename T>
+struct Key;
 
-// Unsigned key in the order of the floats, both zeros alike; 0 for -infinity
-// and NaN.
-__device__ __forceinline__ uint32_t key_of(float l) {
-  if (!(l > -INFINITY)) return 0u;
-  const uint32_t u = __float_as_uint(l + 0.f);  // -0 becomes +0
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-__device__ __forceinline__ float logit_of(uint32_t key) {
-  return __uint_as_float((key & 0x80000000u) ? (key & 0x7fffffffu) : ~key);
-}
+template <>
+struct Key<float> {
+  using Word = unsigned long long;  // key, complement of the expert
+  static __device__ __forceinline__ Word make(uint32_t bits, int e) {
+    const float l = __uint_as_float(bits);
+    if (!(l > -INFINITY)) return 0ull;
+    const uint32_t u = __float_as_uint(l + 0.f);  // -0 becomes +0
+    const uint32_t k = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+    return (static_cast<Word>(k) << 32) | static_cast<uint32_t>(~e);
+  }
+  static __device__ __forceinline__ Word largest(Word w) {
+    const uint32_t hi = static_cast<uint32_t>(w >> 32);
+    const uint32_t m = __reduce_max_sync(0xffffffffu, hi);
+    const uint32_t lo = __reduce_max_sync(0xffffffffu, hi == m ? static_cast<uint32_t>(w) : 0u);
+    return (static_cast<Word>(m) << 32) | lo;
+  }
+  static __device__ __forceinline__ int expert(Word w) { return ~static_cast<int>(w); }
+  static __device__ __forceinline__ float logit(Word w) {
+    const uint32_t k = static_cast<uint32_t>(w >> 32);
+    return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
+  }
+};
+
+template <>
+struct Key<__nv_bfloat16> {
+  using Word = uint32_t;  // key in the upper half, complement of the expert in the lower
+  static __device__ __forceinline__ Word make(uint32_t bits, int e) {
+    const uint32_t u = bits == 0x8000u ? 0u : bits;
+    const uint32_t k = (u & 0x8000u) ? (u ^ 0xffffu) : (u | 0x8000u);
+    // 0x7f: -infinity, below it and above 0xff80 (infinity): NaN
+    return k > 0x7fu && k <= 0xff80u ? (k << 16) | (0xffffu - e) : 0u;
+  }
+  static __device__ __forceinline__ Word largest(Word w) { return __reduce_max_sync(0xffffffffu, w); }
+  static __device__ __forceinline__ int expert(Word w) { return 0xffff - static_cast<int>(w & 0xffffu); }
+  static __device__ __forceinline__ float logit(Word w) {
+    const uint32_t k = w >> 16;
+    return __uint_as_float(((k & 0x8000u) ? (k & 0x7fffu) : (k ^ 0xffffu)) << 16);
+  }
+};
+
 // exp(l - top), 1 where both are infinite
 __device__ __forceinline__ float exp_below(float l, float top) { return l == top ? 1.f : expf(l - top); }
 
+// Batcher's odd-even merge sort, largest first, all indexes known at compile time.
+template <int N, typename W>
+__device__ __forceinline__ void sort_down(W (&a)[N]) {
+#pragma unroll
+  for (int p = 1; p < N; p *= 2) {
+#pragma unroll
+    for (int k = p; k >= 1; k /= 2) {
+#pragma unroll
+      for (int j = k % p; j + k < N; j += 2 * k) {
+#pragma unroll
+        for (int i = 0; i < k; ++i) {
+          if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+            const W x = a[i + j], y = a[i + j + k];
+            a[i + j] = x > y ? x : y;
+            a[i + j + k] = x > y ? y : x;
+          }
+        }
+      }
+    }
+  }
+}
+
+// A lane's logits of one token: chunks of V consecutive experts, 32 chunks (one
+// a lane) next to one another.
+template <typename T, int VPL>
+struct Logits {
+  static constexpr int V = VPL * sizeof(T) < 16 ? VPL : 16 / sizeof(T);
+  uint32_t bits[VPL];
+
+  static __device__ __forceinline__ int expert(int i, int lane) { return ((i / V) * 32 + lane) * V + i % V; }
+
+  __device__ __forceinline__ void load(const RouteParams& p, int64_t t, int lane) {
+    const T* row = static_cast<const T*>(p.logits) + t * p.ldl;
+    constexpr uint32_t NONE = sizeof(T) == 2 ? 0xff80u : 0xff800000u;  // -infinity
+#pragma unroll
+    for (int c = 0; c < VPL; c += V) {
+      const int e = expert(c, lane);
+      constexpr int BYTES = V * sizeof(T);
+      uint32_t w[(BYTES + 3) / 4];
+      if (p.whole && e + V <= p.E) {
+        if constexpr (BYTES == 16) {
+          const uint4 u = __ldcs(reinterpret_cast<const uint4*>(row + e));
+          w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+        } else if constexpr (BYTES == 8) {
+          const uint2 u = __ldcs(reinterpret_cast<const uint2*>(row + e));
+          w[0] = u.x; w[1] = u.y;
+        } else if constexpr (BYTES == 4) {
+          w[0] = __ldcs(reinterpret_cast<const uint32_t*>(row + e));
+        } else {
+          w[0] = __ldcs(reinterpret_cast<const unsigned short*>(row + e));
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          bits[c + i] = sizeof(T) == 4 ? w[i] : ((w[i / 2] >> (16 * (i % 2))) & 0xffffu);
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          bits[c + i] = NONE;
+          if (e + i < p.E)
+            bits[c + i] = sizeof(T) == 4 ? __ldcs(reinterpret_cast<const uint32_t*>(row) + e + i)
+                                         : __ldcs(reinterpret_cast<const unsigned short*>(row) + e + i);
+        }
+      }
+    }
+  }
+};
+
 // The choices of one token: lane j < k gets expert (-1: none left) and weight.
 template <typename T, int VPL>
-__device__ __forceinline__ void pick(const RouteParams& p, int64_t t, int lane, int& expert, float& weight) {
-  const T* row = static_cast<const T*>(p.logits) + t * p.ldl;
-  uint32_t key[VPL];
+__device__ __forceinline__ void pick(const RouteParams& p, const Logits<T, VPL>& l, int lane, int& expert, float& weight) {
+  using K = Key<T>;
+  typename K::Word key[VPL];
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int e = i * 32 + lane;
-    key[i] = e < p.E ? key_of(ld_logit(row + e)) : 0u;
-  }
-  // this lane's largest key and its first place
-  uint32_t best = 0u;
-  int at = 0;
-  auto rescan = [&] {
-    best = 0u;
-    at = 0;
+  for (int i = 0; i < VPL; ++i) key[i] = K::make(l.bits[i], Logits<T, VPL>::expert(i, lane));
+  // the lane's largest key: first of the sorted ones; with more than eight the
+  // network outgrows the registers, and the lane that gave one looks again
+  constexpr bool SORTED = VPL <= 8;
+  typename K::Word head = 0;
+  auto look = [&] {
+    head = key[0];
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (key[i] > best) {
-        best = key[i];
-        at = i;
-      }
+    for (int i = 1; i < VPL; ++i) head = key[i] > head ? key[i] : head;
   };
-  rescan();
-  float top = 0.f, sum = 0.f;
-  expert = -1;
-  weight = 0.f;
+  if constexpr (SORTED) {
+    sort_down(key);
+    head = key[0];
+  } else {
+    look();
+  }
+  typename K::Word mine = 0, first = 0;
+  float sum = 0.f;
   for (int j = 0; j < p.k; ++j) {
-    const uint32_t m = __reduce_max_sync(0xffffffffu, best);
-    if (m == 0u) break;  // no finite logit is left
-    const int e = static_cast<int>(__reduce_min_sync(0xffffffffu, best == m ? static_cast<uint32_t>(at * 32 + lane) : ~0u));
-    const float l = logit_of(m);
+    const typename K::Word m = K::largest(head);
+    if (m == 0) break;  // no logit is left
     if (j == 0) {
-      top = l;
-      if (!p.renormalize) {
-        // over all experts, before any key is taken away
+      first = m;
+      if (!p.renormalize) {  // over all experts, before any key is taken away
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) sum += key[i] ? exp_below(logit_of(key[i]), top) : 0.f;
+        for (int i = 0; i < VPL; ++i) sum += key[i] ? exp_below(K::logit(key[i]), K::logit(m)) : 0.f;
 #pragma unroll
         for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
       }
     }
-    const float w = exp_below(l, top);
-    if (p.renormalize) sum += w;
-    if (lane == j) {
-      expert = e;
-      weight = w;
-    }
-    if (lane == (e & 31)) {
+    if (lane == j) mine = m;
+    if (head == m) {  // one lane: experts differ
+      if constexpr (SORTED) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (i == at) key[i] = 0u;
-      rescan();
+        for (int i = 0; i + 1 < VPL; ++i) key[i] = key[i + 1];
+        key[VPL - 1] = 0;
+        head = key[0];
+      } else {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) key[i] = key[i] == m ? 0 : key[i];
+        look();
+      }
     }
   }
-  if (expert >= 0) weight = weight / sum;
+  expert = mine ? K::expert(mine) : -1;
+  weight = mine ? exp_below(K::logit(mine), K::logit(first)) : 0.f;
+  if (p.renormalize) {
+    sum = weight;
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  }
+  if (mine) weight = weight / sum;
 }
 
-// Exclusive sum of counts[0..E) into base[0..E], by the first warp.
+// Exclusive sum of counts[0..E) into base[0..E], by the whole block; ends with
+// the block in step.
 __device__ __forceinline__ void scan_experts(const uint32_t* counts, uint32_t* base, int E) {
-  if (threadIdx.x >= 32) return;
-  const int lane = threadIdx.x;
-  uint32_t carry = 0;
-  for (int e0 = 0; e0 < E; e0 += 32) {
-    const uint32_t c = e0 + lane < E ? counts[e0 + lane] : 0u;
-    uint32_t s = c;
+  __shared__ uint32_t part[kMaxExperts / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int chunks = (E + 31) / 32;
+  for (int c = warp; c < chunks; c += warps) {
+    const int e = c * 32 + lane;
+    const uint32_t n = e < E ? counts[e] : 0u;
+    uint32_t sum = n;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
-      const uint32_t o = __shfl_up_sync(0xffffffffu, s, d);
-      if (lane >= d) s += o;
+      const uint32_t o = __shfl_up_sync(0xffffffffu, sum, d);
+      if (lane >= d) sum += o;
     }
-    if (e0 + lane < E) base[e0 + lane] = carry + s - c;
-    carry += __shfl_sync(0xffffffffu, s, 31);
+    if (e < E) base[e] = sum - n;
+    if (lane == 31) part[c] = sum;
   }
-  if (lane == 0) base[E] = carry;
+  __syncthreads();
+  for (int c = warp; c < chunks; c += warps) {
+    const int e = c * 32 + lane;
+    const uint32_t below = __reduce_add_sync(0xffffffffu, lane < c ? part[lane] : 0u);
+    if (e < E) base[e] += below;
+    if (c == chunks - 1 && lane == 0) base[E] = below + part[c];
+  }
+  __syncthreads();
 }
 
 // Pairs [i0, i1): slot = base of the expert + rank, which slots[] holds so far.
@@ -154,64 +267,84 @@ __device__ __forceinline__ void scatter_pairs(const RouteParams& p, const uint32
 __device__ __forceinline__ int64_t cut(int64_t T, int b, int blocks) { return T * b / blocks; }
 
 // First kernel: choices, weights, ranks, and the block's counts.  Alone (one
-// block) it also scans and scatters.
+// block) it also scans and scatters.  Blocks of 1024 threads have 64 registers
+// each; where a lane sorts more than eight keys they are 512 threads wide.
+constexpr int route_threads(int vpl) { return vpl <= 8 ? 1024 : 512; }
+
 template <typename T, int VPL>
-__global__ void __launch_bounds__(1024) route_kernel(const RouteParams p) {
+__global__ void __launch_bounds__(route_threads(VPL)) route_kernel(const RouteParams p) {
+  // tokens of a group that a warp takes: the launch has a warp for each token
+  // or route_threads / 32
+  constexpr int TPW = kGroup * 32 / route_threads(VPL);
   __shared__ uint32_t mask[kGroup / 32][kMaxExperts];
   __shared__ uint32_t count[kMaxExperts];
   __shared__ uint32_t base[kMaxExperts + 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int64_t first = cut(p.T, blockIdx.x, gridDim.x), last = cut(p.T, blockIdx.x + 1, gridDim.x);
-  for (int e = threadIdx.x; e < p.E; e += blockDim.x) count[e] = 0u;
+  for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
+    count[e] = 0u;
+#pragma unroll
+    for (int w = 0; w < kGroup / 32; ++w) mask[w][e] = 0u;
+  }
   pdl_wait();
   pdl_launch_dependents();
   for (int64_t t0 = first; t0 < last; t0 += kGroup) {
-    for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
-#pragma unroll
-      for (int w = 0; w < kGroup / 32; ++w) mask[w][e] = 0u;
-    }
-    __syncthreads();
     const int n = static_cast<int>(min(static_cast<int64_t>(kGroup), last - t0));
-    for (int i = warp; i < n; i += warps) {
-      int e;
-      float w;
-      pick<T, VPL>(p, t0 + i, lane, e, w);
-      if (lane < p.k) {
-        p.experts[(t0 + i) * p.k + lane] = e;
-        p.weights[(t0 + i) * p.k + lane] = w;
-        if (e >= 0) atomicOr(&mask[i >> 5][e], 1u << (i & 31));
-      }
-    }
+    Logits<T, VPL> next;
+    if (warp < n) next.load(p, t0 + warp, lane);
     __syncthreads();
-    for (int i = threadIdx.x; i < n * p.k; i += blockDim.x) {
-      const int e = p.experts[t0 * p.k + i];  // written by this block, before the barrier
-      const int t = i / p.k;
-      int32_t rank = -1;
-      if (e >= 0) {
-        rank = static_cast<int32_t>(count[e]);
+    int expert[TPW];
 #pragma unroll
-        for (int w = 0; w < kGroup / 32; ++w) {
-          const int below = t - 32 * w;  // tokens of this word before t
-          const uint32_t m = below >= 32 ? ~0u : (below <= 0 ? 0u : (1u << below) - 1u);
-          rank += __popc(mask[w][e] & m);
+    for (int h = 0; h < TPW; ++h) {
+      const int i = warp + h * warps;
+      expert[h] = -1;
+      if (i < n) {
+        const Logits<T, VPL> now = next;
+        if (h + 1 < TPW && i + warps < n) next.load(p, t0 + i + warps, lane);  // on its way during this token's work
+        float w;
+        pick<T, VPL>(p, now, lane, expert[h], w);
+        if (lane < p.k) {
+          p.experts[(t0 + i) * p.k + lane] = expert[h];
+          p.weights[(t0 + i) * p.k + lane] = w;
+          if (expert[h] >= 0) atomicOr(&mask[i >> 5][expert[h]], 1u << (i & 31));
         }
       }
-      p.slots[t0 * p.k + i] = rank;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < TPW; ++h) {
+      const int i = warp + h * warps;
+      if (i < n && lane < p.k) {
+        const int e = expert[h];
+        int32_t rank = -1;
+        if (e >= 0) {
+          rank = static_cast<int32_t>(count[e]);
+#pragma unroll
+          for (int w = 0; w < kGroup / 32; ++w) {
+            const int below = i - 32 * w;  // tokens of this word before i
+            const uint32_t m = below >= 32 ? ~0u : (below <= 0 ? 0u : (1u << below) - 1u);
+            rank += __popc(mask[w][e] & m);
+          }
+        }
+        p.slots[(t0 + i) * p.k + lane] = rank;
+      }
     }
     __syncthreads();
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
 #pragma unroll
-      for (int w = 0; w < kGroup / 32; ++w) count[e] += __popc(mask[w][e]);
+      for (int w = 0; w < kGroup / 32; ++w) {
+        count[e] += __popc(mask[w][e]);
+        mask[w][e] = 0u;
+      }
     }
   }
   __syncthreads();
   if (gridDim.x > 1) {
     for (int e = threadIdx.x; e < p.E; e += blockDim.x)
-      p.counts[static_cast<size_t>(blockIdx.x) * p.E + e] = count[e];
+      p.counts[static_cast<size_t>(blockIdx.x) * ((p.E + 3) & ~3) + e] = count[e];
     return;
   }
   scan_experts(count, base, p.E);
-  __syncthreads();
   scatter_pairs(p, base, 0, p.T * p.k);
   for (int e = threadIdx.x; e <= p.E; e += blockDim.x) p.offsets[e] = static_cast<int32_t>(base[e]);
   for (int64_t i = base[p.E] + threadIdx.x; i < p.T * p.k; i += blockDim.x) p.rows[i] = -1;
@@ -229,23 +362,43 @@ __global__ void __launch_bounds__(1024) route_scatter_kernel(const RouteParams p
     before[e] = 0u;
   }
   __syncthreads();
-  // threads in groups of E (rounded up to warps) share the blocks' counts
-  const int width = (p.E + 31) / 32 * 32;
-  const int groups = max(1, static_cast<int>(blockDim.x) / width);
-  const int g = threadIdx.x / width;
-  for (int e = threadIdx.x - g * width; e < p.E && g < groups; e += blockDim.x) {
-    uint32_t all = 0, mine = 0;
-    for (int b = g; b < static_cast<int>(gridDim.x); b += groups) {
-      const uint32_t c = p.counts[static_cast<size_t>(b) * p.E + e];
-      all += c;
-      if (b < static_cast<int>(blockIdx.x)) mine += c;
+  // every block reads all counts, four experts a thread, the blocks' rows
+  // shared out over the threads
+  const int quads = (p.E + 3) / 4;
+  const int groups = static_cast<int>(blockDim.x) / quads;  // E <= 1024: at least 4
+  const int g = threadIdx.x / quads, e4 = (threadIdx.x - g * quads) * 4;
+  if (g < groups) {
+    uint32_t all[4] = {}, mine[4] = {};
+    const uint4* row = reinterpret_cast<const uint4*>(p.counts) + e4 / 4;
+    const int blocks = gridDim.x;
+    for (int b0 = g; b0 < blocks; b0 += 4 * groups) {
+      uint4 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int b = b0 + i * groups;
+        v[i] = b < blocks ? __ldcg(row + static_cast<size_t>(b) * quads) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t c[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        const bool before_me = b0 + i * groups < static_cast<int>(blockIdx.x);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          all[j] += c[j];
+          mine[j] += before_me ? c[j] : 0u;
+        }
+      }
     }
-    atomicAdd(&total[e], all);
-    atomicAdd(&before[e], mine);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (e4 + j < p.E) {  // (the row's padding is not counted)
+        atomicAdd(&total[e4 + j], all[j]);
+        atomicAdd(&before[e4 + j], mine[j]);
+      }
+    }
   }
   __syncthreads();
   scan_experts(total, base, p.E);
-  __syncthreads();
   if (blockIdx.x == 0) {
     for (int e = threadIdx.x; e <= p.E; e += blockDim.x) p.offsets[e] = static_cast<int32_t>(base[e]);
   }
@@ -274,21 +427,25 @@ cudaError_t launch_route(const RouteParams& p, cudaStream_t st) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-  // a warp per token, and threads enough for the experts' loops
-  const int64_t warps = p.T < 8 ? 8 : (p.T < 32 ? p.T : 32);
-  cfg.blockDim = dim3(static_cast<unsigned>(32 * warps));
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = pdl_enabled() ? 1 : 0;
+  auto launch = [&](auto kernel, int most) {
+    // a warp per token, and threads enough for the experts' loops
+    const int64_t warps = p.T < 8 ? 8 : (p.T < most / 32 ? p.T : most / 32);
+    cfg.blockDim = dim3(static_cast<unsigned>(32 * warps));
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+  };
   const int vpl = (p.E + 31) / 32;
   cudaError_t e;
-  if (vpl <= 1) e = cudaLaunchKernelEx(&cfg, route_kernel<T, 1>, p);
-  else if (vpl <= 2) e = cudaLaunchKernelEx(&cfg, route_kernel<T, 2>, p);
-  else if (vpl <= 4) e = cudaLaunchKernelEx(&cfg, route_kernel<T, 4>, p);
-  else if (vpl <= 8) e = cudaLaunchKernelEx(&cfg, route_kernel<T, 8>, p);
-  else if (vpl <= 16) e = cudaLaunchKernelEx(&cfg, route_kernel<T, 16>, p);
-  else e = cudaLaunchKernelEx(&cfg, route_kernel<T, 32>, p);
+  if (vpl <= 1) e = launch(route_kernel<T, 1>, route_threads(1));
+  else if (vpl <= 2) e = launch(route_kernel<T, 2>, route_threads(2));
+  else if (vpl <= 4) e = launch(route_kernel<T, 4>, route_threads(4));
+  else if (vpl <= 8) e = launch(route_kernel<T, 8>, route_threads(8));
+  else if (vpl <= 16) e = launch(route_kernel<T, 16>, route_threads(16));
+  else e = launch(route_kernel<T, 32>, route_threads(32));
   if (e != cudaSuccess || blocks == 1) return e;
+  cfg.blockDim = dim3(1024);
   return cudaLaunchKernelEx(&cfg, route_scatter_kernel, p);
 }
 
@@ -360,7 +517,7 @@ fg_status fg_moe_route_workspace_size(int64_t T, int E, uint64_t* bytes) {
   if (T < 0 || E < 1 || E > kMaxExperts)
     return fail(FG_ERR_SHAPE, "fg_moe_route: T=%lld, E=%d (1..%d experts)", (long long)T, E, kMaxExperts);
   const int blocks = route_blocks(T);
-  *bytes = blocks > 1 ? static_cast<uint64_t>(blocks) * E * 4 : 0;
+  *bytes = blocks > 1 ? static_cast<uint64_t>(blocks) * ((E + 3) / 4 * 4) * 4 : 0;
   return FG_OK;
 }
 
@@ -380,14 +537,21 @@ fg_status fg_moe_route(const void* logits, int type, int64_t T, int E, int64_t l
   if (!offsets || (T > 0 && (!logits || !weights || !experts || !rows || !slots)))
     return fail(FG_ERR_INVALID_ARG, "%s: null pointer", what);
   if (!aligned(logits, type == FG_TYPE_F32 ? 4 : 2) || !aligned(weights, 4) || !aligned(experts, 4) ||
-      !aligned(offsets, 4) || !aligned(rows, 4) || !aligned(slots, 4) || !aligned(workspace, 4))
+      !aligned(offsets, 4) || !aligned(rows, 4) || !aligned(slots, 4))
     return fail(FG_ERR_ALIGN, "%s: a pointer is not aligned to its type", what);
+  if (need && !aligned(workspace, 16)) return fail(FG_ERR_ALIGN, "%s: workspace must be 16-byte aligned", what);
   if (need && (!workspace || workspace_bytes < need))
     return fail(FG_ERR_WORKSPACE, "%s: T=%lld, E=%d need a %llu-byte workspace", what, (long long)T, E,
                 (unsigned long long)need);
   if ((s = check_arch()) != FG_OK) return s;
   RouteParams p{logits, weights, experts, offsets, rows, slots, static_cast<uint32_t*>(workspace),
-                T, ldl, E, top_k, (flags & FG_FLAG_RENORMALIZE) ? 1 : 0};
+                T, ldl, E, top_k, (flags & FG_FLAG_RENORMALIZE) ? 1 : 0, 0};
+  // a lane's chunk: at most 16 bytes, and no more than its share of the experts
+  const int es = type == FG_TYPE_F32 ? 4 : 2;
+  int vpl = 1;
+  while (vpl < (E + 31) / 32) vpl *= 2;
+  const int chunk = vpl * es < 16 ? vpl * es : 16;
+  p.whole = aligned(logits, chunk) && (T <= 1 || ldl * es % chunk == 0) ? 1 : 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = type == FG_TYPE_F32 ? launch_route<float>(p, st) : launch_route<__nv_bfloat16>(p, st);
   return e == cudaSuccess ? FG_OK : cuda_fail(e, "routing launch");
