@@ -33,22 +33,39 @@ constexpr int kVec = 8;  // consecutive values per thread
 
 // ------------------------------------------------------------ loads, codes
 
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[kVec]) {
-  const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p));
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// Eight values as they lie in memory: loads are issued together and widened
+// when they are used.  once: not read again, so kept out of the caches' way.
+template <typename T>
+struct Raw8 {
+  uint4 q[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) q[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
   }
-}
-
-__device__ __forceinline__ void load8(const float* p, float (&v)[kVec]) {
-  const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
-  const float4 b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
+  __device__ __forceinline__ void load_once(const T* p) {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) q[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) q[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void widen(float (&v)[kVec]) const {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) {
+      const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (sizeof(T) == 2) {
+          v[2 * j] = __uint_as_float(w[j] << 16);
+          v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+        } else {
+          v[4 * i + j] = __uint_as_float(w[j]);
+        }
+      }
+    }
+  }
+};
 
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[kVec]) {
   uint32_t w[4];
@@ -135,29 +152,42 @@ __device__ __forceinline__ void quantize8(float (&v)[kVec], bool live, size_t ch
 // 2^-4 steps of the codes); a product below about 2^-120 becomes zero.
 __device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.f + __expf(-g)) * u; }
 
-// Threads (x, y) of a block take eight values of row blockIdx.x * blockDim.y +
-// y: no division, and a warp's lanes never split a scale block.
-template <int MODE, int ACT, typename T>
+// Threads (x, y) of a block take eight values of each of ROWS rows, blockDim.y
+// apart: no division, and a warp's lanes never split a scale block.  With many
+// rows a thread takes four, so that 128 bytes of it are in flight.
+template <int MODE, int ACT, int ROWS, typename T>
 __global__ void __launch_bounds__(256) quantize_kernel(const T* __restrict__ x, int64_t M, int64_t K, int64_t ldx,
                                                        void* __restrict__ codes, void* __restrict__ scales) {
   pdl_wait();
   pdl_launch_dependents();
   const int64_t cpr = K / kVec;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * (blockDim.y * ROWS) + threadIdx.y;
   const int64_t c = static_cast<int64_t>(blockIdx.y) * blockDim.x + threadIdx.x;
-  const bool live = row < M && c < cpr;
-  float v[kVec] = {};
-  if (live) {
-    const T* src = x + row * ldx + c * kVec;
-    load8(src, v);
-    if (ACT == FG_ACT_SWIGLU) {
-      float u[kVec];
-      load8(src + K, u);
+  Raw8<T> a[ROWS], b[ROWS];
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) v[i] = swiglu(v[i], u[i]);
+  for (int i = 0; i < ROWS; ++i) {
+    const int64_t row = row0 + i * blockDim.y;
+    a[i].zero();
+    b[i].zero();
+    if (row < M && c < cpr) {
+      const T* src = x + row * ldx + c * kVec;
+      a[i].load_once(src);
+      if (ACT == FG_ACT_SWIGLU) b[i].load_once(src + K);
     }
   }
-  quantize8<MODE>(v, live, static_cast<size_t>(row * cpr + c), codes, scales);
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    const int64_t row = row0 + i * blockDim.y;
+    float v[kVec];
+    a[i].widen(v);
+    if (ACT == FG_ACT_SWIGLU) {
+      float u[kVec];
+      b[i].widen(u);
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) v[j] = swiglu(v[j], u[j]);
+    }
+    quantize8<MODE>(v, row < M && c < cpr, static_cast<size_t>(row * cpr + c), codes, scales);
+  }
 }
 
 // -------------------------------------------------------- RMS norm, quantise
@@ -186,30 +216,39 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormParams p) {
   pdl_launch_dependents();
   const T* x = static_cast<const T*>(p.x) + row * p.ldx;
   const T* r = static_cast<const T*>(p.residual) + row * p.ldr;
+  const T* w = static_cast<const T*>(p.weight);
   float v[NC][kVec];
-  float ss = 0.f;
-#pragma unroll
-  for (int i = 0; i < NC; ++i) {
-    const int c = threadIdx.x + i * blockDim.x;
-    if (c < cpr) {
-      load8(x + c * kVec, v[i]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < kVec; ++j) v[i][j] = 0.f;
-    }
-  }
-  if (p.residual) {
+  Raw8<T> g[NC];  // the weight, on its way during the reduction
+  {
+    Raw8<T> a[NC], b[NC];
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int c = threadIdx.x + i * blockDim.x;
+      a[i].zero();
+      b[i].zero();
+      g[i].zero();
       if (c < cpr) {
-        float a[kVec];
-        load8(r + c * kVec, a);
+        a[i].load_once(x + c * kVec);
+        if (p.residual) b[i].load_once(r + c * kVec);
+      }
+    }
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) v[i][j] += a[j];
+    for (int i = 0; i < NC; ++i) {
+      const int c = threadIdx.x + i * blockDim.x;
+      if (c < cpr) g[i].load(w + c * kVec);
+    }
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      float u[kVec];
+      a[i].widen(v[i]);
+      b[i].widen(u);
+      if (p.residual) {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) v[i][j] += u[j];
       }
     }
   }
+  float ss = 0.f;
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
 #pragma unroll
@@ -231,16 +270,15 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormParams p) {
 #pragma unroll
   for (int d = 16; d > 0; d /= 2) ss += __shfl_xor_sync(0xffffffffu, ss, d);
   const float inv = rsqrtf(ss / static_cast<float>(p.K) + p.eps);
-  const T* w = static_cast<const T*>(p.weight);
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     const int c = threadIdx.x + i * blockDim.x;
     const bool live = c < cpr;
-    if (live) {
-      float g[kVec];
-      load8(w + c * kVec, g);
+    float u[kVec];
+    g[i].widen(u);
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) v[i][j] = v[i][j] * inv * g[j];
+    for (int j = 0; j < kVec; ++j) v[i][j] = v[i][j] * inv * u[j];
+    if (live) {
       if (p.y) store8(static_cast<T*>(p.y) + row * p.K + c * kVec, v[i]);
     }
     if constexpr (MODE != kBF16)
@@ -271,11 +309,16 @@ cudaError_t launch_quantize(const void* x, int64_t M, int64_t K, int64_t ldx, vo
   for (int b = 32; b <= 256; b *= 2)
     if ((cpr + b - 1) / b * b <= (cpr + 15) / 16 * 16) bx = b;
   const int by = 256 / bx;
+  const int64_t cols = (cpr + bx - 1) / bx;
+  // four rows a thread once that leaves eight blocks for every SM
+  const bool many = (M + 4 * by - 1) / (4 * by) * cols >= 8 * sm_count();
+  const int64_t rows = many ? 4 * by : by;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr;
-  pdl_config(cfg, attr, dim3(static_cast<unsigned>((M + by - 1) / by), static_cast<unsigned>((cpr + bx - 1) / bx)),
-             dim3(bx, by), st);
-  return cudaLaunchKernelEx(&cfg, quantize_kernel<MODE, ACT, T>, static_cast<const T*>(x), M, K, ldx, codes, scales);
+  pdl_config(cfg, attr, dim3(static_cast<unsigned>((M + rows - 1) / rows), static_cast<unsigned>(cols)), dim3(bx, by), st);
+  const T* src = static_cast<const T*>(x);
+  return many ? cudaLaunchKernelEx(&cfg, quantize_kernel<MODE, ACT, 4, T>, src, M, K, ldx, codes, scales)
+              : cudaLaunchKernelEx(&cfg, quantize_kernel<MODE, ACT, 1, T>, src, M, K, ldx, codes, scales);
 }
 
 template <int MODE, typename T>

@@ -7,6 +7,7 @@ Calls of a few microseconds: checks are plain comparisons, and the stream is
 read without making a Stream object.
 """
 import ctypes
+import functools
 from typing import NamedTuple
 
 import torch
@@ -142,6 +143,11 @@ def rmsnorm_quantize(mode, x, weight, residual=None, eps=1e-6, normed=False, str
     return codes, scales, h, y
 
 
+@functools.lru_cache(maxsize=4096)  # a call of its own costs as much as an allocation
+def _route_workspace(device_index, tokens, experts):
+    return moe_route_workspace_size(tokens, experts)
+
+
 def moe_route_workspace_size(tokens, experts):
     b = ctypes.c_uint64()
     _fg._check(_fg.lib().fg_moe_route_workspace_size(tokens, experts, ctypes.byref(b)))
@@ -161,13 +167,18 @@ def moe_route(logits, top_k, renormalize=True, stream=None):
     offsets = torch.empty(e + 1, dtype=torch.int32, device=device)
     rows = torch.empty(t * top_k, dtype=torch.int32, device=device)
     slots = torch.empty((t, top_k), dtype=torch.int32, device=device)
-    need = moe_route_workspace_size(t, e)
+    need = _route_workspace(device.index, t, e)
     ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None
     _fg._check(_fg.lib().fg_moe_route(logits.data_ptr(), _type(logits, "logits"), t, e, ld, top_k,
                                       FG_FLAG_RENORMALIZE if renormalize else 0, weights.data_ptr(), experts.data_ptr(),
                                       offsets.data_ptr(), rows.data_ptr(), slots.data_ptr(), _p(ws), need,
                                       _on(device, stream, weights, experts, offsets, rows, slots, ws)))
     return Routing(weights, experts, offsets, rows, slots)
+
+
+@functools.lru_cache(maxsize=4096)
+def _grouped_workspace(device_index, mode, rows, experts, n, k, gather):
+    return grouped_gemm_workspace_size(mode, rows, experts, n, k, gather)
 
 
 def grouped_gemm_workspace_size(mode, rows, experts, n, k, gather=False):
@@ -210,7 +221,7 @@ def grouped_gemm(A, pb, offsets, a_scales=None, rows=None, Y=None, workspace=Non
         _fg._require(Y, "Y", _fg._dtypes("bfloat16", "int16"), device, shape=(r, n))
     need = 0
     if workspace is None:
-        need = grouped_gemm_workspace_size(mode, r, e, n, k, rows is not None)
+        need = _grouped_workspace(device.index, mode, r, e, n, k, rows is not None)
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=device)
     else:
