@@ -16,7 +16,7 @@
 // it once.  No work is launched for experts without rows, and nothing comes
 // back to the host.
 //
-//  - TT = 256 (many rows an expert): units are dealt out whole.  Bound by the
+//  - TT = 128, 256 (many rows an expert): units are dealt out whole.  Bound by the
 //    tensor cores and the stream from L2.  A first kernel lays out what every
 //    weight tile reads again: the gathered rows one after the other (tensor
 //    copies of four indexed rows each took three times as long as the product
@@ -58,7 +58,7 @@ struct GroupedParams {
   const int32_t* offsets;     // [E + 1]
   const int32_t* rows;        // [R] or null
   __nv_bfloat16* y;           // [R][N]
-  const uint8_t* a_sf;        // TT = 256, MX: token scale atoms [tile][K step][atom][2][512]
+  const uint8_t* a_sf;        // TT >= 128, MX: token scale atoms [tile][K step][atom][128-row block][512]
   float* part;                // [blocks][2][TT][128] partials (cut line)
   unsigned long long* tickets;  // [blocks] arrivals at the unit that begins last in the block
   unsigned long long epoch;
@@ -74,7 +74,7 @@ struct GCfg {
   static constexpr bool CUT = TT == 32;           // the cut line of K steps
   // fp8 x fp4 moves half a stage's bytes from HBM: one stage more (28.5 -> 28.2 us
   // for one token, 103 -> 100 us for eight); the 8-bit modes lost 2-4 % with it
-  static constexpr int STAGES = TT == 32 && MODE == kMXFP4FP8A ? 5 : 4;
+  static constexpr int STAGES = TT == 128 ? 6 : (TT == 32 && MODE == kMXFP4FP8A ? 5 : 4);
   static constexpr int TOK_BYTES = TT * 128;
   static constexpr int TOK_ATOMS = (TT + 127) / 128;
   static constexpr int SFW_BYTES = APS * 512;
@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(GCfg<MODE, TT>::THREADS, GCfg<MODE, TT>::BLOCK
               m = 128;
             }
 #pragma unroll
-            for (int b = TT == 256 ? 3 : 1; b >= 0; --b) {
+            for (int b = TT >= 128 ? 3 : 1; b >= 0; --b) {
               if (q.n16 - m >= 16 << b) {
                 tma_load_2d(tok + m * 128, &a_maps.rows[b], kb * 128, q.row0 + m, &full_bar[slot]);
                 m += 16 << b;
@@ -514,8 +514,8 @@ __global__ void __launch_bounds__(GCfg<MODE, TT>::THREADS, GCfg<MODE, TT>::BLOCK
   } else {
     // -------------------------------------------------------------- results
     const int qd = warp & 3;
-    const int half = (warp - 4) >> 2;  // TT = 256: columns 0..127 or 128..255
-    constexpr int COLS = TT == 32 ? 32 : 128;  // columns (rows of Y) per warp
+    const int half = (warp - 4) >> 2;  // TT >= 128: which half of the columns
+    constexpr int COLS = TT == 32 ? 32 : TT / 2;  // columns (rows of Y) per warp
     const float scale = MODE == kTensor ? __ldg(static_cast<const float*>(p.a_scales)) * __ldg(p.b_s) : 1.f;
     bool ok = true;
     for (int i = 0; i < shares; ++i) {
@@ -610,7 +610,7 @@ __global__ void __launch_bounds__(GCfg<MODE, TT>::THREADS, GCfg<MODE, TT>::BLOCK
   if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
 }
 
-// What TT = 256 lays out first: the gathered rows of A (a_rows) and the token
+// What TT >= 128 lays out first: the gathered rows of A (a_rows) and the token
 // scale atoms (a_sf), each where wanted.
 struct PrepParams {
   const uint8_t* a;
@@ -618,78 +618,87 @@ struct PrepParams {
   const int32_t* offsets;
   const int32_t* rows;
   uint8_t* a_rows;  // [R][rb] or null
-  uint8_t* a_sf;    // [tile][NA][2][512], NA atoms a 128-row block (null: no MX scales)
+  uint8_t* a_sf;    // [tile][NA][128-row block of the tile][512] (null: no MX scales)
   int T, R, E;
   int rb;           // bytes of a row of A
   int sb;           // scale bytes of a row
   int NA;           // atoms of a 128-row block: four scale bytes of each row to an atom
+  int copy_blocks;  // the first blocks copy rows, the others build atoms
 };
 
+constexpr int kPrepRows = 4;  // rows a copying block has in flight, 64 threads each
+
+template <int TT>
 __global__ void __launch_bounds__(256) grouped_prep_kernel(const PrepParams p) {
-  __shared__ int offs_sh[kMaxExperts + 1], tiles_sh[kMaxExperts + 1];
+  extern __shared__ int sched_sh[];
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t threads = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  const int64_t tid = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (p.a_rows) {
-    // a warp per row, 16 bytes a lane
-    const int lane = threadIdx.x & 31;
-    for (int64_t i = tid >> 5; i < p.R; i += threads >> 5) {
+  if (static_cast<int>(blockIdx.x) < p.copy_blocks) {
+    const int lane = threadIdx.x & 63, chunks = p.rb / 16;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kPrepRows + (threadIdx.x >> 6); i < p.R;
+         i += static_cast<int64_t>(p.copy_blocks) * kPrepRows) {
       const int row = min(max(__ldg(p.rows + i), 0), p.T - 1);
       const uint4* src = reinterpret_cast<const uint4*>(p.a + static_cast<size_t>(row) * p.rb);
       uint4* dst = reinterpret_cast<uint4*>(p.a_rows + static_cast<size_t>(i) * p.rb);
-      for (int c0 = 0; c0 < p.rb / 16; c0 += 128) {
-        uint4 v[4];
+      for (int c0 = lane; c0 < chunks; c0 += 8 * 64) {
+        uint4 v[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (c0 + j * 32 + lane < p.rb / 16) v[j] = __ldg(src + c0 + j * 32 + lane);
+        for (int j = 0; j < 8; ++j)
+          if (c0 + j * 64 < chunks) v[j] = __ldg(src + c0 + j * 64);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (c0 + j * 32 + lane < p.rb / 16) dst[c0 + j * 32 + lane] = v[j];
+        for (int j = 0; j < 8; ++j)
+          if (c0 + j * 64 < chunks) dst[c0 + j * 64] = v[j];
       }
     }
+    return;
   }
-  if (!p.a_sf) return;
-  read_offsets<256>(p.offsets, p.R, p.E, offs_sh, tiles_sh);
+  constexpr int BLOCKS = TT / 128;  // 128-row blocks of a tile
+  int* offs = sched_sh;
+  int* tiles = sched_sh + p.E + 1;
+  read_offsets<TT>(p.offsets, p.R, p.E, offs, tiles);
   Schedule s;
-  s.offs = offs_sh;
-  s.tiles = tiles_sh;
+  s.offs = offs;
+  s.tiles = tiles;
   s.E = p.E;
   s.NT = 1;
   // A thread takes four atoms in a row of one line: byte 16 * line + 4 * b + j
   // of an atom belongs to row 32 * b + line of its 128, scale byte 4 * atom + j.
   const int quads = (p.NA + 3) / 4;
-  const int64_t total = static_cast<int64_t>(tiles_sh[p.E]) * quads * 64;
-  for (int64_t i = tid; i < total; i += threads) {
-    const int line = static_cast<int>(i & 31), half = static_cast<int>(i >> 5) & 1;
-    const int64_t tq = i >> 6;
+  const bool whole = (p.sb & 15) == 0 && (reinterpret_cast<uintptr_t>(p.scales) & 15u) == 0;
+  const int64_t total = static_cast<int64_t>(tiles[p.E]) * quads * (32 * BLOCKS);
+  const int64_t step = static_cast<int64_t>(gridDim.x - p.copy_blocks) * blockDim.x;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x - p.copy_blocks) * blockDim.x + threadIdx.x; i < total; i += step) {
+    const int line = static_cast<int>(i & 31), blk = static_cast<int>(i >> 5) % BLOCKS;
+    const int64_t tq = (i >> 5) / BLOCKS;
     const int tile = static_cast<int>(tq / quads), quad = static_cast<int>(tq - static_cast<int64_t>(tile) * quads);
-    const Unit q = unit_at<256>(s, tile);
-    if (half * 128 >= q.n16) continue;
-    uint32_t w[4][4];  // [atom][block of 32 rows]
+    const Unit q = unit_at<TT>(s, tile);
+    if (blk * 128 >= q.n16) continue;
+    uint32_t w[4][4];  // [block of 32 rows][atom]
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
-      const int m = min(half * 128 + b * 32 + line, q.count - 1);
+      const int m = min(blk * 128 + b * 32 + line, q.count - 1);
       int row = q.row0 + m;
       if (p.rows) row = min(max(__ldg(p.rows + row), 0), p.T - 1);
-      const uint8_t* src = p.scales + static_cast<size_t>(row) * p.sb;
+      const uint8_t* src = p.scales + static_cast<size_t>(row) * p.sb + quad * 16;
+      if (whole) {
+        const uint4 u = __ldg(reinterpret_cast<const uint4*>(src));
+        w[b][0] = u.x; w[b][1] = u.y; w[b][2] = u.z; w[b][3] = u.w;
+      } else {
 #pragma unroll
-      for (int a = 0; a < 4; ++a) {
-        uint32_t v = 0;
+        for (int a = 0; a < 4; ++a) {
+          w[b][a] = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int c = (quad * 4 + a) * 4 + j;
-          if (c < p.sb) v |= static_cast<uint32_t>(__ldg(src + c)) << (8 * j);
+          for (int j = 0; j < 4; ++j)
+            if (quad * 16 + a * 4 + j < p.sb) w[b][a] |= static_cast<uint32_t>(__ldg(src + a * 4 + j)) << (8 * j);
         }
-        w[a][b] = v;
       }
     }
 #pragma unroll
     for (int a = 0; a < 4; ++a) {
       const int atom = quad * 4 + a;
       if (atom < p.NA)
-        *reinterpret_cast<uint4*>(p.a_sf + ((static_cast<size_t>(tile) * p.NA + atom) * 2 + half) * 512 + line * 16) =
-            make_uint4(w[a][0], w[a][1], w[a][2], w[a][3]);
+        *reinterpret_cast<uint4*>(p.a_sf + ((static_cast<size_t>(tile) * p.NA + atom) * BLOCKS + blk) * 512 + line * 16) =
+            make_uint4(w[0][a], w[1][a], w[2][a], w[3][a]);
     }
   }
 }
@@ -720,27 +729,36 @@ cudaError_t launch_mode(const AMaps& a_maps, const CUtensorMap& tmap_b, const Gr
   if (tt == 32)
     return p.rows ? launch_one<MODE, 32, true>(a_maps, tmap_b, p, blocks, stream)
                   : launch_one<MODE, 32, false>(a_maps, tmap_b, p, blocks, stream);
-  return launch_one<MODE, 256, false>(a_maps, tmap_b, p, blocks, stream);
+  return tt == 128 ? launch_one<MODE, 128, false>(a_maps, tmap_b, p, blocks, stream)
+                   : launch_one<MODE, 256, false>(a_maps, tmap_b, p, blocks, stream);
 }
 
-cudaError_t launch_prep(const PrepParams& p, cudaStream_t stream) {
+cudaError_t launch_prep(PrepParams p, int tt, int64_t tiles, cudaStream_t stream) {
+  // blocks in proportion to the work, at most eight an SM for each part
+  const int64_t most = 8 * static_cast<int64_t>(sm_count());
+  const int64_t rows = p.a_rows ? (p.R + kPrepRows - 1) / kPrepRows : 0;
+  const int64_t lines = p.a_sf ? (tiles * ((p.NA + 3) / 4) * (tt / 4) + 255) / 256 : 0;
+  p.copy_blocks = static_cast<int>(rows < most ? rows : most);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(sm_count() * 8);
+  cfg.gridDim = dim3(static_cast<unsigned>(p.copy_blocks + (lines < most ? lines : most)));
   cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 8 * (p.E + 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = pdl_enabled() ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, grouped_prep_kernel, p);
+  return tt == 128 ? cudaLaunchKernelEx(&cfg, grouped_prep_kernel<128>, p)
+                   : cudaLaunchKernelEx(&cfg, grouped_prep_kernel<256>, p);
 }
 
 // Token tile, blocks and workspace of a call: partials and tickets (tt 32), or
-// scale atoms and gathered rows (tt 256), in this order.
+// scale atoms and gathered rows (tt 128 and 256), in this order.
 struct GroupedPlan {
   int tt, blocks;
-  int atoms;  // scale atoms of a 128-row block
+  int64_t tiles;  // no more token tiles than this, however the rows fall
+  int atoms;      // scale atoms of a 128-row block
   uint64_t part_bytes, ticket_bytes, sf_bytes, rows_bytes;
   uint64_t total() const { return part_bytes + ticket_bytes + sf_bytes + rows_bytes; }
 };
@@ -750,11 +768,15 @@ GroupedPlan grouped_plan(int mode, int64_t R, int64_t E, int64_t N, int64_t K, b
   memset(&g, 0, sizeof g);
   if (R == 0) return g;
   const int64_t KB = row_bytes(mode, K) / 128;
-  g.tt = R <= 16 * E ? 32 : 256;
+  // Rows an expert on average decide the tile.  Measured (64 experts, 4096 x
+  // 7168, mxfp8): 16 rows an expert 326 us with tt 32 (experts above 32 rows
+  // read their weights again) and 289 with 128; 64 rows 311 us with 128 (six
+  // stages) and 338 with 256; 128 rows 402 and 381.  At 8 rows tt 32 and 128
+  // are equal; below, the layout kernel and idle blocks cost more.
+  g.tt = R <= 8 * E ? 32 : (R <= 80 * E ? 128 : 256);
   const int64_t most = g.tt == 32 ? 2 * static_cast<int64_t>(sm_count()) : sm_count();
-  // no more token tiles than this, however the rows fall
-  const int64_t tiles = R / g.tt + (E < R ? E : R);
-  const int64_t units = tiles * (N / 128);
+  g.tiles = R / g.tt + (E < R ? E : R);
+  const int64_t units = g.tiles * (N / 128);
   const int64_t want = g.tt == 32 ? (units * KB + kMinSlabs - 1) / kMinSlabs : units;
   g.blocks = static_cast<int>(want < most ? want : most);
   if (g.tt == 32) {
@@ -763,7 +785,7 @@ GroupedPlan grouped_plan(int mode, int64_t R, int64_t E, int64_t N, int64_t K, b
   } else {
     if (is_mx(mode)) {
       g.atoms = static_cast<int>((mx_sf_cols(mode, K) + 3) / 4);
-      g.sf_bytes = static_cast<uint64_t>(tiles) * g.atoms * 1024;
+      g.sf_bytes = static_cast<uint64_t>(g.tiles) * g.atoms * (g.tt / 128) * 512;
     }
     if (gather) g.rows_bytes = static_cast<uint64_t>(R) * row_bytes(mode, K);
   }
@@ -867,8 +889,8 @@ fg_status fg_grouped_gemm(const void* A, const void* a_scales, int64_t T, const 
   if (g.sf_bytes || g.rows_bytes) {
     PrepParams q{static_cast<const uint8_t*>(A), static_cast<const uint8_t*>(a_scales), offsets, rows, a_rows,
                  g.sf_bytes ? ws : nullptr, p.T, p.R, E, static_cast<int>(rb),
-                 is_mx(mode) ? static_cast<int>(mx_sf_cols(mode, K)) : 0, g.atoms};
-    if ((e = launch_prep(q, st)) != cudaSuccess) return cuda_fail(e, "grouped product's layout launch");
+                 is_mx(mode) ? static_cast<int>(mx_sf_cols(mode, K)) : 0, g.atoms, 0};
+    if ((e = launch_prep(q, g.tt, g.tiles, st)) != cudaSuccess) return cuda_fail(e, "grouped product's layout launch");
   }
   switch (mode) {
     case FG_BF16: e = launch_mode<kBF16>(a_maps, tmap_b, p, g.tt, g.blocks, st); break;
