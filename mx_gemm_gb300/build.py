@@ -2,7 +2,9 @@
 (one process per translation unit, in parallel) and links ``_build/libfg.so``
 next to this file.  The CUDA runtime is linked statically; the driver's
 tensor-map encoder is looked up at run time, so the library needs no
-libcuda at link time.
+libcuda at link time.  csrc/fg_torch.cpp, the binding that allocates outputs
+through torch, is compiled beside them with g++ into ``_build/fg_torch.so``,
+which finds libfg.so next to itself and torch's libraries in the process.
 """
 import concurrent.futures as cf
 import glob
@@ -15,6 +17,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT, "libfg.so")
+BINDING = os.path.join(OUT, "fg_torch.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-Xcompiler", "-fvisibility=hidden"]
@@ -32,15 +35,44 @@ def _sources():
 
 
 def _deps():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + \
+    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.cpp")) + \
         [os.path.join(os.path.dirname(HERE), "include", "fg.h")]
 
 
 def up_to_date():
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(BINDING)):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(d) <= t for d in _deps())
+
+
+def _run(cmd, what):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("%s failed:\n%s%s" % (what, r.stdout, r.stderr))
+
+
+def _compile_binding(obj):
+    """csrc/fg_torch.cpp against the installed torch's headers."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    paths = cpp_extension.include_paths() + [sysconfig.get_paths()["include"], os.path.join(os.path.dirname(
+        os.path.dirname(nvcc())), "include")]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wno-deprecated-declarations",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI]
+    _run(cmd + ["-isystem" + p for p in paths] + ["-c", os.path.join(CSRC, "fg_torch.cpp"), "-o", obj],
+         "g++ for fg_torch.cpp")
+
+
+def _link_binding(obj):
+    import torch
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + ".tmp.%d" % os.getpid()
+    _run(["g++", "-shared", "-o", tmp, obj, "-L" + OUT, "-l:libfg.so", "-Wl,-rpath,$ORIGIN", "-L" + libs, "-ltorch_python",
+          "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda"], "link of fg_torch.so")
+    os.replace(tmp, BINDING)
 
 
 def build(force=False, verbose=False):
@@ -60,8 +92,11 @@ def build(force=False, verbose=False):
         return obj, r.stderr
 
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
+    binding = os.path.join(OUT, "fg_torch.cpp.o")
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
+        other = ex.submit(_compile_binding, binding)
         results = list(ex.map(compile_one, srcs))
+        other.result()
     if verbose:
         for _, log in results:
             sys.stderr.write(log)
@@ -72,6 +107,7 @@ def build(force=False, verbose=False):
     if r.returncode != 0:
         raise RuntimeError("link failed:\n%s%s" % (r.stdout, r.stderr))
     os.replace(tmp, LIB)
+    _link_binding(binding)
     return LIB
 
 
