@@ -430,6 +430,8 @@ fg_status make_tmap_out64(CUtensorMap* map, void* y, int64_t rows, int64_t n) {
   return FG_OK;
 }
 
+}  // namespace
+
 // Plain (unswizzled) 2-D map over `rows` rows of `rbytes` bytes (a multiple
 // of 8, at most 2048) in 8-byte elements, with a box of box_rows whole rows:
 // the weight image as 2 KiB rows (a 16 KiB slab is 8 of them) or a scale
@@ -448,8 +450,6 @@ fg_status make_tmap_rows(CUtensorMap* map, const void* base, int64_t rows, uint3
   if (r != CUDA_SUCCESS) return fail(FG_ERR_CUDA, "cuTensorMapEncodeTiled (rows) failed (%d)", static_cast<int>(r));
   return FG_OK;
 }
-
-}  // namespace
 
 // MXFP4_FP8A weight image (blocks of 128 rows x 64 bytes of packed e2m1, see
 // fg_preshuffle_b) as a 3-D map of 4-bit codes {128 codes, 128 rows,

@@ -37,6 +37,7 @@
 
 #include <cstring>
 
+#include "fg_grouped.cuh"
 #include "fg_host.cuh"
 #include "fg_internal.cuh"
 #include "fg_ptx.cuh"
@@ -45,28 +46,8 @@ namespace fg {
 
 namespace {
 
-constexpr int kMaxExperts = 1024;
-constexpr int kSlabBytes = 16384;
 constexpr int kMinSlabs = 4;    // K steps a block of the cut line takes at least
 constexpr int kShareSteps = 8;  // see the schedule
-
-struct GroupedParams {
-  const uint8_t* b_img;
-  const uint8_t* b_sf;
-  const float* b_s;           // FP8_TENSOR
-  const void* a_scales;
-  const int32_t* offsets;     // [E + 1]
-  const int32_t* rows;        // [R] or null
-  __nv_bfloat16* y;           // [R][N]
-  const uint8_t* a_sf;        // TT >= 128, MX: token scale atoms [tile][K step][atom][128-row block][512]
-  float* part;                // [blocks][2][TT][128] partials (cut line)
-  unsigned long long* tickets;  // [blocks] arrivals at the unit that begins last in the block
-  unsigned long long epoch;
-  uint32_t* err;
-  uint64_t timeout_ns;
-  int T, R, E, N, K, KB;
-  int debug_stall;
-};
 
 template <int MODE, int TT>
 struct GCfg {
@@ -99,47 +80,11 @@ struct GCfg {
                 "shared memory budget");
 };
 
-// The unit's rows and weight tile.
-struct Unit {
-  int e, row0, count, n16, nt;  // n16: rows rounded up to 16
-  int tile;                     // token tile, over all experts
-};
-
 // One block's share of a unit: K steps [k0, k1).
 struct Share {
   long long u;
   int k0, k1;
 };
-
-struct Schedule {
-  const int* offs;   // [E + 1] clamped offsets
-  const int* tiles;  // [E + 1] token tiles before expert e
-  long long units, W, lo, hi;
-  int E, NT, KB, blocks, c;
-  bool cut;  // the line of all K steps is cut evenly; else units are dealt out whole
-};
-
-template <int TT>
-__device__ __forceinline__ Unit unit_at(const Schedule& s, long long u) {
-  int a = 0, b = s.E;  // the last e with tiles[e] * NT <= u
-  while (b - a > 1) {
-    const int m = (a + b) >> 1;
-    if (static_cast<long long>(s.tiles[m]) * s.NT <= u) a = m; else b = m;
-  }
-  const int r = static_cast<int>(u - static_cast<long long>(s.tiles[a]) * s.NT);
-  const int n = s.tiles[a + 1] - s.tiles[a];
-  const int rows = s.offs[a + 1] - s.offs[a];
-  const int per = ((rows + n - 1) / n + 15) & ~15;
-  Unit q;
-  q.e = a;
-  q.nt = r / n;
-  const int m = r - q.nt * n;
-  q.tile = s.tiles[a] + m;
-  q.row0 = s.offs[a] + m * per;
-  q.count = min(per, rows - m * per);
-  q.n16 = (q.count + 15) & ~15;
-  return q;
-}
 
 // Cut c of the line of W steps over `blocks` blocks, and the block that holds step x.
 __device__ __forceinline__ long long cut_at(const Schedule& s, int c) { return s.W * c / s.blocks; }
@@ -167,32 +112,6 @@ __device__ __forceinline__ Share share_at(const Schedule& s, int i) {
   return h;
 }
 
-// The offsets, clamped into 0..R, and the token tiles before each expert, by
-// the whole block (any count of warps); ends with the block in step.
-template <int TT>
-__device__ __forceinline__ void read_offsets(const int32_t* offsets, int R, int E, int* offs, int* tiles) {
-  for (int e = threadIdx.x; e <= E; e += blockDim.x) offs[e] = min(max(__ldg(offsets + e), 0), R);
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    const int lane = threadIdx.x;
-    int carry = 0;
-    for (int e0 = 0; e0 < E; e0 += 32) {
-      const int e = e0 + lane;
-      const int t = e < E ? (max(0, offs[e + 1] - offs[e]) + TT - 1) / TT : 0;
-      int sum = t;
-#pragma unroll
-      for (int d = 1; d < 32; d *= 2) {
-        const int o = __shfl_up_sync(0xffffffffu, sum, d);
-        if (lane >= d) sum += o;
-      }
-      if (e < E) tiles[e] = carry + sum - t;
-      carry += __shfl_sync(0xffffffffu, sum, 31);
-    }
-    if (lane == 0) tiles[E] = carry;
-  }
-  __syncthreads();
-}
-
 template <int MODE>
 __device__ __forceinline__ void mma_step(uint32_t d, uint64_t a, uint64_t b, int n, int j, int kb, uint32_t sfw,
                                          uint32_t sft, int tok_atoms, uint32_t accum) {
@@ -213,14 +132,6 @@ __device__ __forceinline__ void mma_step(uint32_t d, uint64_t a, uint64_t b, int
     mma_mxf4(d, a, b, idesc_mx(128, n, kMxf4E2M1, id, id), sfw + 4 * g, sft + 4 * tok_atoms * g, accum);
   }
 }
-
-// A as rows of bytes: boxes of 128 bytes x 16, 32, 64, 128 rows, so that a tile
-// of up to 256 rows takes few copies and moves only its own rows (a copy costs
-// its issuing thread tens of cycles: 16 boxes of 16 rows a K step held the
-// whole kernel back).  TT = 32 uses the first; GATHER: 1 row.
-struct AMaps {
-  CUtensorMap rows[4];
-};
 
 // tmap_b: fp8 x fp4 only, the weight image's blocks.
 template <int MODE, int TT, bool GATHER>
@@ -315,7 +226,7 @@ __global__ void __launch_bounds__(GCfg<MODE, TT>::THREADS, GCfg<MODE, TT>::BLOCK
       const long long wt = static_cast<long long>(q.e) * s.NT + q.nt;  // weight tile of the stacked image
       // rows that are copied; the accumulator's columns past them hold what
       // the rows of an earlier step left and are not stored
-      const int copied = GATHER ? (q.count + 3) & ~3 : q.n16;
+      const int copied = GATHER ? (q.count + 3) & ~3 : q.width;
       const uint32_t bytes = (MODE == kMXFP4FP8A ? kSlabBytes / 2 : kSlabBytes) + copied * 128 + C::SFW_BYTES +
                              (C::SCALE_WARPS ? 0 : C::SFT_BYTES);
       // the weight's part of a stage (one lane)
@@ -361,13 +272,9 @@ __global__ void __launch_bounds__(GCfg<MODE, TT>::THREADS, GCfg<MODE, TT>::BLOCK
           if (it >= early) weights(kb, slot);
           if (!GATHER) {
             int m = 0;
-            if (TT == 256 && q.n16 == 256) {
-              tma_load_2d(tok, &a_maps.rows[3], kb * 128, q.row0, &full_bar[slot]);
-              m = 128;
-            }
 #pragma unroll
-            for (int b = TT >= 128 ? 3 : 1; b >= 0; --b) {
-              if (q.n16 - m >= 16 << b) {
+            for (int b = TT == 128 ? 3 : 1; b >= 0; --b) {
+              if (q.width - m >= 16 << b) {
                 tma_load_2d(tok + m * 128, &a_maps.rows[b], kb * 128, q.row0 + m, &full_bar[slot]);
                 m += 16 << b;
               }
@@ -420,14 +327,14 @@ __global__ void __launch_bounds__(GCfg<MODE, TT>::THREADS, GCfg<MODE, TT>::BLOCK
               tc_cp_32x128b_warpx4(sfw + 4 * g, sdesc_plain_rows16(sw + 512 * g));
 #pragma unroll
               for (int a = 0; a < C::TOK_ATOMS; ++a)
-                if (a == 0 || q.n16 > a * 128)
+                if (a == 0 || q.width > a * 128)
                   tc_cp_32x128b_warpx4(sft + 4 * (g * C::TOK_ATOMS + a),
                                        sdesc_plain_rows16(stk + 512 * (g * C::TOK_ATOMS + a)));
             }
           }
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            mma_step<MODE>(d, sdesc_sw128(st + j * 32), sdesc_sw128(st + kSlabBytes + j * 32), q.n16, j, kb, sfw, sft,
+            mma_step<MODE>(d, sdesc_sw128(st + j * 32), sdesc_sw128(st + kSlabBytes + j * 32), q.width, j, kb, sfw, sft,
                            C::TOK_ATOMS, (kb > h.k0 || j > 0) ? 1u : 0u);
           tc_commit(&empty_bar[slot]);
         }
@@ -482,7 +389,7 @@ __global__ void __launch_bounds__(GCfg<MODE, TT>::THREADS, GCfg<MODE, TT>::BLOCK
           for (int j = 0; j < PT; ++j)
 #pragma unroll
             for (int g = 0; g < C::APS; ++g)
-              if (st_id + 64 * j < q.n16) next[j][g] = word(j, kb, g);
+              if (st_id + 64 * j < q.width) next[j][g] = word(j, kb, g);
         };
         fetch(h.k0);
         for (int kb = h.k0; kb < h.k1; ++kb, ++it) {
@@ -496,7 +403,7 @@ __global__ void __launch_bounds__(GCfg<MODE, TT>::THREADS, GCfg<MODE, TT>::BLOCK
 #pragma unroll
           for (int j = 0; j < PT; ++j) {
             const int m = st_id + 64 * j;
-            if (m < q.n16) {
+            if (m < q.width) {
 #pragma unroll
               for (int g = 0; g < C::APS; ++g)
                 *reinterpret_cast<uint32_t*>(sft + (g * C::TOK_ATOMS + (m >> 7)) * 512 + (m & 31) * 16 +
@@ -672,7 +579,7 @@ __global__ void __launch_bounds__(256) grouped_prep_kernel(const PrepParams p) {
     const int64_t tq = (i >> 5) / BLOCKS;
     const int tile = static_cast<int>(tq / quads), quad = static_cast<int>(tq - static_cast<int64_t>(tile) * quads);
     const Unit q = unit_at<TT>(s, tile);
-    if (blk * 128 >= q.n16) continue;
+    if (blk * 128 >= q.width) continue;
     uint32_t w[4][4];  // [block of 32 rows][atom]
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
@@ -729,8 +636,7 @@ cudaError_t launch_mode(const AMaps& a_maps, const CUtensorMap& tmap_b, const Gr
   if (tt == 32)
     return p.rows ? launch_one<MODE, 32, true>(a_maps, tmap_b, p, blocks, stream)
                   : launch_one<MODE, 32, false>(a_maps, tmap_b, p, blocks, stream);
-  return tt == 128 ? launch_one<MODE, 128, false>(a_maps, tmap_b, p, blocks, stream)
-                   : launch_one<MODE, 256, false>(a_maps, tmap_b, p, blocks, stream);
+  return launch_one<MODE, 128, false>(a_maps, tmap_b, p, blocks, stream);
 }
 
 cudaError_t launch_prep(PrepParams p, int tt, int64_t tiles, cudaStream_t stream) {
@@ -753,7 +659,7 @@ cudaError_t launch_prep(PrepParams p, int tt, int64_t tiles, cudaStream_t stream
                    : cudaLaunchKernelEx(&cfg, grouped_prep_kernel<256>, p);
 }
 
-// Token tile, blocks and workspace of a call: partials and tickets (tt 32), or
+// Token tile, blocks (two for each pair of SMs) and workspace of a call: partials and tickets (tt 32), or
 // scale atoms and gathered rows (tt 128 and 256), in this order.
 struct GroupedPlan {
   int tt, blocks;
@@ -774,11 +680,11 @@ GroupedPlan grouped_plan(int mode, int64_t R, int64_t E, int64_t N, int64_t K, b
   // stages) and 338 with 256; 128 rows 402 and 381.  At 8 rows tt 32 and 128
   // are equal; below, the layout kernel and idle blocks cost more.
   g.tt = R <= 8 * E ? 32 : (R <= 80 * E ? 128 : 256);
-  const int64_t most = g.tt == 32 ? 2 * static_cast<int64_t>(sm_count()) : sm_count();
+  const int64_t most = g.tt == 32 ? 2 * static_cast<int64_t>(sm_count()) : (g.tt == 128 ? sm_count() : grouped_pair_clusters());
   g.tiles = R / g.tt + (E < R ? E : R);
-  const int64_t units = g.tiles * (N / 128);
+  const int64_t units = g.tiles * (g.tt == 256 ? (N / 128 + 1) / 2 : N / 128);
   const int64_t want = g.tt == 32 ? (units * KB + kMinSlabs - 1) / kMinSlabs : units;
-  g.blocks = static_cast<int>(want < most ? want : most);
+  g.blocks = static_cast<int>(want < most ? want : most) * (g.tt == 256 ? 2 : 1);
   if (g.tt == 32) {
     g.part_bytes = static_cast<uint64_t>(g.blocks) * 2 * g.tt * 128 * 4;
     g.ticket_bytes = static_cast<uint64_t>(g.blocks) * 8;
@@ -891,6 +797,20 @@ fg_status fg_grouped_gemm(const void* A, const void* a_scales, int64_t T, const 
                  g.sf_bytes ? ws : nullptr, p.T, p.R, E, static_cast<int>(rb),
                  is_mx(mode) ? static_cast<int>(mx_sf_cols(mode, K)) : 0, g.atoms, 0};
     if ((e = launch_prep(q, g.tt, g.tiles, st)) != cudaSuccess) return cuda_fail(e, "grouped product's layout launch");
+  }
+  if (g.tt == 256) {
+    if (g.blocks == 0) return fail(FG_ERR_CUDA, "%s: no room for a pair of SMs", what);
+    CUtensorMap tmap_w = tmap_b, tmap_wsf, tmap_asf;
+    memset(&tmap_wsf, 0, sizeof tmap_wsf);
+    memset(&tmap_asf, 0, sizeof tmap_asf);
+    if (mode != FG_MXFP4_FP8A && (s = make_tmap_rows(&tmap_w, b->data, (b->N / 128) * p.KB * 8, 2048, 8)) != FG_OK) return s;
+    if (is_mx(mode)) {
+      const uint32_t aps = mode == FG_MXFP4 ? 2 : 1;
+      if ((s = make_tmap_rows(&tmap_wsf, b->sf, static_cast<int64_t>(b->sf_bytes / 512), 512, aps)) != FG_OK) return s;
+      if ((s = make_tmap_rows(&tmap_asf, ws, static_cast<int64_t>(g.sf_bytes / 512), 512, 2 * aps)) != FG_OK) return s;
+    }
+    e = launch_grouped_pair(mode, a_maps, tmap_w, tmap_wsf, tmap_asf, p, g.blocks, st);
+    return e == cudaSuccess ? FG_OK : cuda_fail(e, "grouped product launch");
   }
   switch (mode) {
     case FG_BF16: e = launch_mode<kBF16>(a_maps, tmap_b, p, g.tt, g.blocks, st); break;

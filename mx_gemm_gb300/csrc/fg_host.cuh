@@ -27,8 +27,10 @@ uint64_t wait_timeout_ns();
 uint64_t next_epoch();
 
 // Byte-typed 2-D map of [rows][row bytes], boxes of box_rows x 128 bytes in
-// the 128-byte swizzle; and the 3-D map of an fp4 weight image.
+// the 128-byte swizzle; a plain map of whole rows (at most 2048 bytes) in
+// 8-byte elements; and the 3-D map of an fp4 weight image.
 fg_status make_tmap(CUtensorMap* map, const void* base, int64_t rows, int64_t rbytes, uint32_t box_rows);
+fg_status make_tmap_rows(CUtensorMap* map, const void* base, int64_t rows, uint32_t rbytes, uint32_t box_rows);
 fg_status make_tmap_fp4w(CUtensorMap* map, const void* base, int64_t N, int64_t K);
 
 }  // namespace fg
