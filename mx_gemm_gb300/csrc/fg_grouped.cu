@@ -16,16 +16,18 @@
 // it once.  No work is launched for experts without rows, and nothing comes
 // back to the host.
 //
-//  - TT = 128, 256 (many rows an expert): units are dealt out whole.  Bound by the
-//    tensor cores and the stream from L2.  A first kernel lays out what every
-//    weight tile reads again: the gathered rows one after the other (tensor
-//    copies of four indexed rows each took three times as long as the product
-//    itself: 1797 us against 624 us for 32768 mxfp4 rows, 4096 x 7168), and the
-//    token scales as the atoms the tensor core reads.
-//  - TT = 32 (decoding): bound by the weights' bytes from HBM, whatever the
-//    rows.  The K steps of all units form one line that is cut evenly over the
-//    blocks, wherever the cuts fall, so that all SMs stream to the end.  Blocks
-//    that share a unit leave fp32 partials in the workspace; the last to
+//  - Many rows an expert (TT = 256): units of two weight tiles are dealt out
+//    whole to pairs of SMs (fg_grouped_pair.cu).  Bound by the tensor cores and
+//    the weights' bytes from HBM.  A first kernel lays out what every weight tile
+//    reads again: the gathered rows one after the other (tensor copies of four
+//    indexed rows each took three times as long as the product itself: 1797 us
+//    against 624 us for 32768 mxfp4 rows, 4096 x 7168), and the token scales as
+//    the atoms the tensor core reads.
+//  - Few (TT = 32, decoding; this file): bound by the weights' bytes from HBM,
+//    whatever the rows.  Where dealing whole units to the blocks would leave
+//    much idle, the K steps of all units form one line that is cut evenly over
+//    the blocks, wherever the cuts fall, so that all SMs stream to the end.
+//    Blocks that share a unit leave fp32 partials in the workspace; the last to
 //    arrive adds them in the order of K (the same bits each time) and stores.
 //    Nobody waits for another block.
 //
@@ -49,35 +51,31 @@ namespace {
 constexpr int kMinSlabs = 4;    // K steps a block of the cut line takes at least
 constexpr int kShareSteps = 8;  // see the schedule
 
-template <int MODE, int TT>
+constexpr int TT = 32;           // rows of a token tile
+constexpr int kThreads = 256;    // copies, MMAs, two warps of scales, four of results
+constexpr int kBlocksPerSm = 2;
+
+constexpr bool smem_fits(int bytes) { return kBlocksPerSm * (bytes + 1024 + 256) <= 233472; }
+
+template <int MODE>
 struct GCfg {
   static constexpr int APS = MODE == kMXFP4 ? 2 : (is_mx(MODE) ? 1 : 0);
-  static constexpr bool CUT = TT == 32;           // the cut line of K steps
   // fp8 x fp4 moves half a stage's bytes from HBM: one stage more (28.5 -> 28.2 us
   // for one token, 103 -> 100 us for eight); the 8-bit modes lost 2-4 % with it
-  static constexpr int STAGES = TT == 128 ? 6 : (TT == 32 && MODE == kMXFP4FP8A ? 5 : 4);
+  static constexpr int STAGES = MODE == kMXFP4FP8A ? 5 : 4;
   static constexpr int TOK_BYTES = TT * 128;
-  static constexpr int TOK_ATOMS = (TT + 127) / 128;
   static constexpr int SFW_BYTES = APS * 512;
-  static constexpr int SFT_BYTES = APS * TOK_ATOMS * 512;
-  static constexpr bool SCALE_WARPS = APS > 0 && TT == 32;  // else the atoms come by bulk copy
+  static constexpr int SFT_BYTES = APS * 512;
   static constexpr int STAGE_RAW = kSlabBytes + TOK_BYTES + SFW_BYTES + SFT_BYTES;
   static constexpr int STAGE_BYTES = (STAGE_RAW + 1023) / 1024 * 1024;
-  static constexpr int SMEM = STAGES * STAGE_BYTES + 1024;
-  static constexpr int EPI_WARPS = TT == 32 ? 4 : 8;
-  static constexpr int THREADS = 128 + 32 * EPI_WARPS;
-  static constexpr int ACCS = TT <= 128 ? 2 : 1;  // accumulators
-  static constexpr int ACC_COLS = ACCS * TT;
-  static constexpr int SFW_COLS = APS * 4, SFT_COLS = APS * 4 * TOK_ATOMS;
-  static constexpr int TMEM_NEED = ACC_COLS + STAGES * (SFW_COLS + SFT_COLS);
-  static constexpr int TMEM_COLS =
-      TMEM_NEED <= 64 ? 64 : (TMEM_NEED <= 128 ? 128 : (TMEM_NEED <= 256 ? 256 : 512));
-  static constexpr int BLOCKS_PER_SM = TT == 32 ? 2 : 1;
-  static_assert(TMEM_NEED <= 512 && BLOCKS_PER_SM * TMEM_COLS <= 512, "TMEM budget");
-  // with the schedule of E experts: two blocks an SM up to 500 experts at TT = 32
-  static constexpr int smem(int E) { return SMEM + 8 * (E + 1); }
-  static_assert(SMEM + 8 * (kMaxExperts + 1) <= 232448 - 1024 && BLOCKS_PER_SM * (SMEM + 8 * 500 + 1536) <= 233472,
-                "shared memory budget");
+  static constexpr int SF_COLS = APS * 4;  // of each operand
+  static constexpr int ACC_COLS = 2 * TT;  // two accumulators
+  static constexpr int TMEM_NEED = ACC_COLS + STAGES * 2 * SF_COLS;
+  static constexpr int TMEM_COLS = TMEM_NEED <= 64 ? 64 : (TMEM_NEED <= 128 ? 128 : 256);
+  // with the schedule of E experts: two blocks an SM up to 500 experts
+  static constexpr int smem(int E) { return STAGES * STAGE_BYTES + 1024 + 8 * (E + 1); }
+  static_assert(TMEM_NEED <= TMEM_COLS && kBlocksPerSm * TMEM_COLS <= 512, "TMEM budget");
+  static_assert(smem_fits(STAGES * STAGE_BYTES + 1024 + 8 * 501), "shared memory budget");
 };
 
 // One block's share of a unit: K steps [k0, k1).
@@ -114,37 +112,36 @@ __device__ __forceinline__ Share share_at(const Schedule& s, int i) {
 
 template <int MODE>
 __device__ __forceinline__ void mma_step(uint32_t d, uint64_t a, uint64_t b, int n, int j, int kb, uint32_t sfw,
-                                         uint32_t sft, int tok_atoms, uint32_t accum) {
+                                         uint32_t sft, uint32_t accum) {
   if (MODE == kBF16) {
     mma_f16(d, a, b, idesc_bf16(128, n), accum);
   } else if (MODE == kTensor) {
     mma_f8f6f4(d, a, b, idesc_e4m3(128, n), accum);
   } else if (MODE == kMXFP8) {
-    // the weight's byte of its four-slab atom; the token atoms likewise, or
-    // (TT = 32) with the slab's scale in all four bytes
-    mma_mxf8f6f4(d, a, b, idesc_mx(128, n, kF8f6f4E4M3, kb & 3, kb & 3), sfw, sft, accum);
+    // the weight's byte of its four-slab atom; the token atoms have the slab's
+    // scale in all four
+    mma_mxf8f6f4(d, a, b, idesc_mx(128, n, kF8f6f4E4M3, kb & 3, j), sfw, sft, accum);
   } else if (MODE == kMXFP8B32) {
     mma_mxf8f6f4(d, a, b, idesc_mx(128, n, kF8f6f4E4M3, j, j), sfw, sft, accum);
   } else if (MODE == kMXFP4FP8A) {
     mma_mxf8f6f4(d, a, b, idesc_mx_ab(128, n, kF8f6f4E2M1, kF8f6f4E4M3, j, j), sfw, sft, accum);
   } else {
     const int g = j >> 1, id = 2 * (j & 1);
-    mma_mxf4(d, a, b, idesc_mx(128, n, kMxf4E2M1, id, id), sfw + 4 * g, sft + 4 * tok_atoms * g, accum);
+    mma_mxf4(d, a, b, idesc_mx(128, n, kMxf4E2M1, id, id), sfw + 4 * g, sft + 4 * g, accum);
   }
 }
 
 // tmap_b: fp8 x fp4 only, the weight image's blocks.
-template <int MODE, int TT, bool GATHER>
-__global__ void __launch_bounds__(GCfg<MODE, TT>::THREADS, GCfg<MODE, TT>::BLOCKS_PER_SM)
+template <int MODE, bool GATHER>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     grouped_kernel(const __grid_constant__ AMaps a_maps, const __grid_constant__ CUtensorMap tmap_b,
                    const GroupedParams p) {
-  using C = GCfg<MODE, TT>;
+  using C = GCfg<MODE>;
   constexpr int ST = C::STAGES;
-  constexpr bool CUT = C::CUT;
   extern __shared__ uint8_t dsmem[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsmem) + 1023) & ~uintptr_t(1023));
   __shared__ __align__(8) uint64_t full_bar[ST], empty_bar[ST];
-  __shared__ __align__(8) uint64_t accf_bar[C::ACCS], acce_bar[C::ACCS];
+  __shared__ __align__(8) uint64_t accf_bar[2], acce_bar[2];
   __shared__ __align__(8) uint64_t stall_bar, drain_bar;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh, issued_sh, consumed_sh, last_sh;
@@ -156,12 +153,12 @@ __global__ void __launch_bounds__(GCfg<MODE, TT>::THREADS, GCfg<MODE, TT>::BLOCK
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < ST; ++i) {
-      mbar_init(&full_bar[i], C::SCALE_WARPS ? 3 : 1);  // + one arrival per scale warp
+      mbar_init(&full_bar[i], C::APS ? 3 : 1);  // + one arrival per scale warp
       mbar_init(&empty_bar[i], 1);
     }
-    for (int i = 0; i < C::ACCS; ++i) {
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&accf_bar[i], 1);
-      mbar_init(&acce_bar[i], C::EPI_WARPS);
+      mbar_init(&acce_bar[i], 4);
     }
     mbar_init(&stall_bar, 1);
     mbar_init(&drain_bar, 1);
@@ -196,15 +193,14 @@ __global__ void __launch_bounds__(GCfg<MODE, TT>::THREADS, GCfg<MODE, TT>::BLOCK
   s.W = s.units * s.KB;
   s.c = blockIdx.x;
   s.blocks = gridDim.x;
-  s.cut = false;
-  if (CUT) {
-    // Sharing units costs a round of partials at the end, about as long as
-    // kShareSteps K steps of every block.  Units stay whole where dealing them
-    // out leaves less than that idle, and where there is at most one for each
-    // block but enough of them to keep the memory busy (a block alone has 64 KB
-    // in flight).  256 units on 304 blocks, 8-bit, K = 7168: see the table.
-    const long long G = gridDim.x;
-    const long long rounds = (s.units + G - 1) / G;
+  // Sharing units costs a round of partials at the end, about as long as
+  // kShareSteps K steps of every block.  Units stay whole where dealing them
+  // out leaves less than that idle, and where there is at most one for each
+  // block but enough of them to keep the memory busy (a block alone has 64 KB
+  // in flight).  256 units on 304 blocks, K = 7168: 26.9 us whole, 30.6 cut (fp8
+  // x fp4), 40.3 and 45.6 (mxfp8).
+  {
+    const long long G = gridDim.x, rounds = (s.units + G - 1) / G;
     const bool one_each = s.units <= G && 10 * s.units >= 6 * G;
     s.cut = !(one_each || (rounds * G - s.units) * s.KB <= kShareSteps * G);
   }
@@ -227,8 +223,7 @@ __global__ void __launch_bounds__(GCfg<MODE, TT>::THREADS, GCfg<MODE, TT>::BLOCK
       // rows that are copied; the accumulator's columns past them hold what
       // the rows of an earlier step left and are not stored
       const int copied = GATHER ? (q.count + 3) & ~3 : q.width;
-      const uint32_t bytes = (MODE == kMXFP4FP8A ? kSlabBytes / 2 : kSlabBytes) + copied * 128 + C::SFW_BYTES +
-                             (C::SCALE_WARPS ? 0 : C::SFT_BYTES);
+      const uint32_t bytes = (MODE == kMXFP4FP8A ? kSlabBytes / 2 : kSlabBytes) + copied * 128 + C::SFW_BYTES;
       // the weight's part of a stage (one lane)
       auto weights = [&](int kb, int slot) {
         uint8_t* st = smem + slot * C::STAGE_BYTES;
@@ -270,22 +265,7 @@ __global__ void __launch_bounds__(GCfg<MODE, TT>::THREADS, GCfg<MODE, TT>::BLOCK
         uint8_t* tok = st + kSlabBytes;
         if (elect_one()) {
           if (it >= early) weights(kb, slot);
-          if (!GATHER) {
-            int m = 0;
-#pragma unroll
-            for (int b = TT == 128 ? 3 : 1; b >= 0; --b) {
-              if (q.width - m >= 16 << b) {
-                tma_load_2d(tok + m * 128, &a_maps.rows[b], kb * 128, q.row0 + m, &full_bar[slot]);
-                m += 16 << b;
-              }
-            }
-          }
-          if (C::APS && !C::SCALE_WARPS) {
-            const long long step = MODE == kMXFP8 ? static_cast<long long>(q.tile) * ((s.KB + 3) / 4) + kb / 4
-                                                  : static_cast<long long>(q.tile) * s.KB + kb;
-            bulk_g2s(st + kSlabBytes + C::TOK_BYTES + C::SFW_BYTES, p.a_sf + step * C::SFT_BYTES, C::SFT_BYTES,
-                     &full_bar[slot]);
-          }
+          if (!GATHER) tma_load_2d(tok, &a_maps.rows[q.width > 16 ? 1 : 0], kb * 128, q.row0, &full_bar[slot]);
         }
         __syncwarp();
         if (GATHER) {
@@ -305,8 +285,8 @@ __global__ void __launch_bounds__(GCfg<MODE, TT>::THREADS, GCfg<MODE, TT>::BLOCK
     for (int i = 0; ok && i < shares; ++i) {
       const Share h = share_at(s, i);
       const Unit q = unit_at<TT>(s, h.u);
-      const int acc = i % C::ACCS;
-      ok = __all_sync(0xffffffffu, mbar_wait(&acce_bar[acc], ((i / C::ACCS) & 1) ^ 1u, T, p.err, 63));
+      const int acc = i & 1;
+      ok = __all_sync(0xffffffffu, mbar_wait(&acce_bar[acc], ((i >> 1) & 1) ^ 1u, T, p.err, 63));
       if (!ok) break;
       tc_fence_after();
       const uint32_t d = tmem + acc * TT;
@@ -316,8 +296,8 @@ __global__ void __launch_bounds__(GCfg<MODE, TT>::THREADS, GCfg<MODE, TT>::BLOCK
         if (!ok) break;
         tc_fence_after();
         const uint32_t st = smem_u32(smem) + slot * C::STAGE_BYTES;
-        const uint32_t sfw = tmem + C::ACC_COLS + slot * (C::SFW_COLS + C::SFT_COLS);
-        const uint32_t sft = sfw + C::SFW_COLS;
+        const uint32_t sfw = tmem + C::ACC_COLS + slot * 2 * C::SF_COLS;
+        const uint32_t sft = sfw + C::SF_COLS;
         if (elect_one()) {
           if (C::APS) {
             const uint32_t sw = st + kSlabBytes + C::TOK_BYTES;
@@ -325,17 +305,13 @@ __global__ void __launch_bounds__(GCfg<MODE, TT>::THREADS, GCfg<MODE, TT>::BLOCK
 #pragma unroll
             for (int g = 0; g < C::APS; ++g) {
               tc_cp_32x128b_warpx4(sfw + 4 * g, sdesc_plain_rows16(sw + 512 * g));
-#pragma unroll
-              for (int a = 0; a < C::TOK_ATOMS; ++a)
-                if (a == 0 || q.width > a * 128)
-                  tc_cp_32x128b_warpx4(sft + 4 * (g * C::TOK_ATOMS + a),
-                                       sdesc_plain_rows16(stk + 512 * (g * C::TOK_ATOMS + a)));
+              tc_cp_32x128b_warpx4(sft + 4 * g, sdesc_plain_rows16(stk + 512 * g));
             }
           }
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             mma_step<MODE>(d, sdesc_sw128(st + j * 32), sdesc_sw128(st + kSlabBytes + j * 32), q.width, j, kb, sfw, sft,
-                           C::TOK_ATOMS, (kb > h.k0 || j > 0) ? 1u : 0u);
+                           (kb > h.k0 || j > 0) ? 1u : 0u);
           tc_commit(&empty_bar[slot]);
         }
         __syncwarp();
@@ -356,9 +332,11 @@ __global__ void __launch_bounds__(GCfg<MODE, TT>::THREADS, GCfg<MODE, TT>::BLOCK
     }
   } else if (warp < 4) {
     // ----------------------------------------------------- token scale atoms
-    if (C::SCALE_WARPS) {
-      constexpr int PT = (TT + 63) / 64;  // rows of the tile per thread
-      const int st_id = threadIdx.x - 64;
+    if (C::APS) {
+      // thread (warp - 2, lane): row lane of the tile; the two warps share the
+      // slab's atoms (mxfp4) or one of them only arrives
+      const int g = warp - 2;
+      const bool mine = g < C::APS;
       const uint8_t* asf = static_cast<const uint8_t*>(p.a_scales);
       const int cols = MODE == kMXFP8 ? p.K / 128 : p.K / 32;
       const bool words = (reinterpret_cast<uintptr_t>(asf) & 3u) == 0;
@@ -367,50 +345,26 @@ __global__ void __launch_bounds__(GCfg<MODE, TT>::THREADS, GCfg<MODE, TT>::BLOCK
       for (int i = 0; ok && i < shares; ++i) {
         const Share h = share_at(s, i);
         const Unit q = unit_at<TT>(s, h.u);
-        const uint8_t* src[PT];
-#pragma unroll
-        for (int j = 0; j < PT; ++j) {
-          const int m = st_id + 64 * j;
-          int row = q.row0 + min(m, q.count - 1);
-          if (GATHER) row = min(max(__ldg(p.rows + row), 0), p.T - 1);
-          src[j] = asf + static_cast<size_t>(row) * cols;
-        }
-        // the four E8M0 bytes of atom g of K step kb
-        auto word = [&](int j, int kb, int g) -> uint32_t {
-          if (MODE == kMXFP8) return static_cast<uint32_t>(__ldg(src[j] + kb)) * 0x01010101u;
-          const uint8_t* b = src[j] + (kb * C::APS + g) * 4;
+        int row = q.row0 + min(lane, q.count - 1);
+        if (GATHER && mine) row = min(max(__ldg(p.rows + row), 0), p.T - 1);
+        const uint8_t* src = asf + static_cast<size_t>(row) * cols;
+        // the four E8M0 bytes of this warp's atom at K step kb
+        auto word = [&](int kb) -> uint32_t {
+          if (!mine) return 0u;
+          if (MODE == kMXFP8) return static_cast<uint32_t>(__ldg(src + kb)) * 0x01010101u;
+          const uint8_t* b = src + (kb * C::APS + g) * 4;
           if (words) return __ldg(reinterpret_cast<const uint32_t*>(b));
           return b[0] | (static_cast<uint32_t>(b[1]) << 8) | (static_cast<uint32_t>(b[2]) << 16) |
                  (static_cast<uint32_t>(b[3]) << 24);
         };
-        uint32_t next[PT][C::APS ? C::APS : 1];
-        auto fetch = [&](int kb) {
-#pragma unroll
-          for (int j = 0; j < PT; ++j)
-#pragma unroll
-            for (int g = 0; g < C::APS; ++g)
-              if (st_id + 64 * j < q.width) next[j][g] = word(j, kb, g);
-        };
-        fetch(h.k0);
+        uint32_t next = word(h.k0);
         for (int kb = h.k0; kb < h.k1; ++kb, ++it) {
           const int slot = it % ST;
-          const bool w = mbar_wait(&empty_bar[slot], ((it / ST) & 1) ^ 1u, T, p.err, 66);
-          if (!__all_sync(0xffffffffu, w)) {
-            ok = false;
-            break;
-          }
+          ok = __all_sync(0xffffffffu, mbar_wait(&empty_bar[slot], ((it / ST) & 1) ^ 1u, T, p.err, 66));
+          if (!ok) break;
           uint8_t* sft = smem + slot * C::STAGE_BYTES + kSlabBytes + C::TOK_BYTES + C::SFW_BYTES;
-#pragma unroll
-          for (int j = 0; j < PT; ++j) {
-            const int m = st_id + 64 * j;
-            if (m < q.width) {
-#pragma unroll
-              for (int g = 0; g < C::APS; ++g)
-                *reinterpret_cast<uint32_t*>(sft + (g * C::TOK_ATOMS + (m >> 7)) * 512 + (m & 31) * 16 +
-                                             ((m & 127) >> 5) * 4) = next[j][g];
-            }
-          }
-          if (kb + 1 < h.k1) fetch(kb + 1);
+          if (mine) *reinterpret_cast<uint32_t*>(sft + g * 512 + lane * 16) = next;
+          if (kb + 1 < h.k1) next = word(kb + 1);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&full_bar[slot]);
@@ -421,40 +375,35 @@ __global__ void __launch_bounds__(GCfg<MODE, TT>::THREADS, GCfg<MODE, TT>::BLOCK
   } else {
     // -------------------------------------------------------------- results
     const int qd = warp & 3;
-    const int half = (warp - 4) >> 2;  // TT >= 128: which half of the columns
-    constexpr int COLS = TT == 32 ? 32 : TT / 2;  // columns (rows of Y) per warp
     const float scale = MODE == kTensor ? __ldg(static_cast<const float*>(p.a_scales)) * __ldg(p.b_s) : 1.f;
     bool ok = true;
     for (int i = 0; i < shares; ++i) {
       const Share h = share_at(s, i);
       const Unit q = unit_at<TT>(s, h.u);
-      const int acc = i % C::ACCS;
+      const int acc = i & 1;
       // a warp that gave up waits for nothing more, but still meets the others
       // at the barriers of the shared units
       if (ok) {
-        const bool w = mbar_wait(&accf_bar[acc], (i / C::ACCS) & 1, T, p.err, 67);
+        const bool w = mbar_wait(&accf_bar[acc], (i >> 1) & 1, T, p.err, 67);
         ok = __all_sync(0xffffffffu, w);
         if (!ok && lane == 0) abort_sh = 1;
       }
-      const bool shared_unit = CUT && (h.k0 > 0 || h.k1 < s.KB);  // of a cut line
+      const bool shared_unit = h.k0 > 0 || h.k1 < s.KB;  // of a cut line
       if (!ok) {
         if (shared_unit) {
-          bar_sync_named(1, 32 * C::EPI_WARPS);
-          bar_sync_named(1, 32 * C::EPI_WARPS);
+          bar_sync_named(1, 128);
+          bar_sync_named(1, 128);
         }
         continue;
       }
       tc_fence_after();
-      uint32_t v[COLS];
-      const uint32_t taddr = tmem + acc * TT + half * COLS + (static_cast<uint32_t>(qd * 32) << 16);
-#pragma unroll
-      for (int c = 0; c < COLS; c += 32) tmem_ld32(taddr + c, *reinterpret_cast<uint32_t(*)[32]>(&v[c]));
+      uint32_t v[TT];
+      tmem_ld32(tmem + acc * TT + (static_cast<uint32_t>(qd * 32) << 16), v);
       tmem_wait_ld();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&acce_bar[acc]);
       const int n = qd * 32 + lane;  // row of the weight tile
-      const int m0 = half * COLS;
       if (shared_unit) {
         // a shared unit: leave the partial, and let the last to arrive add up
         const long long first = h.u * s.KB;
@@ -464,9 +413,9 @@ __global__ void __launch_bounds__(GCfg<MODE, TT>::THREADS, GCfg<MODE, TT>::BLOCK
         // that begins with the unit and ends inside it is its last, slot 1
         float* mine = p.part + (2 * static_cast<size_t>(s.c) + (h.k0 > 0 ? 0 : 1)) * tile;
 #pragma unroll
-        for (int m = 0; m < COLS; ++m)
+        for (int m = 0; m < TT; ++m)
           if (m < q.count) __stcg(mine + m * 128 + n, __uint_as_float(v[m]));
-        bar_sync_named(1, 32 * C::EPI_WARPS);
+        bar_sync_named(1, 128);
         if (threadIdx.x == 128) last_sh = 0;
         if (threadIdx.x == 128 && *reinterpret_cast<volatile int*>(&abort_sh) == 0) {
           // Tickets hold the call's tag and the arrivals; a word of another
@@ -486,22 +435,29 @@ __global__ void __launch_bounds__(GCfg<MODE, TT>::THREADS, GCfg<MODE, TT>::BLOCK
           __threadfence();
           last_sh = arrived == c1 - c0;
         }
-        bar_sync_named(1, 32 * C::EPI_WARPS);
+        bar_sync_named(1, 128);
         const bool last = last_sh != 0;
         if (!last) continue;
+        // in the order of K; a partial's rows are all on their way before the
+        // first is added
+        const float* part = p.part + (2 * static_cast<size_t>(c0) + 1) * tile + n;
 #pragma unroll
-        for (int m = 0; m < COLS; ++m) {
-          if (m < q.count) {
-            float sum = __ldcg(p.part + (2 * static_cast<size_t>(c0) + 1) * tile + m * 128 + n);
-            for (int c = c0 + 1; c <= c1; ++c) sum += __ldcg(p.part + 2 * static_cast<size_t>(c) * tile + m * 128 + n);
-            v[m] = __float_as_uint(sum);
-          }
+        for (int m = 0; m < TT; ++m)
+          if (m < q.count) v[m] = __float_as_uint(__ldcg(part + m * 128));
+#pragma unroll 1
+        for (int c = c0 + 1; c <= c1; ++c) {
+          part = p.part + 2 * static_cast<size_t>(c) * tile + n;
+          float w[TT];
+#pragma unroll
+          for (int m = 0; m < TT; ++m) w[m] = m < q.count ? __ldcg(part + m * 128) : 0.f;
+#pragma unroll
+          for (int m = 0; m < TT; ++m) v[m] = __float_as_uint(__uint_as_float(v[m]) + w[m]);
         }
       }
-      __nv_bfloat16* out = p.y + static_cast<size_t>(q.row0 + m0) * p.N + q.nt * 128 + n;
+      __nv_bfloat16* out = p.y + static_cast<size_t>(q.row0) * p.N + q.nt * 128 + n;
 #pragma unroll
-      for (int m = 0; m < COLS; ++m)
-        if (m0 + m < q.count) out[static_cast<size_t>(m) * p.N] = __float2bfloat16_rn(__uint_as_float(v[m]) * scale);
+      for (int m = 0; m < TT; ++m)
+        if (m < q.count) out[static_cast<size_t>(m) * p.N] = __float2bfloat16_rn(__uint_as_float(v[m]) * scale);
     }
   }
 
@@ -517,7 +473,7 @@ __global__ void __launch_bounds__(GCfg<MODE, TT>::THREADS, GCfg<MODE, TT>::BLOCK
   if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
 }
 
-// What TT >= 128 lays out first: the gathered rows of A (a_rows) and the token
+// What TT = 256 lays out first: the gathered rows of A (a_rows) and the token
 // scale atoms (a_sf), each where wanted.
 struct PrepParams {
   const uint8_t* a;
@@ -535,7 +491,6 @@ struct PrepParams {
 
 constexpr int kPrepRows = 4;  // rows a copying block has in flight, 64 threads each
 
-template <int TT>
 __global__ void __launch_bounds__(256) grouped_prep_kernel(const PrepParams p) {
   extern __shared__ int sched_sh[];
   pdl_wait();
@@ -559,10 +514,10 @@ __global__ void __launch_bounds__(256) grouped_prep_kernel(const PrepParams p) {
     }
     return;
   }
-  constexpr int BLOCKS = TT / 128;  // 128-row blocks of a tile
+  constexpr int BLOCKS = 2;  // 128-row blocks of a tile
   int* offs = sched_sh;
   int* tiles = sched_sh + p.E + 1;
-  read_offsets<TT>(p.offsets, p.R, p.E, offs, tiles);
+  read_offsets<256>(p.offsets, p.R, p.E, offs, tiles);
   Schedule s;
   s.offs = offs;
   s.tiles = tiles;
@@ -578,7 +533,7 @@ __global__ void __launch_bounds__(256) grouped_prep_kernel(const PrepParams p) {
     const int line = static_cast<int>(i & 31), blk = static_cast<int>(i >> 5) % BLOCKS;
     const int64_t tq = (i >> 5) / BLOCKS;
     const int tile = static_cast<int>(tq / quads), quad = static_cast<int>(tq - static_cast<int64_t>(tile) * quads);
-    const Unit q = unit_at<TT>(s, tile);
+    const Unit q = unit_at<256>(s, tile);
     if (blk * 128 >= q.width) continue;
     uint32_t w[4][4];  // [block of 32 rows][atom]
 #pragma unroll
@@ -610,16 +565,16 @@ __global__ void __launch_bounds__(256) grouped_prep_kernel(const PrepParams p) {
   }
 }
 
-template <int MODE, int TT, bool GATHER>
+template <int MODE, bool GATHER>
 cudaError_t launch_one(const AMaps& a_maps, const CUtensorMap& tmap_b, const GroupedParams& p, int blocks,
                        cudaStream_t stream) {
-  using C = GCfg<MODE, TT>;
-  auto* kernel = &grouped_kernel<MODE, TT, GATHER>;
+  using C = GCfg<MODE>;
+  auto* kernel = &grouped_kernel<MODE, GATHER>;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), C::smem(kMaxExperts));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(blocks);
-  cfg.blockDim = dim3(C::THREADS);
+  cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::smem(p.E);
   cfg.stream = stream;
   cudaLaunchAttribute attr;
@@ -631,19 +586,17 @@ cudaError_t launch_one(const AMaps& a_maps, const CUtensorMap& tmap_b, const Gro
 }
 
 template <int MODE>
-cudaError_t launch_mode(const AMaps& a_maps, const CUtensorMap& tmap_b, const GroupedParams& p, int tt, int blocks,
+cudaError_t launch_mode(const AMaps& a_maps, const CUtensorMap& tmap_b, const GroupedParams& p, int blocks,
                         cudaStream_t stream) {
-  if (tt == 32)
-    return p.rows ? launch_one<MODE, 32, true>(a_maps, tmap_b, p, blocks, stream)
-                  : launch_one<MODE, 32, false>(a_maps, tmap_b, p, blocks, stream);
-  return launch_one<MODE, 128, false>(a_maps, tmap_b, p, blocks, stream);
+  return p.rows ? launch_one<MODE, true>(a_maps, tmap_b, p, blocks, stream)
+                : launch_one<MODE, false>(a_maps, tmap_b, p, blocks, stream);
 }
 
-cudaError_t launch_prep(PrepParams p, int tt, int64_t tiles, cudaStream_t stream) {
+cudaError_t launch_prep(PrepParams p, int64_t tiles, cudaStream_t stream) {
   // blocks in proportion to the work, at most eight an SM for each part
   const int64_t most = 8 * static_cast<int64_t>(sm_count());
   const int64_t rows = p.a_rows ? (p.R + kPrepRows - 1) / kPrepRows : 0;
-  const int64_t lines = p.a_sf ? (tiles * ((p.NA + 3) / 4) * (tt / 4) + 255) / 256 : 0;
+  const int64_t lines = p.a_sf ? (tiles * ((p.NA + 3) / 4) * 64 + 255) / 256 : 0;
   p.copy_blocks = static_cast<int>(rows < most ? rows : most);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.copy_blocks + (lines < most ? lines : most)));
@@ -655,12 +608,11 @@ cudaError_t launch_prep(PrepParams p, int tt, int64_t tiles, cudaStream_t stream
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = pdl_enabled() ? 1 : 0;
-  return tt == 128 ? cudaLaunchKernelEx(&cfg, grouped_prep_kernel<128>, p)
-                   : cudaLaunchKernelEx(&cfg, grouped_prep_kernel<256>, p);
+  return cudaLaunchKernelEx(&cfg, grouped_prep_kernel, p);
 }
 
-// Token tile, blocks (two for each pair of SMs) and workspace of a call: partials and tickets (tt 32), or
-// scale atoms and gathered rows (tt 128 and 256), in this order.
+// Token tile, blocks (two for each pair of SMs) and workspace of a call: partials
+// and tickets (tt 32), or scale atoms and gathered rows (tt 256), in this order.
 struct GroupedPlan {
   int tt, blocks;
   int64_t tiles;  // no more token tiles than this, however the rows fall
@@ -674,15 +626,23 @@ GroupedPlan grouped_plan(int mode, int64_t R, int64_t E, int64_t N, int64_t K, b
   memset(&g, 0, sizeof g);
   if (R == 0) return g;
   const int64_t KB = row_bytes(mode, K) / 128;
-  // Rows an expert on average decide the tile.  Measured (64 experts, 4096 x
-  // 7168, mxfp8): 16 rows an expert 326 us with tt 32 (experts above 32 rows
-  // read their weights again) and 289 with 128; 64 rows 311 us with 128 (six
-  // stages) and 338 with 256; 128 rows 402 and 381.  At 8 rows tt 32 and 128
-  // are equal; below, the layout kernel and idle blocks cost more.
-  g.tt = R <= 8 * E ? 32 : (R <= 80 * E ? 128 : 256);
-  const int64_t most = g.tt == 32 ? 2 * static_cast<int64_t>(sm_count()) : (g.tt == 128 ? sm_count() : grouped_pair_clusters());
-  g.tiles = R / g.tt + (E < R ? E : R);
-  const int64_t units = g.tiles * (g.tt == 256 ? (N / 128 + 1) / 2 : N / 128);
+  // Token tiles of 32 rows or pairs of SMs with tiles of 256.  By the rows of an
+  // expert on average (64 experts, 4096 x 7168, mxfp8): at 16 rows 326 us with 32
+  // (experts above 32 rows read their weights again) and 290 on pairs; at 8 the
+  // two are equal, and below that pairs idle.  But pairs share no unit, so a
+  // call with few units leaves SMs without work, and the layout kernel before
+  // them takes 3 us: where the rows times weight tiles are few, and so are the
+  // units or the K steps, the cut line of 32-row tiles is faster up to about
+  // rows x pairs of weight tiles = 8000 (8 experts of 512 x 7168: 25 rows each
+  // 20 us against 26, 100 rows 22 against 30; bf16 38 rows 26 against 43; 4 of 1024
+  // x 7168 mxfp4, 250 rows: 20 against 22; 16 of 128 x 2048, 375 rows: 10 against
+  // 18; 8 of 2048 x 7168, 15 rows: 31 and 31; 2048 x 1024 mxfp4: 8 against 12).
+  const int64_t wpairs = (N / 128 + 1) / 2, active = E < R ? E : R;
+  const bool few = R * wpairs < 8000 && (active * wpairs < 48 || KB <= 8);
+  g.tt = R <= 8 * E || few ? 32 : 256;
+  g.tiles = R / g.tt + active;
+  const int64_t units = g.tiles * (g.tt == 256 ? wpairs : N / 128);
+  const int64_t most = g.tt == 32 ? kBlocksPerSm * static_cast<int64_t>(sm_count()) : grouped_pair_clusters();
   const int64_t want = g.tt == 32 ? (units * KB + kMinSlabs - 1) / kMinSlabs : units;
   g.blocks = static_cast<int>(want < most ? want : most) * (g.tt == 256 ? 2 : 1);
   if (g.tt == 32) {
@@ -691,7 +651,7 @@ GroupedPlan grouped_plan(int mode, int64_t R, int64_t E, int64_t N, int64_t K, b
   } else {
     if (is_mx(mode)) {
       g.atoms = static_cast<int>((mx_sf_cols(mode, K) + 3) / 4);
-      g.sf_bytes = static_cast<uint64_t>(g.tiles) * g.atoms * (g.tt / 128) * 512;
+      g.sf_bytes = static_cast<uint64_t>(g.tiles) * g.atoms * 1024;
     }
     if (gather) g.rows_bytes = static_cast<uint64_t>(R) * row_bytes(mode, K);
   }
@@ -796,7 +756,7 @@ fg_status fg_grouped_gemm(const void* A, const void* a_scales, int64_t T, const 
     PrepParams q{static_cast<const uint8_t*>(A), static_cast<const uint8_t*>(a_scales), offsets, rows, a_rows,
                  g.sf_bytes ? ws : nullptr, p.T, p.R, E, static_cast<int>(rb),
                  is_mx(mode) ? static_cast<int>(mx_sf_cols(mode, K)) : 0, g.atoms, 0};
-    if ((e = launch_prep(q, g.tt, g.tiles, st)) != cudaSuccess) return cuda_fail(e, "grouped product's layout launch");
+    if ((e = launch_prep(q, g.tiles, st)) != cudaSuccess) return cuda_fail(e, "grouped product's layout launch");
   }
   if (g.tt == 256) {
     if (g.blocks == 0) return fail(FG_ERR_CUDA, "%s: no room for a pair of SMs", what);
@@ -813,12 +773,12 @@ fg_status fg_grouped_gemm(const void* A, const void* a_scales, int64_t T, const 
     return e == cudaSuccess ? FG_OK : cuda_fail(e, "grouped product launch");
   }
   switch (mode) {
-    case FG_BF16: e = launch_mode<kBF16>(a_maps, tmap_b, p, g.tt, g.blocks, st); break;
-    case FG_FP8_TENSOR: e = launch_mode<kTensor>(a_maps, tmap_b, p, g.tt, g.blocks, st); break;
-    case FG_MXFP8: e = launch_mode<kMXFP8>(a_maps, tmap_b, p, g.tt, g.blocks, st); break;
-    case FG_MXFP4: e = launch_mode<kMXFP4>(a_maps, tmap_b, p, g.tt, g.blocks, st); break;
-    case FG_MXFP8_B32: e = launch_mode<kMXFP8B32>(a_maps, tmap_b, p, g.tt, g.blocks, st); break;
-    case FG_MXFP4_FP8A: e = launch_mode<kMXFP4FP8A>(a_maps, tmap_b, p, g.tt, g.blocks, st); break;
+    case FG_BF16: e = launch_mode<kBF16>(a_maps, tmap_b, p, g.blocks, st); break;
+    case FG_FP8_TENSOR: e = launch_mode<kTensor>(a_maps, tmap_b, p, g.blocks, st); break;
+    case FG_MXFP8: e = launch_mode<kMXFP8>(a_maps, tmap_b, p, g.blocks, st); break;
+    case FG_MXFP4: e = launch_mode<kMXFP4>(a_maps, tmap_b, p, g.blocks, st); break;
+    case FG_MXFP8_B32: e = launch_mode<kMXFP8B32>(a_maps, tmap_b, p, g.blocks, st); break;
+    case FG_MXFP4_FP8A: e = launch_mode<kMXFP4FP8A>(a_maps, tmap_b, p, g.blocks, st); break;
   }
   return e == cudaSuccess ? FG_OK : cuda_fail(e, "grouped product launch");
 }

@@ -22,7 +22,7 @@ struct GroupedParams {
   const int32_t* offsets;     // [E + 1]
   const int32_t* rows;        // [R] or null
   __nv_bfloat16* y;           // [R][N]
-  const uint8_t* a_sf;        // TT >= 128, MX: token scale atoms [tile][K step][atom][128-row block][512]
+  const uint8_t* a_sf;        // TT = 256, MX: token scale atoms [tile][K step][atom][128-row block][512]
   float* part;                // [blocks][2][TT][128] partials (cut line)
   unsigned long long* tickets;  // [blocks] arrivals at the unit that begins last in the block
   unsigned long long epoch;
@@ -33,9 +33,9 @@ struct GroupedParams {
 };
 
 // A as rows of bytes: boxes of 128 bytes x 16, 32, 64, 128 rows, so that a tile
-// of up to 256 rows takes few copies and moves only its own rows (a copy costs
-// its issuing thread tens of cycles: 16 boxes of 16 rows a K step held the
-// whole kernel back).  TT = 32 uses the first; GATHER: 1 row.
+// takes few copies and moves only its own rows (a copy costs its issuing warp
+// tens of cycles: 16 boxes of 16 rows a K step held the whole kernel back).  TT
+// = 32 uses the first two; with gathered rows the first, 1 row high.
 struct AMaps {
   CUtensorMap rows[4];
 };
