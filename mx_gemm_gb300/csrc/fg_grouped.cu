@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     bool ok = true;
     for (int i = 0; ok && i < shares; ++i) {
       const Share h = share_at(s, i);
-      const Unit q = unit_at<TT>(s, h.u);
+      const Unit q = uniform(unit_at<TT>(s, h.u));
       const long long wt = static_cast<long long>(q.e) * s.NT + q.nt;  // weight tile of the stacked image
       // rows that are copied; the accumulator's columns past them hold what
       // the rows of an earlier step left and are not stored
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     int it = 0;
     for (int i = 0; ok && i < shares; ++i) {
       const Share h = share_at(s, i);
-      const Unit q = unit_at<TT>(s, h.u);
+      const Unit q = uniform(unit_at<TT>(s, h.u));
       const int acc = i & 1;
       ok = __all_sync(0xffffffffu, mbar_wait(&acce_bar[acc], ((i >> 1) & 1) ^ 1u, T, p.err, 63));
       if (!ok) break;
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       bool ok = true;
       for (int i = 0; ok && i < shares; ++i) {
         const Share h = share_at(s, i);
-        const Unit q = unit_at<TT>(s, h.u);
+        const Unit q = uniform(unit_at<TT>(s, h.u));
         int row = q.row0 + min(lane, q.count - 1);
         if (GATHER && mine) row = min(max(__ldg(p.rows + row), 0), p.T - 1);
         const uint8_t* src = asf + static_cast<size_t>(row) * cols;
@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     bool ok = true;
     for (int i = 0; i < shares; ++i) {
       const Share h = share_at(s, i);
-      const Unit q = unit_at<TT>(s, h.u);
+      const Unit q = uniform(unit_at<TT>(s, h.u));
       const int acc = i & 1;
       // a warp that gave up waits for nothing more, but still meets the others
       // at the barriers of the shared units
@@ -728,8 +728,8 @@ fg_status fg_grouped_gemm(const void* A, const void* a_scales, int64_t T, const 
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   uint8_t* a_rows = g.rows_bytes ? ws + g.sf_bytes : nullptr;  // A's rows in the order of Y's
   const bool indexed = rows && !a_rows;
-  for (int i = 0; i < (indexed ? 1 : (g.tt == 32 ? 2 : 4)); ++i)
-    if ((s = make_tmap(&a_maps.rows[i], a_rows ? a_rows : A, a_rows ? R : T, rb, indexed ? 1 : 16u << i)) != FG_OK) return s;
+  for (int i = 0; i < (indexed ? 1 : (g.tt == 32 ? 2 : 8)); ++i)
+    if ((s = make_tmap(&a_maps.rows[i], a_rows ? a_rows : A, a_rows ? R : T, rb, indexed ? 1 : 16u * (i + 1))) != FG_OK) return s;
   if (mode == FG_MXFP4_FP8A && (s = make_tmap_fp4w(&tmap_b, b->data, b->N, K)) != FG_OK) return s;
   p.b_img = static_cast<const uint8_t*>(b->data);
   p.b_sf = static_cast<const uint8_t*>(b->sf);

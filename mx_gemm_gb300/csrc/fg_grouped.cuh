@@ -32,12 +32,13 @@ struct GroupedParams {
   int debug_stall;
 };
 
-// A as rows of bytes: boxes of 128 bytes x 16, 32, 64, 128 rows, so that a tile
-// takes few copies and moves only its own rows (a copy costs its issuing warp
-// tens of cycles: 16 boxes of 16 rows a K step held the whole kernel back).  TT
-// = 32 uses the first two; with gathered rows the first, 1 row high.
+// A as rows of bytes: boxes of 128 bytes x 16, 32, 48 .. 128 rows, so that a
+// tile, or an SM's half of a pair's, is one copy of just its rows (a copy costs
+// its issuing warp tens of cycles: 16 boxes of 16 rows a K step held the whole
+// kernel back).  Tiles of 32 rows use the first two; with gathered rows the
+// first, 1 row high.
 struct AMaps {
-  CUtensorMap rows[4];
+  CUtensorMap rows[8];
 };
 
 // The unit's rows and weight tile.
@@ -75,6 +76,18 @@ __device__ __forceinline__ Unit unit_at(const Schedule& s, long long u) {
   q.row0 = s.offs[a] + m * per;
   q.count = min(per, rows - m * per);
   q.width = (q.count + STEP - 1) / STEP * STEP;
+  return q;
+}
+
+// The unit, known to the compiler as the same in all lanes: what copies and MMAs
+// are issued with then stays in uniform registers.
+__device__ __forceinline__ Unit uniform(Unit q) {
+  q.e = __shfl_sync(0xffffffffu, q.e, 0);
+  q.row0 = __shfl_sync(0xffffffffu, q.row0, 0);
+  q.count = __shfl_sync(0xffffffffu, q.count, 0);
+  q.nt = __shfl_sync(0xffffffffu, q.nt, 0);
+  q.width = __shfl_sync(0xffffffffu, q.width, 0);
+  q.tile = __shfl_sync(0xffffffffu, q.tile, 0);
   return q;
 }
 

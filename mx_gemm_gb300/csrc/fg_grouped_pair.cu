@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     tmem_relinquish_pair();
   }
   if (warp == 0 && lane == 0) {
-    for (int i = 0; i < 4; ++i) prefetch_tmap(&a_maps.rows[i]);
+    for (int i = 0; i < 8; ++i) prefetch_tmap(&a_maps.rows[i]);
     prefetch_tmap(&tmap_w);
     if (C::APS) {
       prefetch_tmap(&tmap_wsf);
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   s.units = static_cast<long long>(tiles_sh[p.E]) * s.NT;
   const int pair = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
   const int shares = pair < s.units ? static_cast<int>((s.units - pair + pairs - 1) / pairs) : 0;
-  auto unit = [&](int i) { return unit_at<TT>(s, pair + static_cast<long long>(i) * pairs); };
+  auto unit = [&](int i) { return uniform(unit_at<TT>(s, pair + static_cast<long long>(i) * pairs)); };
   // bytes that one SM's copies of a stage of unit q count
   auto stage_tx = [&](const Unit& q) {
     return static_cast<uint32_t>(C::W_TX + q.width * 64 + C::SFW_BYTES + C::SFT_BYTES);
@@ -150,6 +150,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const Unit q = unit(i);
       const int wt = q.e * wtiles + min(2 * q.nt + rank, wtiles - 1);  // this SM's tile of the stacked image
       const int half = q.width >> 1, row0 = q.row0 + rank * half;      // its rows of the token tile
+      const CUtensorMap* a_map = &a_maps.rows[half / 16 - 1];
       for (int kb = 0; kb < s.KB; ++kb, ++it) {
         const int slot = it % ST;
         ok = __all_sync(0xffffffffu, mbar_wait(&empty_bar[slot], ((it / ST) & 1) ^ 1u, T, p.err, 71));
@@ -163,14 +164,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           else
             tma_load_2d_pair(st, &tmap_w, 0, (wt * s.KB + kb) * 8, fb);
           uint8_t* tok = st + kSlabBytes;
-          int m = 0;
-#pragma unroll
-          for (int b = 3; b >= 0; --b) {
-            if (half - m >= 16 << b) {
-              tma_load_2d_pair(tok + m * 128, &a_maps.rows[b], kb * 128, row0 + m, fb);
-              m += 16 << b;
-            }
-          }
+          tma_load_2d_pair(tok, a_map, kb * 128, row0, fb);
           if (C::APS) {
             const int watom = MODE == kMXFP8 ? wt * ((s.KB + 3) / 4) + kb / 4 : (wt * s.KB + kb) * C::APS;
             const int tatom = MODE == kMXFP8 ? q.tile * ((s.KB + 3) / 4) + kb / 4 : (q.tile * s.KB + kb) * C::APS;
@@ -284,7 +278,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const int hi = L > P ? L : P;
       for (int it = consumed_sh; it < hi; ++it) {
         const int slot = it % ST;
-        const uint32_t tx = stage_tx(unit(it / s.KB));
+        const uint32_t tx = stage_tx(unit_at<TT>(s, pair + static_cast<long long>(it / s.KB) * pairs));
         if (it >= L)
           mbar_arrive_expect_tx(&full_bar[slot], tx);  // only the odd SM issued this stage: arm it for its bytes
         else if (it >= P)
