@@ -24,6 +24,7 @@
 
 #include "fg_grouped.cuh"
 #include "fg_ptx.cuh"
+#include "fg_tiles.cuh"
 
 namespace fg {
 
@@ -44,8 +45,9 @@ struct PCfg {
   static constexpr int STAGE_RAW = kSlabBytes + TOK_BYTES + SFW_BYTES + SFT_BYTES;
   static constexpr int STAGE_BYTES = (STAGE_RAW + 1023) / 1024 * 1024;
   static constexpr int SFW_COLS = APS * 4, SFT_COLS = APS * 8;
-  static constexpr int smem(int E) { return STAGES * STAGE_BYTES + 1024 + 8 * (E + 1); }
-  static_assert(STAGES * STAGE_BYTES + 1024 + 8 * (kMaxExperts + 1) <= 232448 - 1024, "shared memory budget");
+  static constexpr int OUT_BYTES = 8 * 512;  // per result warp: 8 rows of Y x 32 columns
+  static constexpr int smem(int E) { return STAGES * STAGE_BYTES + OUT_BYTES + 1024 + 8 * (E + 1); }
+  static_assert(STAGES * STAGE_BYTES + OUT_BYTES + 1024 + 8 * (kMaxExperts + 1) <= 232448 - 1024, "shared memory budget");
   static_assert(TT + STAGES * (SFW_COLS + SFT_COLS) <= kTmemCols, "TMEM budget");
 };
 
@@ -82,7 +84,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   __shared__ __align__(8) uint64_t accf_bar, acce_bar, stall_bar, drain_bar;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh, issued_sh, consumed_sh;
-  int* offs_sh = reinterpret_cast<int*>(smem + ST * C::STAGE_BYTES);
+  int* offs_sh = reinterpret_cast<int*>(smem + ST * C::STAGE_BYTES + C::OUT_BYTES);
   int* tiles_sh = offs_sh + p.E + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -236,6 +238,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     // -------------------------------------------------- results (both SMs)
     const int qd = warp & 3;
     const int m0 = ((warp - 2) >> 2) * 128;  // this warp's half of the tile's rows
+    uint8_t* stg_ptr = smem + ST * C::STAGE_BYTES + (warp - 2) * 512;
+    const uint32_t stg = smem_u32(stg_ptr);
     const float scale = MODE == kTensor ? __ldg(static_cast<const float*>(p.a_scales)) * __ldg(p.b_s) : 1.f;
     for (int i = 0; i < shares; ++i) {
       const Unit q = unit(i);
@@ -245,20 +249,36 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         break;
       }
       tc_fence_after();
+      // v[64 h + 32 c + ..]: lanes 16 h .. 16 h + 15 (weight rows), columns 64 c .. (tokens)
       uint32_t v[128];
       const uint32_t taddr = tmem + m0 + (static_cast<uint32_t>(qd * 32) << 16);
 #pragma unroll
-      for (int c = 0; c < 128; c += 32) tmem_ld32(taddr + c, *reinterpret_cast<uint32_t(*)[32]>(&v[c]));
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) tmem_ld_frag64(taddr + 64 * c + (static_cast<uint32_t>(16 * h) << 16), &v[64 * h + 32 * c]);
       tmem_wait_ld();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_remote(&acce_bar, 0);  // the pair's next tile may overwrite the accumulator
       const int nt = 2 * q.nt + rank;
-      if (nt < wtiles) {
-        __nv_bfloat16* out = p.y + static_cast<size_t>(q.row0 + m0) * p.N + nt * 128 + qd * 32 + lane;
+      if (nt >= wtiles) continue;
+      // Eight rows of Y at a time: the fragments go through shared memory
+      // transposed, 64 bytes a row (16-byte piece i of row j at i ^ (j / 2 % 4)),
+      // and leave as 16-byte stores.  (Storing each lane's weight row two bytes
+      // at a time took 9000 cycles a tile, longer than the MMAs of K = 2048.)
+      __nv_bfloat16* out = p.y + static_cast<size_t>(q.row0 + m0 + (lane >> 2)) * p.N + nt * 128 + qd * 32 + (lane & 3) * 8;
+      const uint32_t put = stg + (lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
+      const uint4* get = reinterpret_cast<const uint4*>(stg_ptr + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4));
 #pragma unroll
-        for (int m = 0; m < 128; ++m)
-          if (m0 + m < q.count) out[static_cast<size_t>(m) * p.N] = __float2bfloat16_rn(__uint_as_float(v[m]) * scale);
+      for (int b = 0; b < 16; ++b) {
+        if (m0 + 8 * b >= q.count) break;
+        const int k = 32 * (b >> 3) + 4 * (b & 7);
+        auto pack = [&](int x) { return pack_bf16x2(__uint_as_float(v[x]) * scale, __uint_as_float(v[x + 1]) * scale); };
+        stmatrix4_trans(put, pack(k), pack(k + 2), pack(64 + k), pack(64 + k + 2));
+        __syncwarp();
+        const uint4 o = *get;
+        __syncwarp();
+        if (m0 + 8 * b + (lane >> 2) < q.count) *reinterpret_cast<uint4*>(out + static_cast<size_t>(8 * b) * p.N) = o;
       }
     }
   }
