@@ -183,15 +183,16 @@ def _row_bytes_of(t):
 
 def _check_gemm_args(mode, A, pb, a_scales, Y):
     dev = pb.data.device
+    K = pb.K
     _require(A, "A", _a_dtypes(mode), dev)
     M = A.shape[0] if A.dim() == 2 else -1
-    if A.dim() != 2 or _row_bytes_of(A) != _a_row_bytes(mode, pb.K):
+    if A.dim() != 2 or _row_bytes_of(A) != _a_row_bytes(mode, K):
         raise ValueError("A must be [M][K] codes of the mode (%d bytes per row for K=%d), got shape %s dtype %s"
-                         % (_a_row_bytes(mode, pb.K), pb.K, tuple(A.shape), A.dtype))
+                         % (_a_row_bytes(mode, K), K, tuple(A.shape), A.dtype))
     # a missing scale tensor or a mode that differs from the weight's is the
     # library's to report (FG_ERR_INVALID_ARG / FG_ERR_LAYOUT)
     if a_scales is not None and mode == pb.mode and mode != FG_BF16:
-        dts, n = _scale_spec(mode, M, pb.K, False)
+        dts, n = _scale_spec(mode, M, K, False)
         _require(a_scales, "a_scales", dts, dev, numel=n)
     if Y is not None:
         _require(Y, "Y", _dtypes("bfloat16", "int16"), dev, shape=(M, pb.N))
