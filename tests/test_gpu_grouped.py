@@ -225,3 +225,70 @@ def test_a_wait_that_runs_out_is_reported(total):
         fg.set_wait_timeout_ns(4_000_000_000)
     assert torch.equal(c.run(), want)
     assert fg.get_error() == fg.FG_OK
+
+
+@pytest.mark.parametrize("gather", [True, False])
+def test_outputs_past_32_bits_of_elements(gather):
+    """Y beyond element 2^31: the first and last rows against the reference."""
+    total, experts, n, k = 540_000, 8, 4096, 256
+    c = Experts("mxfp8_b32", [total // experts] * experts, n, k, 21, gather_from=500 if gather else None)
+    y = c.run()
+    b = values(c.b, c.b_s, c.bm)
+    for rows, e in ((slice(0, 40), 0), (slice(total - 40, total), experts - 1)):
+        at = c.rows[rows].long() if gather else torch.arange(total, device="cuda")[rows]
+        mine = values(c.a.view(torch.uint8)[at].view(c.a.dtype), c.a_s.view(torch.uint8)[at], c.am)
+        assert_close(y[rows], mine @ b[e * n:(e + 1) * n].T, rows)
+
+
+@pytest.mark.parametrize("total", [24, 1200])
+def test_another_stream(total):
+    c = Experts("mxfp8_b32", [total // 8] * 8, 512, 4096, 17, gather_from=16)
+    want = c.run()
+    other = torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    got = [c.run(stream=other) for _ in range(3)]
+    junk = [torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda") for _ in range(8)]  # would reuse a freed workspace
+    torch.cuda.current_stream().wait_stream(other)
+    assert all(torch.equal(y, want) for y in got) and len(junk) == 8
+
+
+@pytest.mark.parametrize("total", [24, 1200])
+def test_units_and_tiles_do_not_change_a_row(total):
+    """A row's bits are the same whatever expert counts surround it, in either form."""
+    c = Experts("mxfp8_b32", [total // 8] * 8, 256, 1024, 18)
+    first = c.run()
+    # the same rows of expert 3, alone
+    lo, hi = 3 * (total // 8), 4 * (total // 8)
+    one = torch.zeros(9, dtype=torch.int32, device="cuda")
+    one[4:] = hi - lo
+    y = fg.grouped_gemm(c.a[lo:hi].contiguous(), c.pb, one, c.a_s[lo:hi].contiguous())
+    diff = (y.double() - first[lo:hi].double()).abs()
+    assert (diff <= 2.0 ** -7 * first[lo:hi].double().abs() + 1e-3 * first.double().pow(2).mean().sqrt()).all()
+
+
+@pytest.mark.parametrize("edit,text", [
+    (dict(offsets="long"), "offsets"), (dict(offsets="few"), "divisor"), (dict(a="float"), "A has dtype"), (dict(a="wide"), "A must be"),
+    (dict(rows="long"), "rows"), (dict(scales="short"), "a_scales"), (dict(scales="float"), "a_scales"), (dict(Y="shape"), "Y has"),
+    (dict(Y="float"), "Y has"), (dict(workspace="host"), "workspace"),
+])
+def test_binding_refusals(edit, text):
+    c = Experts("mxfp8_b32", [4, 4, 4], 128, 256, 19, gather_from=12)
+    kw = dict(A=c.a, pb=c.pb, offsets=c.offsets, a_scales=c.a_s, rows=c.rows)
+    what, how = next(iter(edit.items()))
+    kw.update({("offsets", "long"): dict(offsets=c.offsets.long()), ("offsets", "few"): dict(offsets=torch.zeros(6, dtype=torch.int32, device="cuda")),
+               ("a", "float"): dict(A=c.a.float()), ("a", "wide"): dict(A=c.a[:, :128].contiguous()), ("rows", "long"): dict(rows=c.rows.long()),
+               ("scales", "short"): dict(a_scales=c.a_s[:5].contiguous()), ("scales", "float"): dict(a_scales=c.a_s.float()),
+               ("Y", "shape"): dict(Y=torch.empty(12, 256, dtype=torch.bfloat16, device="cuda")),
+               ("Y", "float"): dict(Y=torch.empty(12, 128, device="cuda")), ("workspace", "host"): dict(workspace=torch.empty(8))}[(what, how)])
+    with pytest.raises(ValueError, match=text):
+        fg.grouped_gemm(**kw)
+
+
+def test_library_refusals_come_as_errors():
+    c = Experts("mxfp8_b32", [4, 4, 4], 128, 256, 20)
+    with pytest.raises(fg.FgError) as e:
+        c.run(workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == fg.FG_ERR_WORKSPACE
+    with pytest.raises(fg.FgError) as e:
+        c.run(flags=1)
+    assert e.value.status == fg.FG_ERR_INVALID_ARG

@@ -135,3 +135,46 @@ def test_combine_nan_rows_of_dropped_choices_stay_out():
     slots = torch.full((3, 2), -1, dtype=torch.int32, device="cuda")
     weights = torch.full((3, 2), float("nan"), device="cuda")
     assert (fg.moe_combine(y, slots, weights) == 0).all()
+
+
+def test_combine_past_32_bits_of_elements():
+    """Rows of Y beyond element 2^31: the first and last tokens against the formula."""
+    n, r = 8192, 270_000                    # 2.2e9 elements
+    y = torch.empty(r, n, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    edge = torch.randn(64, n, generator=g, device="cuda").to(torch.bfloat16)
+    y[:32], y[-32:] = edge[:32], edge[32:]
+    slots = torch.cat([torch.arange(32), torch.arange(r - 32, r)]).int().cuda().view(32, 2)
+    weights = torch.rand(32, 2, generator=g, device="cuda")
+    want, size = combine_reference(edge, torch.arange(64, device="cuda").int().view(32, 2), weights, None)
+    assert ((fg.moe_combine(y, slots, weights).double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -20 * size).all()
+
+
+@pytest.mark.parametrize("call,text", [
+    (lambda x, i: fg.moe_route(x, 0), "top_k"),
+    (lambda x, i: fg.moe_route(x, 9), "top_k"),
+    (lambda x, i: fg.moe_route(x.t(), 2), "contiguous rows"),
+    (lambda x, i: fg.moe_route(x.double(), 2), "dtype"),
+    (lambda x, i: fg.moe_route(x[0], 2), "2-D"),
+    (lambda x, i: fg.moe_route(x.expand(4, 8)[:, :1].expand(4, 8), 2), "rows"),
+    (lambda x, i: fg.moe_combine(x, i, x), "dtype"),
+    (lambda x, i: fg.moe_combine(x.to(torch.bfloat16), x, x), "dtype"),
+    (lambda x, i: fg.moe_combine(x.to(torch.bfloat16), i, x[:, :3].contiguous()), "shape"),
+    (lambda x, i: fg.moe_combine(x.to(torch.bfloat16), i.t(), x), "contiguous"),
+    (lambda x, i: fg.moe_combine(x.to(torch.bfloat16), i, x, residual=x.to(torch.bfloat16)[:2]), "residual"),
+])
+def test_binding_refusals(call, text):
+    x = torch.zeros(4, 8, device="cuda")
+    i = torch.zeros(4, 8, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match=text):
+        call(x, i)
+
+
+def test_library_refusals_come_as_errors():
+    with pytest.raises(fg.FgError) as e:
+        fg.moe_route(torch.zeros(2, 2000, device="cuda"), 2)      # more experts than it takes
+    assert e.value.status == fg.FG_ERR_SHAPE and "1024" in str(e.value)
+    with pytest.raises(fg.FgError) as e:
+        fg.moe_combine(torch.zeros(2, 12, dtype=torch.bfloat16, device="cuda"),
+                       torch.zeros(1, 1, dtype=torch.int32, device="cuda"), torch.zeros(1, 1, device="cuda"))
+    assert e.value.status == fg.FG_ERR_SHAPE

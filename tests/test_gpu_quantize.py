@@ -228,3 +228,48 @@ def test_empty_and_other_stream():
     got = fg.quantize("mxfp8_b32", x, stream=other)
     torch.cuda.current_stream().wait_stream(other)
     assert all(np.array_equal(code_bytes(a), b) for a, b in zip(got, want))
+
+
+def test_rows_past_32_bits_of_elements():
+    m, k = 270_000, 8192
+    x = torch.zeros(m, k, dtype=torch.bfloat16, device="cuda")
+    edge = rows_of(16, k, torch.bfloat16, 5)
+    x[:8], x[-8:] = edge[:8].cuda(), edge[8:].cuda()
+    codes, scales = fg.quantize("mxfp8_b32", x)
+    v, s = reference(edge.double().numpy(), "mxfp8_b32")
+    take = torch.cat([torch.arange(8), torch.arange(m - 8, m)]).cuda()
+    got = codes.view(torch.uint8)[take].view(torch.float8_e4m3fn)
+    assert np.array_equal(decoded(got, "mxfp8_b32"), v)
+    assert np.array_equal(scales.view(torch.uint8)[take].cpu().numpy(), s)
+    del codes, scales
+    w = torch.ones(k, dtype=torch.bfloat16, device="cuda")
+    x[-1] = 2.0
+    _, _, _, y = fg.rmsnorm_quantize("bf16", x, w)
+    assert ((y[-1].float() - 1).abs() < 2.0 ** -7).all() and (y[m // 2] == 0).all()
+
+
+@pytest.mark.parametrize("call,text", [
+    (lambda x: fg.quantize("mxfp8_b32", x.t()), "contiguous rows"),
+    (lambda x: fg.quantize("mxfp8_b32", x.half()), "dtype"),
+    (lambda x: fg.quantize("mxfp8_b32", x[0]), "2-D"),
+    (lambda x: fg.quantize("mxfp8_b32", x[:, :255], act="swiglu"), "halves"),
+    (lambda x: fg.quantize("mxfp8_b32", x[:1].expand(4, 256)), "overlapping"),
+    (lambda x: fg.rmsnorm_quantize("mxfp8_b32", x, x[0, :128]), "weight"),
+    (lambda x: fg.rmsnorm_quantize("mxfp8_b32", x, x[0].float()), "weight"),
+    (lambda x: fg.rmsnorm_quantize("mxfp8_b32", x, x[0], residual=x[:2]), "residual"),
+    (lambda x: fg.rmsnorm_quantize("mxfp8_b32", x, x[0], residual=x.float()), "residual"),
+    (lambda x: fg.rmsnorm_quantize("mxfp8_b32", x, x[0], eps="a"), "eps"),
+])
+def test_binding_refusals(call, text):
+    with pytest.raises(ValueError, match=text):
+        call(torch.zeros(4, 256, dtype=torch.bfloat16, device="cuda"))
+
+
+def test_library_refusals_come_as_errors():
+    x = torch.zeros(4, 264, dtype=torch.bfloat16, device="cuda")
+    for call, status in ((lambda: fg.quantize("mxfp8_b32", x), fg.FG_ERR_SHAPE),              # not whole blocks
+                         (lambda: fg.quantize("fp8_tensor", x[:, :256]), fg.FG_ERR_INVALID_ARG),
+                         (lambda: fg.quantize("mxfp8_b32", x[:, 1:257]), fg.FG_ERR_ALIGN)):    # rows 2 bytes off
+        with pytest.raises(fg.FgError) as e:
+            call()
+        assert e.value.status == status
