@@ -71,7 +71,7 @@ def _link_binding(obj):
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = BINDING + ".tmp.%d" % os.getpid()
     _run(["g++", "-shared", "-o", tmp, obj, "-L" + OUT, "-l:libfg.so", "-Wl,-rpath,$ORIGIN", "-L" + libs, "-ltorch_python",
-          "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda"], "link of fg_torch.so")
+          "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-lc10", "-lc10_cuda"], "link of fg_torch.so")
     os.replace(tmp, BINDING)
 
 

@@ -9,7 +9,7 @@
 // FgError for a status of the C ABI, and torch's own for the allocations.
 #include <Python.h>
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -142,8 +142,9 @@ int type_of(const at::Tensor& t, const char* name) {
 
 // ------------------------------------------------- outputs and the stream
 
+// What torch.empty ends in for a CUDA device, without the dispatch before it.
 at::Tensor make(at::IntArrayRef sizes, at::ScalarType type, const at::Device& device) {
-  return at::empty(sizes, at::TensorOptions().dtype(type).device(device));
+  return at::detail::empty_cuda(sizes, type, device, std::nullopt);
 }
 
 PyObject* wrap(const at::Tensor& t) {
