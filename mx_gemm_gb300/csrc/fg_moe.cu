@@ -58,11 +58,10 @@ template <>
 struct Key<float> {
   using Word = unsigned long long;  // key, complement of the expert
   static __device__ __forceinline__ Word make(uint32_t bits, int e) {
-    const float l = __uint_as_float(bits);
-    if (!(l > -INFINITY)) return 0ull;
-    const uint32_t u = __float_as_uint(l + 0.f);  // -0 becomes +0
-    const uint32_t k = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-    return (static_cast<Word>(k) << 32) | static_cast<uint32_t>(~e);
+    const float l = __uint_as_float(bits) + 0.f;  // -0 becomes +0
+    const int32_t u = __float_as_int(l);
+    const uint32_t k = static_cast<uint32_t>(u ^ ((u >> 31) | 0x80000000));  // negative: complement; else: sign set
+    return l > -INFINITY ? (static_cast<Word>(k) << 32) | static_cast<uint32_t>(~e) : 0ull;
   }
   static __device__ __forceinline__ Word largest(Word w) {
     const uint32_t hi = static_cast<uint32_t>(w >> 32);
@@ -81,10 +80,10 @@ template <>
 struct Key<__nv_bfloat16> {
   using Word = uint32_t;  // key in the upper half, complement of the expert in the lower
   static __device__ __forceinline__ Word make(uint32_t bits, int e) {
-    const uint32_t u = bits == 0x8000u ? 0u : bits;
-    const uint32_t k = (u & 0x8000u) ? (u ^ 0xffffu) : (u | 0x8000u);
-    // 0x7f: -infinity, below it and above 0xff80 (infinity): NaN
-    return k > 0x7fu && k <= 0xff80u ? (k << 16) | (0xffffu - e) : 0u;
+    const float l = __uint_as_float(bits << 16) + 0.f;  // -0 becomes +0
+    const int32_t u = __float_as_int(l);
+    const uint32_t k = static_cast<uint32_t>(u ^ ((u >> 31) | 0x80000000));  // negative: complement; else: sign set
+    return l > -INFINITY ? (k & 0xffff0000u) | (0xffffu - e) : 0u;
   }
   static __device__ __forceinline__ Word largest(Word w) { return __reduce_max_sync(0xffffffffu, w); }
   static __device__ __forceinline__ int expert(Word w) { return 0xffff - static_cast<int>(w & 0xffffu); }
@@ -186,21 +185,20 @@ __device__ __forceinline__ void pick(const RouteParams& p, const Logits<T, VPL>&
   } else {
     look();
   }
-  typename K::Word mine = 0, first = 0;
+  const typename K::Word first = K::largest(head);
   float sum = 0.f;
-  for (int j = 0; j < p.k; ++j) {
-    const typename K::Word m = K::largest(head);
-    if (m == 0) break;  // no logit is left
-    if (j == 0) {
-      first = m;
-      if (!p.renormalize) {  // over all experts, before any key is taken away
+  if (!p.renormalize) {  // over all experts, before any key is taken away
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) sum += key[i] ? exp_below(K::logit(key[i]), K::logit(m)) : 0.f;
+    for (int i = 0; i < VPL; ++i) sum += key[i] ? exp_below(K::logit(key[i]), K::logit(first)) : 0.f;
 #pragma unroll
-        for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-      }
-    }
+    for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  }
+  // the lane whose head was taken moves up; once none is left m stays 0
+  typename K::Word mine = 0, m = first;
+#pragma unroll 2
+  for (int j = 0;;) {
     if (lane == j) mine = m;
+    if (++j >= p.k) break;
     if (head == m) {  // one lane: experts differ
       if constexpr (SORTED) {
 #pragma unroll
@@ -213,6 +211,7 @@ __device__ __forceinline__ void pick(const RouteParams& p, const Logits<T, VPL>&
         look();
       }
     }
+    m = K::largest(head);
   }
   expert = mine ? K::expert(mine) : -1;
   weight = mine ? exp_below(K::logit(mine), K::logit(first)) : 0.f;
@@ -259,7 +258,7 @@ __device__ __forceinline__ void scatter_pairs(const RouteParams& p, const uint32
     if (e < 0) continue;
     const int32_t slot = static_cast<int32_t>(base[e]) + p.slots[i];
     p.slots[i] = slot;
-    p.rows[slot] = static_cast<int32_t>(i / p.k);
+    p.rows[slot] = static_cast<int32_t>(static_cast<uint32_t>(i) / static_cast<uint32_t>(p.k));  // i < 2^30
   }
 }
 
@@ -318,13 +317,10 @@ __global__ void __launch_bounds__(route_threads(VPL)) route_kernel(const RoutePa
         const int e = expert[h];
         int32_t rank = -1;
         if (e >= 0) {
-          rank = static_cast<int32_t>(count[e]);
+          // the expert's pairs of earlier groups, of earlier words, and before i in its own
+          rank = static_cast<int32_t>(count[e]) + __popc(mask[i >> 5][e] & ((1u << (i & 31)) - 1u));
 #pragma unroll
-          for (int w = 0; w < kGroup / 32; ++w) {
-            const int below = i - 32 * w;  // tokens of this word before i
-            const uint32_t m = below >= 32 ? ~0u : (below <= 0 ? 0u : (1u << below) - 1u);
-            rank += __popc(mask[w][e] & m);
-          }
+          for (int w = 0; w + 1 < kGroup / 32; ++w) rank += i >= 32 * (w + 1) ? __popc(mask[w][e]) : 0;
         }
         p.slots[(t0 + i) * p.k + lane] = rank;
       }
