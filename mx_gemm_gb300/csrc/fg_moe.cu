@@ -194,24 +194,36 @@ __device__ __forceinline__ void pick(const RouteParams& p, const Logits<T, VPL>&
     for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
   }
   // the lane whose head was taken moves up; once none is left m stays 0
-  typename K::Word mine = 0, m = first;
-#pragma unroll 2
-  for (int j = 0;;) {
-    if (lane == j) mine = m;
-    if (++j >= p.k) break;
-    if (head == m) {  // one lane: experts differ
-      if constexpr (SORTED) {
+  typename K::Word mine = lane == 0 ? first : 0, m = first;
+  if (SORTED && p.k <= 8) {
+    // written out: a step needs no more of the sorted keys than choices are left
 #pragma unroll
-        for (int i = 0; i + 1 < VPL; ++i) key[i] = key[i + 1];
-        key[VPL - 1] = 0;
-        head = key[0];
-      } else {
+    for (int j = 1; j < 8; ++j) {
+      if (j >= p.k) break;
+      const bool taken = key[0] == m;  // one lane: experts differ
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) key[i] = key[i] == m ? 0 : key[i];
-        look();
-      }
+      for (int i = 0; i < 8 - j && i < VPL; ++i) key[i] = taken ? (i + 1 < VPL ? key[i + 1 < VPL ? i + 1 : 0] : 0) : key[i];
+      m = K::largest(key[0]);
+      mine = lane == j ? m : mine;
     }
-    m = K::largest(head);
+  } else {
+#pragma unroll 1
+    for (int j = 1; j < p.k; ++j) {
+      if (head == m) {
+        if constexpr (SORTED) {
+#pragma unroll
+          for (int i = 0; i + 1 < VPL; ++i) key[i] = key[i + 1];
+          key[VPL - 1] = 0;
+          head = key[0];
+        } else {
+#pragma unroll
+          for (int i = 0; i < VPL; ++i) key[i] = key[i] == m ? 0 : key[i];
+          look();
+        }
+      }
+      m = K::largest(head);
+      mine = lane == j ? m : mine;
+    }
   }
   expert = mine ? K::expert(mine) : -1;
   weight = mine ? exp_below(K::logit(mine), K::logit(first)) : 0.f;
