@@ -108,7 +108,7 @@ def _mode(mode):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()  # (the void* argument types take it as it is)
 
 
 # ----------------------------------------------------------- argument checks
@@ -128,16 +128,20 @@ _E8M0 = _BYTES + _dtypes("float8_e8m0fnu")
 _F32 = (torch.float32,)
 
 
+_A_DTYPES = {FG_BF16: _BF16, FG_MXFP4: _FP4}
+_B_DTYPES = {FG_BF16: _BF16, FG_MXFP4: _FP4, FG_MXFP4_FP8A: _FP4}
+
+
 def _a_dtypes(mode):
-    return {FG_BF16: _BF16, FG_MXFP4: _FP4}.get(mode, _FP8)
+    return _A_DTYPES.get(mode, _FP8)
 
 
 def _b_dtypes(mode):
-    return {FG_BF16: _BF16, FG_MXFP4: _FP4, FG_MXFP4_FP8A: _FP4}.get(mode, _FP8)
+    return _B_DTYPES.get(mode, _FP8)
 
 
 def _a_row_bytes(mode, K):
-    return {FG_BF16: 2 * K, FG_MXFP4: K // 2}.get(mode, K)
+    return 2 * K if mode == FG_BF16 else (K // 2 if mode == FG_MXFP4 else K)
 
 
 def _b_row_bytes(mode, K):
@@ -201,10 +205,10 @@ def _check_gemm_args(mode, A, pb, a_scales, Y):
 
 def _stream(stream):
     if stream is None:  # (without making a Stream object, which takes 3 us)
-        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
-        return ctypes.c_void_p(stream.cuda_stream)
-    return ctypes.c_void_p(int(stream))
+        return stream.cuda_stream
+    return int(stream)
 
 
 def set_wait_timeout_ns(ns):
@@ -311,13 +315,14 @@ def gemm(A, pb, a_scales=None, mode=None, split_k=0, Y=None, workspace=None, fla
     """
     mode = pb.mode if mode is None else _mode(mode)
     M = _check_gemm_args(mode, A, pb, a_scales, Y)
+    N = pb.N
     if Y is None:
-        Y = torch.empty((M, pb.N), dtype=torch.bfloat16, device=A.device)
+        Y = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
     if workspace is not None:
         _require(workspace, "workspace", device=A.device)
     ws_bytes = 0
     if workspace is None:
-        need = gemm_workspace_size(mode, M, pb.N, pb.K, split_k) if M > 0 else 0
+        need = gemm_workspace_size(mode, M, N, pb.K, split_k) if M > 0 else 0
         if need:
             workspace = torch.empty(need // 4, dtype=torch.float32, device=A.device)
     if workspace is not None:

@@ -29,7 +29,11 @@
 //    the blocks, wherever the cuts fall, so that all SMs stream to the end.
 //    Blocks that share a unit leave fp32 partials in the workspace; the last to
 //    arrive adds them in the order of K (the same bits each time) and stores.
-//    Nobody waits for another block.
+//    Nobody waits for another block.  Measured, 4096 x 7168 of 64 experts, one
+//    token x 8: mxfp8 40 us, fp8 x fp4 27, mxfp4 25, where the bytes alone take 35,
+//    18 and 18: 4 us before the first K step (offsets, row indexes, the first
+//    bytes) and 4 between one call's last store and the next one's start.  61
+//    tokens, 7168 x 2048: 138 us, 6.5 TB/s by the bytes that HBM moves.
 //
 // Warp roles: 0 copies (weights by bulk copy, tokens by tensor copy: boxes of
 // 16 rows, or four rows at a time by their index where rows are gathered);

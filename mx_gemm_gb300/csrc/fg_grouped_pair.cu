@@ -1,14 +1,21 @@
 // Products grouped by expert on pairs of SMs: token tiles of up to 256 rows
-// (TT = 256) against two weight tiles at a time.  Schedule and layouts as in
-// fg_grouped.cu.
+// against two weight tiles at a time.  Schedule and layouts as in fg_grouped.cu.
 //
 // Why pairs.  One SM's tile of 128 weight rows x n tokens moves, per K step,
 // 16 KB of weights and n * 128 bytes of tokens into shared memory and the MMA
 // reads both again: at n = 208 that is 86 KB through a 128-byte port, 670
 // cycles, while the tensor core needs 410.  On a pair the tokens are staged
 // half by each SM and the hardware hands each half to both (cta_group::2), so
-// an SM moves 58 KB: 450 cycles.  Measured, 32768 mxfp4 rows of 64 experts, 4096
-// x 7168: see the table of fg_grouped.cu's design.
+// an SM moves 58 KB: 450 cycles.  Measured, 64 experts, 4096 x 7168, 32768 rows:
+// mxfp4 438 us one-SM, 332 now (5.8 PFLOP/s); 32-K mxfp8 795, 640 (3.0); fp8 x fp4
+// 749, 595; bf16 (32 experts, 16384 rows) 725, 596 (1.6, at the power limit).  A
+// step takes 520 (bf16) to 640 (mxfp4) cycles, the tensor pipe busy for 430 of
+// them; the rest is the issue of the scale copies and the barriers.  With 64 rows
+// an expert the weights' bytes bound it: mxfp8 301 us, 6.65 TB/s.
+//
+// Tried and dropped: tiles of 192 rows with two accumulators (mxfp4 436 us: more
+// steps of the same length), a second copying warp (no faster), prefetches of the
+// weights to L2 (356 -> 393 us), asking for the next barrier a step ahead (equal).
 //
 // The even SM's warp 1 issues the MMAs (256 weight rows x n tokens; rows
 // 0..127 accumulate in the even SM's tensor memory, 128..255 in the odd one's);

