@@ -313,6 +313,12 @@ def gemm(A, pb, a_scales=None, mode=None, split_k=0, Y=None, workspace=None, fla
     [M][K/2]).  A workspace is allocated here when the resolved split needs
     one and none is given.  Returns Y.
     """
+    if mode is None and Y is None and workspace is None and flags == 0 and stream is None:
+        # the ordinary call, compiled; None where an argument is amiss, which
+        # the checks below name
+        Y = (moe._binding or moe.binding()).gemm(A, pb.data, ctypes.addressof(pb.desc), a_scales, split_k)
+        if Y is not None:
+            return Y
     mode = pb.mode if mode is None else _mode(mode)
     M = _check_gemm_args(mode, A, pb, a_scales, Y)
     N = pb.N
@@ -360,5 +366,6 @@ def gemm_splitk_reduce(ws, split_k, M, N, a_s=None, b_s=None, Y=None, stream=Non
     return Y
 
 
+from . import moe  # noqa: E402
 from .moe import (FG_ACT_NONE, FG_ACT_SWIGLU, FG_TYPE_BF16, FG_TYPE_F32, Routing, grouped_gemm,  # noqa: E402,F401
                   grouped_gemm_workspace_size, moe_combine, moe_route, quantize, rmsnorm_quantize)

@@ -1,6 +1,6 @@
-// Python binding of the operators around the GEMM (mx_gemm_gb300/moe.py): the
-// checks of their tensors, their outputs' allocation, and the call of the C
-// ABI.  A call of theirs on one token keeps the GPU busy for 2 to 5 us, while
+// Python binding of the operators around the GEMM (mx_gemm_gb300/moe.py) and of
+// the GEMM's ordinary call: the checks of their tensors, their outputs'
+// allocation, and the call of the C ABI.  A call of theirs on one token keeps the GPU busy for 2 to 5 us, while
 // allocating each output from Python takes 1.5 us and a ctypes call of fifteen
 // arguments as much again (routing: 17 us a call that way); from here the same
 // steps cost a third of it.
@@ -418,6 +418,57 @@ PyObject* moe_combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// fg_gemm's ordinary call, (A, weight data, descriptor's address, a_scales or
+// None, split_k) -> Y; None where an argument is not as it should be or needs
+// more than this, which the caller's own checks then name.
+PyObject* gemm(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    arity(n, 5, "gemm");
+    if (!THPVariable_Check(v[0]) || !THPVariable_Check(v[1]) || !PyLong_Check(v[4])) Py_RETURN_NONE;
+    const at::Tensor &A = THPVariable_Unpack(v[0]), &weight = THPVariable_Unpack(v[1]);
+    const fg_bshuf* b = reinterpret_cast<const fg_bshuf*>(static_cast<intptr_t>(integer(v[2], "the descriptor's address")));
+    const int mode = b->mode;
+    const int64_t K = b->K;
+    const at::Device device = weight.device();
+    const at::ScalarType type = A.scalar_type();
+    const int64_t row = mode == FG_BF16 ? 2 * K : (mode == FG_MXFP4 ? K / 2 : K);
+    const bool codes = mode == FG_BF16 ? type == at::kBFloat16 || type == at::kShort || type == at::kUInt16
+                                       : is_bytes(type) || type == (mode == FG_MXFP4 ? at::kFloat4_e2m1fn_x2 : at::kFloat8_e4m3fn);
+    if (!weight.is_cuda() || device.index() != c10::cuda::current_device() || A.device() != device || !A.is_contiguous() ||
+        A.dim() != 2 || A.size(0) == 0 || !codes || A.size(1) * (int64_t)A.element_size() != row)
+      Py_RETURN_NONE;
+    const int64_t M = A.size(0);
+    const void* scales = nullptr;
+    if (mode != FG_BF16) {
+      if (!THPVariable_Check(v[3])) Py_RETURN_NONE;
+      const at::Tensor& s = THPVariable_Unpack(v[3]);
+      const bool fp32 = mode == FG_FP8_TENSOR || mode == FG_FP8_BLOCK128;
+      const int64_t want = mode == FG_FP8_TENSOR ? 1 : M * (K / (mode == FG_MXFP8 || mode == FG_FP8_BLOCK128 ? 128 : 32));
+      const at::ScalarType t = s.scalar_type();
+      if (s.device() != device || !s.is_contiguous() || s.numel() != want ||
+          !(fp32 ? t == at::kFloat : is_bytes(t) || t == at::kFloat8_e8m0fnu))
+        Py_RETURN_NONE;
+      scales = s.data_ptr();
+    } else if (v[3] != Py_None) {
+      Py_RETURN_NONE;
+    }
+    const long split = PyLong_AsLong(v[4]);
+    if (PyErr_Occurred()) return nullptr;
+    if (split < 0 || split > 16) Py_RETURN_NONE;
+    void* st = c10::cuda::getCurrentCUDAStream(device.index()).stream();
+    at::Tensor Y, ws;
+    {
+      Unlocked u;
+      uint64_t need = 0;
+      check(fg_gemm_workspace_size(mode, M, b->N, K, (int)split, &need));
+      Y = make({M, b->N}, at::kBFloat16, device);
+      if (need) ws = make({static_cast<int64_t>(need)}, at::kByte, device);
+      check(fg_gemm(A.data_ptr(), scales, M, b, mode, (int)split, Y.data_ptr(), data(ws), need, 0, st));
+    }
+    return wrap(Y);
+  });
+}
+
 PyObject* set_error(PyObject*, PyObject* cls) {
   Py_INCREF(cls);
   Py_XDECREF(g_error);
@@ -435,6 +486,7 @@ PyMethodDef methods[] = {fast<quantize>("quantize"),
                          fast<moe_route>("moe_route"),
                          fast<grouped_gemm>("grouped_gemm"),
                          fast<moe_combine>("moe_combine"),
+                         fast<gemm>("gemm"),
                          {"set_error", set_error, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 
