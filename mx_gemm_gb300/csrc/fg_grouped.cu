@@ -53,7 +53,7 @@ namespace fg {
 namespace {
 
 constexpr int kMinSlabs = 4;    // K steps a block of the cut line takes at least
-constexpr int kShareSteps = 8;  // see the schedule
+constexpr int kShareSteps = 12;  // see the schedule
 
 constexpr int TT = 32;           // rows of a token tile
 constexpr int kThreads = 256;    // copies, MMAs, two warps of scales, four of results
@@ -197,16 +197,17 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
   s.W = s.units * s.KB;
   s.c = blockIdx.x;
   s.blocks = gridDim.x;
-  // Sharing units costs a round of partials at the end, about as long as
-  // kShareSteps K steps of every block.  Units stay whole where dealing them
-  // out leaves less than that idle, and where there is at most one for each
-  // block but enough of them to keep the memory busy (a block alone has 64 KB
-  // in flight).  256 units on 304 blocks, K = 7168: 26.9 us whole, 30.6 cut (fp8
-  // x fp4), 40.3 and 45.6 (mxfp8).
+  // Whole units or a cut line?  Full rounds of whole units keep the memory
+  // busy.  The units that remain take s.KB steps of a lone block's pace, which
+  // kBusy blocks need to fill the memory; shared evenly they would take rem /
+  // kBusy of that, plus the round of partials at the end, as long as kShareSteps
+  // steps.  256 units on 304 blocks, K = 7168: 26.9 us whole, 30.6 cut (fp8 x fp4),
+  // 40.3 and 45.6 (mxfp8); 105 units, 32 steps, mxfp8: 16 and 20; 112 units, 20 steps,
+  // mxfp4: 12 and 18; 112 units of 25 rows, 56 steps, mxfp8: 27 and 22.
   {
-    const long long G = gridDim.x, rounds = (s.units + G - 1) / G;
-    const bool one_each = s.units <= G && 10 * s.units >= 6 * G;
-    s.cut = !(one_each || (rounds * G - s.units) * s.KB <= kShareSteps * G);
+    constexpr int kBusy = MODE == kMXFP4FP8A ? 216 : 137;
+    const int rem = static_cast<int>(s.units % gridDim.x);
+    s.cut = rem > 0 && rem < kBusy && static_cast<long long>(s.KB) * (kBusy - rem) > kShareSteps * kBusy;
   }
   if (s.cut) {
     const long long most = (s.W + kMinSlabs - 1) / kMinSlabs;
@@ -242,13 +243,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
           bulk_g2s(st + kSlabBytes + C::TOK_BYTES, p.b_sf + atom * 512, C::SFW_BYTES, &full_bar[slot]);
         }
       };
-      // gathered: this lane's four rows; rows past the tile's end repeat its
-      // last one, indexes are clamped into A
-      int idx[4];
-      if (GATHER) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) idx[j] = __ldg(p.rows + q.row0 + min(lane * 4 + j, q.count - 1));
-      }
+      // gathered: the row of A for this lane's row of the tile; rows past the
+      // tile's end repeat its last one, indexes are clamped into A
+      int idx = 0;
+      if (GATHER) idx = __ldg(p.rows + q.row0 + min(lane, q.count - 1));
       // the first stages are empty: their weights go out while the row indexes come
       const int early = GATHER && i == 0 ? min(ST, h.k1 - h.k0) : 0;
       if (early > 0) {
@@ -257,9 +255,14 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         }
         __syncwarp();
       }
+      // ... all of them in every lane, four to a copy
+      int rows4[TT / 4][4];
       if (GATHER) {
+        idx = min(max(idx, 0), p.T - 1);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) idx[j] = min(max(idx[j], 0), p.T - 1);
+        for (int g = 0; g < TT / 4; ++g)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) rows4[g][j] = __shfl_sync(0xffffffffu, idx, 4 * g + j);
       }
       for (int kb = h.k0; kb < h.k1; ++kb, ++it) {
         const int slot = it % ST;
@@ -269,12 +272,15 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         uint8_t* tok = st + kSlabBytes;
         if (elect_one()) {
           if (it >= early) weights(kb, slot);
-          if (!GATHER) tma_load_2d(tok, &a_maps.rows[q.width > 16 ? 1 : 0], kb * 128, q.row0, &full_bar[slot]);
+          if (GATHER) {
+#pragma unroll
+            for (int g = 0; g < TT / 4; ++g)
+              if (4 * g < copied) tma_gather4(tok + g * 512, &a_maps.rows[0], kb * 128, rows4[g], &full_bar[slot]);
+          } else {
+            tma_load_2d(tok, &a_maps.rows[q.width > 16 ? 1 : 0], kb * 128, q.row0, &full_bar[slot]);
+          }
         }
         __syncwarp();
-        if (GATHER) {
-          if (lane * 4 < copied) tma_gather4(tok + lane * 512, &a_maps.rows[0], kb * 128, idx, &full_bar[slot]);
-        }
       }
     }
     if (lane == 0) {
@@ -634,15 +640,15 @@ GroupedPlan grouped_plan(int mode, int64_t R, int64_t E, int64_t N, int64_t K, b
   // expert on average (64 experts, 4096 x 7168, mxfp8): at 16 rows 326 us with 32
   // (experts above 32 rows read their weights again) and 290 on pairs; at 8 the
   // two are equal, and below that pairs idle.  But pairs share no unit, so a
-  // call with few units leaves SMs without work, and the layout kernel before
-  // them takes 3 us: where the rows times weight tiles are few, and so are the
-  // units or the K steps, the cut line of 32-row tiles is faster up to about
-  // rows x pairs of weight tiles = 8000 (8 experts of 512 x 7168: 25 rows each
-  // 20 us against 26, 100 rows 22 against 30; bf16 38 rows 26 against 43; 4 of 1024
-  // x 7168 mxfp4, 250 rows: 20 against 22; 16 of 128 x 2048, 375 rows: 10 against
-  // 18; 8 of 2048 x 7168, 15 rows: 31 and 31; 2048 x 1024 mxfp4: 8 against 12).
+  // call with fewer units than pairs leaves SMs without work, and the layout
+  // kernel before them takes 3 us: there, or where the K steps are few, 32-row
+  // tiles are faster up to about rows x pairs of weight tiles = 8000 (8 experts of
+  // 512 x 7168: 25 rows each 20 us against 26, 100 rows 22 against 30; bf16 38 rows
+  // 26 against 43; 4 of 1024 x 7168 mxfp4, 250 rows: 18 against 22; 16 of 128 x 2048,
+  // 375 rows: 9 against 18; 8 of 2176 x 2048, 34 rows: 13 against 15; 64 of 2304 x
+  // 256, 9 rows, 2 steps: 11 against 19; 8 of 2048 x 7168, 15 rows: 29 and 29).
   const int64_t wpairs = (N / 128 + 1) / 2, active = E < R ? E : R;
-  const bool few = R * wpairs < 8000 && (active * wpairs < 48 || KB <= 8);
+  const bool few = R * wpairs < 8000 && (active * wpairs < grouped_pair_clusters() || KB <= 8);
   g.tt = R <= 8 * E || few ? 32 : 256;
   g.tiles = R / g.tt + active;
   const int64_t units = g.tiles * (g.tt == 256 ? wpairs : N / 128);
