@@ -365,7 +365,8 @@ FG_API fg_status fg_moe_route(const void* logits, int type, int64_t T, int E, in
  *           before offsets[0] and from offsets[E] on are not written.
  *  workspace  fg_grouped_gemm_workspace_size bytes (gather: rows given); any contents.  Calls that
  *           overlap on the GPU need a workspace each.
- * All modes but FP8_BLOCK128; E <= 1024; R, T <= 2^24.
+ * All modes (FP8_BLOCK128 in 32-row tiles whatever the rows: made for decoding);
+ * E <= 1024; R, T <= 2^24.
  * Errors: INVALID_ARG, SHAPE, ALIGN, LAYOUT, WORKSPACE, UNSUPPORTED_ARCH, CUDA.
  */
 FG_API fg_status fg_grouped_gemm_workspace_size(int mode, int64_t R, int E, int64_t N, int64_t K, int gather,

@@ -73,7 +73,12 @@ struct GCfg {
   static constexpr int STAGE_RAW = kSlabBytes + TOK_BYTES + SFW_BYTES + SFT_BYTES;
   static constexpr int STAGE_BYTES = (STAGE_RAW + 1023) / 1024 * 1024;
   static constexpr int SF_COLS = APS * 4;  // of each operand
-  static constexpr int ACC_COLS = 2 * TT;  // two accumulators
+  // FP8_BLOCK128's fp32 scales cannot be the MMA's: every K step (one scale
+  // block) has an accumulator of its own, four in turn, which the result warps
+  // fold into registers with its scales
+  static constexpr bool FOLD = MODE == kBlock;
+  static constexpr int ACCS = FOLD ? 4 : 2;
+  static constexpr int ACC_COLS = ACCS * TT;
   static constexpr int TMEM_NEED = ACC_COLS + STAGES * 2 * SF_COLS;
   static constexpr int TMEM_COLS = TMEM_NEED <= 64 ? 64 : (TMEM_NEED <= 128 ? 128 : 256);
   // with the schedule of E experts: two blocks an SM up to 500 experts
@@ -119,7 +124,7 @@ __device__ __forceinline__ void mma_step(uint32_t d, uint64_t a, uint64_t b, int
                                          uint32_t sft, uint32_t accum) {
   if (MODE == kBF16) {
     mma_f16(d, a, b, idesc_bf16(128, n), accum);
-  } else if (MODE == kTensor) {
+  } else if (MODE == kTensor || MODE == kBlock) {
     mma_f8f6f4(d, a, b, idesc_e4m3(128, n), accum);
   } else if (MODE == kMXFP8) {
     // the weight's byte of its four-slab atom; the token atoms have the slab's
@@ -145,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
   extern __shared__ uint8_t dsmem[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsmem) + 1023) & ~uintptr_t(1023));
   __shared__ __align__(8) uint64_t full_bar[ST], empty_bar[ST];
-  __shared__ __align__(8) uint64_t accf_bar[2], acce_bar[2];
+  __shared__ __align__(8) uint64_t accf_bar[C::ACCS], acce_bar[C::ACCS];
   __shared__ __align__(8) uint64_t stall_bar, drain_bar;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh, issued_sh, consumed_sh, last_sh;
@@ -160,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       mbar_init(&full_bar[i], C::APS ? 3 : 1);  // + one arrival per scale warp
       mbar_init(&empty_bar[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < C::ACCS; ++i) {
       mbar_init(&accf_bar[i], 1);
       mbar_init(&acce_bar[i], 4);
     }
@@ -295,15 +300,27 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     for (int i = 0; ok && i < shares; ++i) {
       const Share h = share_at(s, i);
       const Unit q = uniform(unit_at<TT>(s, h.u));
+      // accumulators are taken in turn by share, or by K step (FOLD)
       const int acc = i & 1;
-      ok = __all_sync(0xffffffffu, mbar_wait(&acce_bar[acc], ((i >> 1) & 1) ^ 1u, T, p.err, 63));
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t d = tmem + acc * TT;
+      uint32_t d = tmem + acc * TT;
+      if (!C::FOLD) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&acce_bar[acc], ((i >> 1) & 1) ^ 1u, T, p.err, 63));
+        if (!ok) break;
+        tc_fence_after();
+      }
       for (int kb = h.k0; kb < h.k1; ++kb, ++it) {
         const int slot = it % ST;
         ok = __all_sync(0xffffffffu, mbar_wait(&full_bar[slot], (it / ST) & 1, T, p.err, 64));
         if (!ok) break;
+        const int part = it % C::ACCS;
+        if (C::FOLD) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&acce_bar[part], ((it / C::ACCS) & 1) ^ 1u, T, p.err, 63));
+          if (!ok) {
+            ++it;  // this step's copies have landed
+            break;
+          }
+          d = tmem + part * TT;
+        }
         tc_fence_after();
         const uint32_t st = smem_u32(smem) + slot * C::STAGE_BYTES;
         const uint32_t sfw = tmem + C::ACC_COLS + slot * 2 * C::SF_COLS;
@@ -321,14 +338,17 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             mma_step<MODE>(d, sdesc_sw128(st + j * 32), sdesc_sw128(st + kSlabBytes + j * 32), q.width, j, kb, sfw, sft,
-                           (kb > h.k0 || j > 0) ? 1u : 0u);
+                           ((!C::FOLD && kb > h.k0) || j > 0) ? 1u : 0u);
           tc_commit(&empty_bar[slot]);
+          if (C::FOLD) tc_commit(&accf_bar[part]);
         }
         __syncwarp();
       }
       if (!ok) break;
-      if (elect_one()) tc_commit(&accf_bar[acc]);
-      __syncwarp();
+      if (!C::FOLD) {
+        if (elect_one()) tc_commit(&accf_bar[acc]);
+        __syncwarp();
+      }
     }
     if (lane == 0) {
       // a step whose wait gave up was not consumed; the teardown waits for it
@@ -387,32 +407,65 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     const int qd = warp & 3;
     const float scale = MODE == kTensor ? __ldg(static_cast<const float*>(p.a_scales)) * __ldg(p.b_s) : 1.f;
     bool ok = true;
+    int it = 0;  // K steps so far (FOLD)
     for (int i = 0; i < shares; ++i) {
       const Share h = share_at(s, i);
       const Unit q = uniform(unit_at<TT>(s, h.u));
       const int acc = i & 1;
       // a warp that gave up waits for nothing more, but still meets the others
       // at the barriers of the shared units
-      if (ok) {
-        const bool w = mbar_wait(&accf_bar[acc], (i >> 1) & 1, T, p.err, 67);
-        ok = __all_sync(0xffffffffu, w);
-        if (!ok && lane == 0) abort_sh = 1;
-      }
       const bool shared_unit = h.k0 > 0 || h.k1 < s.KB;  // of a cut line
+      uint32_t v[TT];
+      if (C::FOLD) {
+        // lane m has the scales of row m of the tile, all lanes the weight
+        // tile's; each is loaded a step ahead
+        int row = q.row0 + min(lane, q.count - 1);
+        if (GATHER) row = min(max(__ldg(p.rows + row), 0), p.T - 1);
+        const float* as = static_cast<const float*>(p.a_scales) + static_cast<size_t>(row) * s.KB;
+        const float* bs = p.b_s + (static_cast<size_t>(q.e) * s.NT + q.nt) * s.KB;
+        float a_next = ld_nc_f32(as + h.k0), b_next = ld_nc_f32(bs + h.k0);
+        float sum[TT];
+#pragma unroll
+        for (int m = 0; m < TT; ++m) sum[m] = 0.f;
+        for (int kb = h.k0; ok && kb < h.k1; ++kb, ++it) {
+          const float w = a_next * b_next;
+          if (kb + 1 < h.k1) {
+            a_next = ld_nc_f32(as + kb + 1);
+            b_next = ld_nc_f32(bs + kb + 1);
+          }
+          const int part = it % C::ACCS;
+          ok = __all_sync(0xffffffffu, mbar_wait(&accf_bar[part], (it / C::ACCS) & 1, T, p.err, 67));
+          if (!ok) break;
+          tc_fence_after();
+          tmem_ld32(tmem + part * TT + (static_cast<uint32_t>(qd * 32) << 16), v);
+          tmem_wait_ld();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&acce_bar[part]);
+#pragma unroll
+          for (int m = 0; m < TT; ++m) sum[m] = fmaf(__shfl_sync(0xffffffffu, w, m), __uint_as_float(v[m]), sum[m]);
+        }
+#pragma unroll
+        for (int m = 0; m < TT; ++m) v[m] = __float_as_uint(sum[m]);
+      } else if (ok) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&accf_bar[acc], (i >> 1) & 1, T, p.err, 67));
+        if (ok) {
+          tc_fence_after();
+          tmem_ld32(tmem + acc * TT + (static_cast<uint32_t>(qd * 32) << 16), v);
+          tmem_wait_ld();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&acce_bar[acc]);
+        }
+      }
       if (!ok) {
+        if (lane == 0) abort_sh = 1;
         if (shared_unit) {
           bar_sync_named(1, 128);
           bar_sync_named(1, 128);
         }
         continue;
       }
-      tc_fence_after();
-      uint32_t v[TT];
-      tmem_ld32(tmem + acc * TT + (static_cast<uint32_t>(qd * 32) << 16), v);
-      tmem_wait_ld();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&acce_bar[acc]);
       const int n = qd * 32 + lane;  // row of the weight tile
       if (shared_unit) {
         // a shared unit: leave the partial, and let the last to arrive add up
@@ -649,7 +702,8 @@ GroupedPlan grouped_plan(int mode, int64_t R, int64_t E, int64_t N, int64_t K, b
   // 256, 9 rows, 2 steps: 11 against 19; 8 of 2048 x 7168, 15 rows: 29 and 29).
   const int64_t wpairs = (N / 128 + 1) / 2, active = E < R ? E : R;
   const bool few = R * wpairs < 8000 && (active * wpairs < grouped_pair_clusters() || KB <= 8);
-  g.tt = R <= 8 * E || few ? 32 : 256;
+  // FP8_BLOCK128's fold is built for 32-row tiles only.
+  g.tt = R <= 8 * E || few || mode == FG_FP8_BLOCK128 ? 32 : 256;
   g.tiles = R / g.tt + active;
   const int64_t units = g.tiles * (g.tt == 256 ? wpairs : N / 128);
   const int64_t most = g.tt == 32 ? kBlocksPerSm * static_cast<int64_t>(sm_count()) : grouped_pair_clusters();
@@ -671,8 +725,6 @@ GroupedPlan grouped_plan(int mode, int64_t R, int64_t E, int64_t N, int64_t K, b
 fg_status check_grouped(int mode, int64_t R, int E, int64_t N, int64_t K) {
   const char* what = "fg_grouped_gemm";
   if (!mode_ok(mode)) return fail(FG_ERR_INVALID_ARG, "%s: bad mode %d", what, mode);
-  if (mode == FG_FP8_BLOCK128)
-    return fail(FG_ERR_INVALID_ARG, "%s: not built for fp8_block128 (fp32 block scales); use an MX mode", what);
   if (E < 1 || E > kMaxExperts) return fail(FG_ERR_SHAPE, "%s: E=%d outside 1..%d", what, E, kMaxExperts);
   if (R < 0 || R > (int64_t(1) << 24)) return fail(FG_ERR_SHAPE, "%s: R=%lld", what, (long long)R);
   if (N <= 0 || N % 128) return fail(FG_ERR_SHAPE, "%s: N=%lld per expert must be a multiple of 128", what, (long long)N);
@@ -716,7 +768,7 @@ fg_status fg_grouped_gemm(const void* A, const void* a_scales, int64_t T, const 
   if (!A || !Y || !offsets) return fail(FG_ERR_INVALID_ARG, "%s: null A, Y or offsets", what);
   if (mode != FG_BF16 && !a_scales) return fail(FG_ERR_INVALID_ARG, "%s: %s needs A scales", what, mode_name(mode));
   if (!aligned(A, 16) || !aligned(Y, 16)) return fail(FG_ERR_ALIGN, "%s: A and Y must be 16-byte aligned", what);
-  if (!aligned(offsets, 4) || !aligned(rows, 4) || (mode == FG_FP8_TENSOR && !aligned(a_scales, 4)))
+  if (!aligned(offsets, 4) || !aligned(rows, 4) || ((mode == FG_FP8_TENSOR || mode == FG_FP8_BLOCK128) && !aligned(a_scales, 4)))
     return fail(FG_ERR_ALIGN, "%s: offsets, rows and fp32 scales must be 4-byte aligned", what);
   const int64_t rb = row_bytes(mode, K);
   const GroupedPlan g = grouped_plan(mode, R, E, N, K, rows != nullptr);
@@ -785,6 +837,7 @@ fg_status fg_grouped_gemm(const void* A, const void* a_scales, int64_t T, const 
   switch (mode) {
     case FG_BF16: e = launch_mode<kBF16>(a_maps, tmap_b, p, g.blocks, st); break;
     case FG_FP8_TENSOR: e = launch_mode<kTensor>(a_maps, tmap_b, p, g.blocks, st); break;
+    case FG_FP8_BLOCK128: e = launch_mode<kBlock>(a_maps, tmap_b, p, g.blocks, st); break;
     case FG_MXFP8: e = launch_mode<kMXFP8>(a_maps, tmap_b, p, g.blocks, st); break;
     case FG_MXFP4: e = launch_mode<kMXFP4>(a_maps, tmap_b, p, g.blocks, st); break;
     case FG_MXFP8_B32: e = launch_mode<kMXFP8B32>(a_maps, tmap_b, p, g.blocks, st); break;

@@ -17,7 +17,7 @@ constexpr int tile_step(int tt) { return tt == 256 ? 32 : 16; }
 struct GroupedParams {
   const uint8_t* b_img;
   const uint8_t* b_sf;
-  const float* b_s;           // FP8_TENSOR
+  const float* b_s;           // FP8_TENSOR: scalar; FP8_BLOCK128: [E * N / 128][K / 128]
   const void* a_scales;
   const int32_t* offsets;     // [E + 1]
   const int32_t* rows;        // [R] or null

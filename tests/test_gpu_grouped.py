@@ -15,7 +15,7 @@ import oracle
 
 pytestmark = pytest.mark.gpu
 
-MODES = ("bf16", "fp8_tensor", "mxfp8", "mxfp8_b32", "mxfp4", "mxfp4_fp8a")
+MODES = ("bf16", "fp8_tensor", "fp8_block128", "mxfp8", "mxfp8_b32", "mxfp4", "mxfp4_fp8a")
 
 
 def values(codes, scales, mode):
@@ -30,6 +30,9 @@ def values(codes, scales, mode):
         v = torch.from_numpy(oracle.table_e4m3()).cuda()[c]
     if mode == "fp8_tensor":
         return v * scales.double()
+    if mode == "fp8_block128":  # [rows][K/128], or a weight's [rows/128][K/128]
+        s = scales.double().repeat_interleave(v.shape[0] // scales.shape[0], 0)
+        return (v.unflatten(1, (s.shape[1], -1)) * s[:, :, None]).flatten(1)
     s = torch.from_numpy(oracle.table_e8m0()).cuda()[scales.view(torch.uint8).long()]
     return (v.unflatten(1, (s.shape[1], -1)) * s[:, :, None]).flatten(1)
 
@@ -41,6 +44,10 @@ def operand(x, mode, weight=False):
     if mode == "fp8_tensor":
         s = (x.abs().max() / 448).reshape(1)
         return (x / s).to(torch.float8_e4m3fn), s, mode
+    if mode == "fp8_block128" and weight:
+        b = x.view(x.shape[0] // 128, 128, -1, 128)
+        s = b.abs().amax((1, 3)) / 448
+        return (b / s[:, None, :, None]).view(x.shape).to(torch.float8_e4m3fn), s, mode
     m = "mxfp4" if weight and mode == "mxfp4_fp8a" else mode
     c, s = fg.quantize(m, x)
     return c, s, m
@@ -151,12 +158,12 @@ def test_offsets_and_rows_out_of_range_stay_in_bounds(total):
     assert_close(y, c.reference(), "clamped")
 
 
-@pytest.mark.parametrize("total", [24, 900])
-def test_same_bits_each_time_and_beside_other_rows(total):
+@pytest.mark.parametrize("mode,total", [("mxfp8_b32", 24), ("mxfp8_b32", 900), ("fp8_block128", 40)])
+def test_same_bits_each_time_and_beside_other_rows(mode, total):
     """The same call gives the same bits, and a row's result does not depend on its neighbours'."""
-    c = Experts("mxfp8_b32", [total // 8] * 8, 512, 4096, 11)
+    c = Experts(mode, [total // 8] * 8, 512, 4096, 11)
     first = c.run()
-    ws = torch.randint(0, 256, (fg.grouped_gemm_workspace_size("mxfp8_b32", total, 8, 512, 4096) + 16,),
+    ws = torch.randint(0, 256, (fg.grouped_gemm_workspace_size(mode, total, 8, 512, 4096) + 16,),
                        dtype=torch.uint8, device="cuda")[:]  # any contents
     for _ in range(5):
         assert torch.equal(c.run(workspace=ws), first)
@@ -211,10 +218,10 @@ def test_graph_replay(total):
         assert torch.equal(y, want)
 
 
-@pytest.mark.parametrize("total", [24, 900])
-def test_a_wait_that_runs_out_is_reported(total):
+@pytest.mark.parametrize("mode,total", [("mxfp8_b32", 24), ("mxfp8_b32", 900), ("fp8_block128", 24)])
+def test_a_wait_that_runs_out_is_reported(mode, total):
     """With the MMA issuer held back every wait gives up and the call ends in FG_ERR_TIMEOUT; the next call is sound."""
-    c = Experts("mxfp8_b32", [total // 8] * 8, 512, 4096, 16)
+    c = Experts(mode, [total // 8] * 8, 512, 4096, 16)
     want = c.run()
     torch.cuda.synchronize()
     fg.set_wait_timeout_ns(20_000_000)
