@@ -559,20 +559,30 @@ __global__ void __launch_bounds__(256) grouped_prep_kernel(const PrepParams p) {
   pdl_wait();
   pdl_launch_dependents();
   if (static_cast<int>(blockIdx.x) < p.copy_blocks) {
+    // two rows at a time, so that both rows' loads are in flight together
     const int lane = threadIdx.x & 63, chunks = p.rb / 16;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kPrepRows + (threadIdx.x >> 6); i < p.R;
-         i += static_cast<int64_t>(p.copy_blocks) * kPrepRows) {
-      const int row = min(max(__ldg(p.rows + i), 0), p.T - 1);
-      const uint4* src = reinterpret_cast<const uint4*>(p.a + static_cast<size_t>(row) * p.rb);
-      uint4* dst = reinterpret_cast<uint4*>(p.a_rows + static_cast<size_t>(i) * p.rb);
-      for (int c0 = lane; c0 < chunks; c0 += 8 * 64) {
-        uint4 v[8];
+    const int64_t step = static_cast<int64_t>(p.copy_blocks) * kPrepRows;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kPrepRows + (threadIdx.x >> 6); i < p.R; i += 2 * step) {
+      const int64_t at[2] = {i, i + step};
+      const uint4* src[2];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (c0 + j * 64 < chunks) v[j] = __ldg(src + c0 + j * 64);
+      for (int r = 0; r < 2; ++r) {
+        const int row = at[r] < p.R ? min(max(__ldg(p.rows + at[r]), 0), p.T - 1) : 0;
+        src[r] = reinterpret_cast<const uint4*>(p.a + static_cast<size_t>(row) * p.rb);
+      }
+      for (int c0 = lane; c0 < chunks; c0 += 4 * 64) {
+        uint4 v[2][4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (c0 + j * 64 < chunks) dst[c0 + j * 64] = v[j];
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (at[r] < p.R && c0 + j * 64 < chunks) v[r][j] = __ldg(src[r] + c0 + j * 64);
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (at[r] < p.R && c0 + j * 64 < chunks)
+              reinterpret_cast<uint4*>(p.a_rows + static_cast<size_t>(at[r]) * p.rb)[c0 + j * 64] = v[r][j];
       }
     }
     return;

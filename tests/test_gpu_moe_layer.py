@@ -7,18 +7,12 @@ product of gate and up adds two such errors (silu' up to 1.1) and is rounded
 again: about 2.6 % * sqrt(2 * 1.1 + 1) = 4.7 %.  Bound: 8 %.  For 4-bit
 activations (e2m1: 2^-2, about 11 %) the same gives 20 %; bound 30 %.
 """
-import os
-import sys
-
 import pytest
 import torch
 
 import mx_gemm_gb300 as fg
-from tests.conftest import ROOT
+from examples import moe_layer
 from tests.test_gpu_grouped import values
-
-sys.path.insert(0, os.path.join(ROOT, "examples"))
-import moe_layer  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
