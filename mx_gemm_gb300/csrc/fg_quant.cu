@@ -19,7 +19,7 @@
 //
 // Both kernels are bound by HBM: every input byte is read once (16 bytes a
 // load) and every output byte written once.  Measured: 8191 x 7168 bf16 with
-// residual to 32-K mxfp8 66 us (6.3 TB/s of the 6.8 that a copy reaches), the
+// residual to 32-K mxfp8 63.4 us (6.5 TB/s of the 6.8 that a copy reaches), the
 // gated activation of 32761 x 2048 in 50 us (6.8 TB/s).  One row of 7168 takes 6.5
 // us of host time, 4.6 us on the GPU, all latency: a block of 896 threads with
 // one chunk each, the weight's load under way during the reduction.
@@ -234,9 +234,11 @@ struct NormParams {
 };
 
 // One block per row; a thread keeps NC chunks of eight values in registers, so
-// the row is read once.
-template <int MODE, typename T, int NC>
-__global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormParams p) {
+// the row is read once.  MOST: threads of the block at most; with 1024 a thread
+// has 64 registers and four chunks spill (8191 x 7168, 224 threads: 66.1 us so, 63.4
+// with up to 128).
+template <int MODE, typename T, int NC, int MOST>
+__global__ void __launch_bounds__(MOST) rmsnorm_kernel(const NormParams p) {
   __shared__ float part[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int cpr = static_cast<int>(p.K / kVec);
@@ -363,9 +365,11 @@ cudaError_t launch_norm(const NormParams& p, int64_t M, cudaStream_t st) {
   cudaLaunchAttribute attr;
   pdl_config(cfg, attr, dim3(static_cast<unsigned>(M)), dim3(static_cast<unsigned>(threads)), st);
   switch (nc) {
-    case 1: return cudaLaunchKernelEx(&cfg, rmsnorm_kernel<MODE, T, 1>, p);
-    case 2: return cudaLaunchKernelEx(&cfg, rmsnorm_kernel<MODE, T, 2>, p);
-    default: return cudaLaunchKernelEx(&cfg, rmsnorm_kernel<MODE, T, 4>, p);
+    case 1: return cudaLaunchKernelEx(&cfg, rmsnorm_kernel<MODE, T, 1, 1024>, p);
+    case 2: return cudaLaunchKernelEx(&cfg, rmsnorm_kernel<MODE, T, 2, 1024>, p);
+    default:
+      return threads <= 512 ? cudaLaunchKernelEx(&cfg, rmsnorm_kernel<MODE, T, 4, 512>, p)
+                            : cudaLaunchKernelEx(&cfg, rmsnorm_kernel<MODE, T, 4, 1024>, p);
   }
 }
 
