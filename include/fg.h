@@ -308,8 +308,9 @@ FG_API fg_status fg_gemm_noalloc(const void* A, const void* a_scales, int64_t M,
  *          of fg_gemm.
  * E8M0 c = 127 + ceil(log2(amax / elem_max)) clamped to 0..254 (127 for an
  * all-zero block), code = RNE(v * 2^(127-c)); FP8_BLOCK128: scale = amax / 448
- * (1 for an all-zero block), code = RNE(v / scale).  A block with a NaN or an
- * infinity gets the NaN scale (255; fp32 NaN) and zero codes.
+ * (1 for an all-zero block; rounded to nearest, for amax < 2^-132 upwards, so
+ * never 0), code = RNE(v / scale).  A block with a NaN or an infinity gets the
+ * NaN scale (255; fp32 NaN) and zero codes.
  * A weight's [N][K] rows quantise the same way (not FP8_BLOCK128, whose
  * weights have 128 x 128 blocks).
  * Errors: INVALID_ARG, SHAPE (K not a multiple of the block), ALIGN (x and its

@@ -8,9 +8,10 @@
 // clamped to 0..254 (127 for an all-zero block), and a value's code is
 // RNE(x * 2^(127 - c)) in the element format: 2^(c-127) is the smallest power
 // of two that keeps the block inside the format.  FP8_BLOCK128 keeps the fp32
-// scale amax / 448 (1 for an all-zero block), codes RNE(x / scale).  A block
-// that holds a NaN or an infinity gets the NaN scale (E8M0 255, fp32 NaN) and
-// zero codes, so whatever is computed from it is NaN.
+// scale amax / 448 (1 for an all-zero block; rounded up where amax < 2^-132),
+// codes RNE(x / scale).  A block that holds a NaN or an infinity gets the NaN
+// scale (E8M0 255, fp32 NaN) and zero codes, so whatever is computed from it is
+// NaN.
 //
 // The ceil(log2()) needs no logarithm: amax = 1.m * 2^e and elem_max is 1.75 *
 // 2^8 (e4m3) or 1.5 * 2^2 (e2m1), so it is e - 8 or e - 2, plus one where 1.m
@@ -131,7 +132,12 @@ __device__ __forceinline__ void quantize8(float (&v)[kVec], bool live, size_t ch
   const bool finite = amax < 0x7f800000u;
   const bool first = (threadIdx.x & (LANES - 1)) == 0;
   if (MODE == kBlock) {
-    const float s = !finite ? __uint_as_float(0x7fc00000u) : (amax == 0 ? 1.f : __fdiv_rn(__uint_as_float(amax), 448.f));
+    const float top = __uint_as_float(amax);
+    float s = !finite ? __uint_as_float(0x7fc00000u) : (amax == 0 ? 1.f : __fdiv_rn(top, 448.f));
+    // below 2^-132 the quotient has nine bits at most, or is zero: the next
+    // value up where it came out too small (s * 448 is exact there), so that
+    // nothing is divided by zero and no code saturates
+    if (finite && top < 0x1p-132f && s * 448.f < top) s = __uint_as_float(__float_as_uint(s) + 1u);
 #pragma unroll
     for (int i = 0; i < kVec; ++i) v[i] = finite ? __fdiv_rn(v[i], s) : 0.f;
     if (live && first) static_cast<float*>(scales)[chunk / LANES] = s;
