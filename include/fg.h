@@ -95,7 +95,8 @@ typedef enum fg_type { FG_TYPE_F32 = 0, FG_TYPE_BF16 = 1 } fg_type;
 /* what fg_quantize applies to its input first */
 typedef enum fg_act {
   FG_ACT_NONE = 0,
-  FG_ACT_SWIGLU = 1 /* rows of 2K values (g, u): silu(g) * u = g / (1 + exp(-g)) * u */
+  FG_ACT_SWIGLU = 1 /* rows of 2K values (g, u): silu(g) * u = g / (1 + exp(-g)) * u, */
+                    /* in 32 bits: zero below g = -88.7, where exp(-g) overflows   */
 } fg_act;
 
 /* fg_moe_route flag: weights over the chosen experts only (they sum to 1) */

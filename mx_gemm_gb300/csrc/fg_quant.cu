@@ -171,17 +171,21 @@ __device__ __forceinline__ void quantize8(float (&v)[kVec], bool live, size_t ch
 
 // v = silu(v) * u = v / (1 + 2^(-v log2 e)) * u for two values, with the fast
 // power and reciprocal (2 ulp each, and |v| 2^-24 from the rounded exponent,
-// against the 2^-4 steps of the codes); below v = -88 the result is zero.
+// against the 2^-4 steps of the codes).  Zero below v = -88.7, where exp(-v) is
+// past 32 bits.  Down to there 1 / (1 + exp(-v)) may be under 2^-126, which the
+// fast reciprocal would flush: it takes a sixteenth of the sum.
 __device__ __forceinline__ void swiglu2(float& v0, float& v1, float u0, float u1) {
   constexpr float kLog2e = 1.44269504088896341f;
+  constexpr float kSixteenth = 0.0625f;
   float e0 = v0, e1 = v1;
   mul2(e0, e1, -kLog2e, -kLog2e);
   asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e0));
   asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e1));
-  e0 += 1.f;
-  e1 += 1.f;
+  e0 = fmaf(e0, kSixteenth, kSixteenth);
+  e1 = fmaf(e1, kSixteenth, kSixteenth);
   asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e0));
   asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e1));
+  mul2(e0, e1, kSixteenth, kSixteenth);
   mul2(v0, v1, e0, e1);
   mul2(v0, v1, u0, u1);
 }
