@@ -363,8 +363,9 @@ FG_API fg_status fg_moe_route(const void* logits, int type, int64_t T, int E, in
  *  A        [T][K] codes as in fg_gemm, a_scales likewise ([T] rows).
  *  rows     device int32 [R]: the row of A that row i multiplies, clamped into
  *           0..T-1; NULL: row i itself (T >= R).
- *  offsets  device int32 [E + 1], not decreasing, clamped into 0..R.  Rows of Y
- *           before offsets[0] and from offsets[E] on are not written.
+ *  offsets  device int32 [E + 1], not decreasing (one that does counts as the
+ *           largest before it), clamped into 0..R.  Rows of Y before offsets[0]
+ *           and from offsets[E] on are not written.
  *  workspace  fg_grouped_gemm_workspace_size bytes (gather: rows given); any contents.  Calls that
  *           overlap on the GPU need a workspace each.
  * All modes (FP8_BLOCK128 in 32-row tiles whatever the rows: made for decoding);

@@ -92,11 +92,23 @@ __device__ __forceinline__ Unit uniform(Unit q) {
 }
 
 // The offsets, clamped into 0..R, and the token tiles before each expert, by
-// the whole block (any count of warps); ends with the block in step.
+// the whole block (any count of warps); ends with the block in step.  Offsets
+// that decrease would make more tiles than the workspace is laid out for: each
+// counts as the largest up to it.
 template <int TT>
 __device__ __forceinline__ void read_offsets(const int32_t* offsets, int R, int E, int* offs, int* tiles) {
-  for (int e = threadIdx.x; e <= E; e += blockDim.x) offs[e] = min(max(__ldg(offsets + e), 0), R);
-  __syncthreads();
+  bool falls = false;
+  for (int e = threadIdx.x; e <= E; e += blockDim.x) {
+    const int o = min(max(__ldg(offsets + e), 0), R);
+    offs[e] = o;
+    falls |= e > 0 && min(max(__ldg(offsets + e - 1), 0), R) > o;
+  }
+  if (__syncthreads_or(falls)) {
+    if (threadIdx.x == 0) {
+      for (int e = 1; e <= E; ++e) offs[e] = max(offs[e], offs[e - 1]);
+    }
+    __syncthreads();
+  }
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x;
     int carry = 0;
