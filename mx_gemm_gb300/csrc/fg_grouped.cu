@@ -54,6 +54,7 @@ namespace {
 
 constexpr int kMinSlabs = 4;    // K steps a block of the cut line takes at least
 constexpr int kShareSteps = 12;  // see the schedule
+constexpr unsigned long long kGaveUp = 0x8000;  // of a ticket: a block of the unit gave up
 
 constexpr int TT = 32;           // rows of a token tile
 constexpr int kThreads = 256;    // copies, MMAs, two warps of scales, four of results
@@ -408,6 +409,34 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     const float scale = MODE == kTensor ? __ldg(static_cast<const float*>(p.a_scales)) * __ldg(p.b_s) : 1.f;
     bool ok = true;
     int it = 0;  // K steps so far (FOLD)
+    // One thread's arrival at a shared unit, when the block's partial is in the
+    // workspace; last_sh: this block adds up.  A ticket holds the call's tag, a
+    // bit for a block that gave up, and the arrivals; a word of another call (or
+    // of nothing) counts as none.  Every block arrives, also one that gave up,
+    // and the last leaves the word clear: a replay of a captured call carries
+    // the same tag and must not find the arrivals of an earlier run.  The
+    // barrier before the call put the block's partial before this thread, its
+    // fence puts it before the arrival.  First guess: the word is clear, as a
+    // finished unit leaves it.
+    auto arrive = [&](long long u, bool gave_up) {
+      const long long first = u * s.KB;
+      const int c0 = holder_of(s, first), others = holder_of(s, first + s.KB - 1) - c0;
+      __threadfence();
+      unsigned long long* t = p.tickets + c0;
+      unsigned long long old = 0ull, seen, held;
+      int arrived;
+      bool last;
+      do {
+        seen = old;
+        held = (seen >> 16) == p.epoch ? seen & 0xffffu : 0ull;
+        arrived = static_cast<int>(held & (kGaveUp - 1));
+        last = arrived == others;
+        held = (held & kGaveUp) | (gave_up ? kGaveUp : 0ull);
+        old = atomicCAS(t, seen, last ? 0ull : (p.epoch << 16) | held | static_cast<unsigned long long>(arrived + 1));
+      } while (old != seen);
+      __threadfence();
+      last_sh = last && held == 0ull;
+    };
     for (int i = 0; i < shares; ++i) {
       const Share h = share_at(s, i);
       const Unit q = uniform(unit_at<TT>(s, h.u));
@@ -462,6 +491,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         if (lane == 0) abort_sh = 1;
         if (shared_unit) {
           bar_sync_named(1, 128);
+          if (threadIdx.x == 128) arrive(h.u, true);
           bar_sync_named(1, 128);
         }
         continue;
@@ -479,25 +509,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         for (int m = 0; m < TT; ++m)
           if (m < q.count) __stcg(mine + m * 128 + n, __uint_as_float(v[m]));
         bar_sync_named(1, 128);
-        if (threadIdx.x == 128) last_sh = 0;
-        if (threadIdx.x == 128 && *reinterpret_cast<volatile int*>(&abort_sh) == 0) {
-          // Tickets hold the call's tag and the arrivals; a word of another
-          // call (or of nothing) counts as none.  The barrier above put the
-          // block's partial before this thread, its fence puts it before the
-          // arrival.  First guess: the word is clear, as a finished unit leaves it.
-          __threadfence();
-          unsigned long long* t = p.tickets + c0;
-          unsigned long long old = 0ull, seen;
-          int arrived;
-          do {
-            seen = old;
-            arrived = (seen >> 16) == p.epoch ? static_cast<int>(seen & 0xffffu) : 0;
-            const bool last = arrived == c1 - c0;  // the others are in: leave the word clear
-            old = atomicCAS(t, seen, last ? 0ull : (p.epoch << 16) | static_cast<unsigned long long>(arrived + 1));
-          } while (old != seen);
-          __threadfence();
-          last_sh = arrived == c1 - c0;
-        }
+        if (threadIdx.x == 128) arrive(h.u, *reinterpret_cast<volatile int*>(&abort_sh) != 0);
         bar_sync_named(1, 128);
         const bool last = last_sh != 0;
         if (!last) continue;

@@ -51,3 +51,38 @@ def test_offsets_that_decrease(mode, total, n, experts, gather):
         assert (y[:lo] == 3).all() and (y[hi:] == 3).all()
         if hi > lo:
             assert_close(y[lo:hi], c.reference()[lo:hi], offsets)
+
+
+def words(ws, c, n, k):
+    """The tickets of a 32-row call: the last of the workspace's (two 32 x 128 fp32 partials and a ticket) a block."""
+    blocks = ws.numel() // (2 * 32 * 128 * 4 + 8)
+    assert blocks * (2 * 32 * 128 * 4 + 8) == ws.numel()
+    return ws[-8 * blocks:].view(torch.int64)
+
+
+@pytest.mark.parametrize("mode", ["mxfp8_b32", "mxfp4_fp8a", "fp8_block128"])
+def test_a_call_that_gave_up_leaves_no_arrivals(mode):
+    """Shared units' tickets are clear after every call, also one that ran out of time: a replay of a captured call
+    carries the call's tag and would count arrivals that an earlier run left."""
+    n, k = 512, 4096
+    c = Experts(mode, [3] * 8, n, k, 22)
+    want = c.run()
+    ws, guard = guarded(c, n, k, False)
+    assert torch.equal(c.run(workspace=ws), want)
+    shared = words(ws, c, n, k) == 0              # (the buffer held 0xa5 bytes)
+    assert shared.any() and not shared.all()
+    ws.fill_(0xa5)
+    torch.cuda.synchronize()
+    fg.set_wait_timeout_ns(20_000_000)
+    try:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            c.run(workspace=ws, flags=fg.FG_FLAG_DEBUG_STALL)
+    finally:
+        fg.set_wait_timeout_ns(4_000_000_000)
+    for _ in range(2):
+        graph.replay()
+        assert fg.get_error() == fg.FG_ERR_TIMEOUT
+        assert torch.equal(words(ws, c, n, k) == 0, shared)
+    assert torch.equal(c.run(workspace=ws), want) and fg.get_error() == fg.FG_OK
+    assert (guard == 0xa5).all()
