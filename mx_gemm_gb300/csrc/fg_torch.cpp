@@ -152,20 +152,47 @@ PyObject* wrap(const at::Tensor& t) {
   Py_RETURN_NONE;
 }
 
-// The stream of a launch on `device`: the current one, or the caller's handle.
-// Tensors made here are then kept from reuse until that stream is done.
-void* stream_of(PyObject* handle, const at::Device& device) {
+// The stream of a call: the current one of the operands' device, or the caller's.
+struct Launch {
+  c10::cuda::CUDAStream current;
+  cudaStream_t stream;
+  bool other() const { return stream != current.stream(); }
+};
+
+Launch launch_of(PyObject* handle, const at::Device& device) {
   if (device.index() != c10::cuda::current_device())
     refuse("the operands are on %s, the current device is cuda:%d", device.str().c_str(), (int)c10::cuda::current_device());
-  if (handle == Py_None) return c10::cuda::getCurrentCUDAStream(device.index()).stream();
-  return reinterpret_cast<void*>(static_cast<intptr_t>(integer(handle, "stream")));
+  const auto current = c10::cuda::getCurrentCUDAStream(device.index());
+  if (handle == Py_None) return {current, current.stream()};
+  auto stream = reinterpret_cast<cudaStream_t>(static_cast<intptr_t>(integer(handle, "stream")));
+  if (stream == cudaStreamLegacy) stream = nullptr;  // the default stream by its other name
+  return {current, stream};
 }
 
-void keep(PyObject* handle, void* stream, const at::Device& device, std::initializer_list<at::Tensor> made) {
-  if (handle == Py_None || stream == c10::cuda::getCurrentCUDAStream(device.index()).stream()) return;
-  const auto other = c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(stream), device.index());
+// While it lives, memory is allocated for the call's stream: a block that was
+// freed on the caller's current stream may still be in use there by work that
+// the call's stream does not wait for.
+struct Pool {
+  const Launch& launch;
+  explicit Pool(const Launch& l) : launch(l) {
+    if (l.other()) c10::cuda::setCurrentCUDAStream(c10::cuda::getStreamFromExternal(l.stream, l.current.device_index()));
+  }
+  ~Pool() {
+    if (launch.other()) c10::cuda::setCurrentCUDAStream(launch.current);
+  }
+};
+
+// On another stream than the current one: the memory of what was made here is
+// not reused before the current stream, on which the caller uses it (after a
+// wait of its own), is done with it, and that of the caller's tensors not before
+// the call's stream is.
+void keep(const Launch& launch, std::initializer_list<at::Tensor> made, std::initializer_list<const at::Tensor*> given) {
+  if (!launch.other()) return;
   for (const at::Tensor& t : made)
-    if (t.defined()) t.record_stream(other.unwrap());
+    if (t.defined()) t.record_stream(launch.current.unwrap());
+  const auto other = c10::cuda::getStreamFromExternal(launch.stream, launch.current.device_index());
+  for (const at::Tensor* t : given)
+    if (t && t->defined()) t->record_stream(other.unwrap());
 }
 
 struct Codes {
@@ -201,13 +228,15 @@ PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
       r.k /= 2;
     }
     const at::Device device = x.device();
-    void* st = stream_of(a[3], device);
+    const Launch launch = launch_of(a[3], device);
     Codes c;
     {
       Unlocked u;
+      Pool pool(launch);
       c = make_codes(mode, r.m, r.k, device);
-      check(fg_quantize((int)mode, (int)act, x.data_ptr(), type, r.m, r.k, r.ld, c.codes.data_ptr(), c.scales.data_ptr(), st));
-      keep(a[3], st, device, {c.codes, c.scales});
+      check(fg_quantize((int)mode, (int)act, x.data_ptr(), type, r.m, r.k, r.ld, c.codes.data_ptr(), c.scales.data_ptr(),
+                        launch.stream));
+      keep(launch, {c.codes, c.scales}, {&x});
     }
     return Py_BuildValue("(NN)", wrap(c.codes), wrap(c.scales));
   });
@@ -242,17 +271,18 @@ PyObject* rmsnorm_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
       refuse("eps must be a number");
     }
     const bool plain = mode == FG_BF16, normed = plain || PyObject_IsTrue(a[5]) == 1;
-    void* st = stream_of(a[6], device);
+    const Launch launch = launch_of(a[6], device);
     Codes c;
     at::Tensor h, y;
     {
       Unlocked u;
+      Pool pool(launch);
       if (!plain) c = make_codes(mode, r.m, r.k, device);
       if (res) h = make({r.m, r.k}, x.scalar_type(), device);
       if (normed) y = make({r.m, r.k}, x.scalar_type(), device);
       check(fg_rmsnorm_quantize((int)mode, x.data_ptr(), r.ld, res ? res->data_ptr() : nullptr, rr.ld, w.data_ptr(), (float)eps,
-                                type, r.m, r.k, data(h), data(y), data(c.codes), data(c.scales), st));
-      keep(a[6], st, device, {c.codes, c.scales, h, y});
+                                type, r.m, r.k, data(h), data(y), data(c.codes), data(c.scales), launch.stream));
+      keep(launch, {c.codes, c.scales, h, y}, {&x, &w, res});
     }
     return Py_BuildValue("(NNNN)", wrap(c.codes), wrap(c.scales), wrap(h), wrap(y));
   });
@@ -269,10 +299,11 @@ PyObject* moe_route(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (k < 1 || k > (r.k > 1 ? r.k : 1)) refuse("top_k=%lld outside 1..%lld", (long long)k, (long long)r.k);
     const bool renormalize = PyObject_IsTrue(a[2]) == 1;
     const at::Device device = x.device();
-    void* st = stream_of(a[3], device);
+    const Launch launch = launch_of(a[3], device);
     at::Tensor weights, experts, offsets, rows, slots, ws;
     {
       Unlocked u;
+      Pool pool(launch);
       uint64_t need = 0;
       check(fg_moe_route_workspace_size(r.m, (int)(r.k < (1 << 30) ? r.k : 1 << 30), &need));
       weights = make({r.m, k}, at::kFloat, device);
@@ -283,8 +314,9 @@ PyObject* moe_route(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (need) ws = make({static_cast<int64_t>(need)}, at::kByte, device);
       check(fg_moe_route(x.data_ptr(), type, r.m, (int)r.k, r.ld, (int)(k < 1024 ? k : 1024),
                          renormalize ? FG_FLAG_RENORMALIZE : 0, weights.data_ptr<float>(), experts.data_ptr<int32_t>(),
-                         offsets.data_ptr<int32_t>(), rows.data_ptr<int32_t>(), slots.data_ptr<int32_t>(), data(ws), need, st));
-      keep(a[3], st, device, {weights, experts, offsets, rows, slots, ws});
+                         offsets.data_ptr<int32_t>(), rows.data_ptr<int32_t>(), slots.data_ptr<int32_t>(), data(ws), need,
+                         launch.stream));
+      keep(launch, {weights, experts, offsets, rows, slots}, {&x});
     }
     return Py_BuildValue("(NNNNN)", wrap(weights), wrap(experts), wrap(offsets), wrap(rows), wrap(slots));
   });
@@ -357,9 +389,10 @@ PyObject* grouped_gemm(PyObject*, PyObject* const* v, Py_ssize_t n) {
       contiguous(ws, "workspace");
     }
     const int64_t flags = integer(v[8], "flags");
-    void* st = stream_of(v[9], device);
+    const Launch launch = launch_of(v[9], device);
     {
       Unlocked u;
+      Pool pool(launch);
       uint64_t bytes = 0;
       if (!ws.defined()) {
         check(fg_grouped_gemm_workspace_size(mode, R, (int)E, N, K, rows != nullptr, &bytes));
@@ -369,8 +402,9 @@ PyObject* grouped_gemm(PyObject*, PyObject* const* v, Py_ssize_t n) {
       }
       if (!Y.defined()) Y = make({R, N}, at::kBFloat16, device);
       check(fg_grouped_gemm(A.data_ptr(), scales ? scales->data_ptr() : nullptr, T, rows ? rows->data_ptr<int32_t>() : nullptr, R,
-                            offsets.data_ptr<int32_t>(), (int)E, b, mode, Y.data_ptr(), data(ws), bytes, (uint32_t)flags, st));
-      keep(v[9], st, device, {Y, ws});
+                            offsets.data_ptr<int32_t>(), (int)E, b, mode, Y.data_ptr(), data(ws), bytes, (uint32_t)flags,
+                            launch.stream));
+      keep(launch, {Y}, {&A, &weight, &offsets, scales, rows, &Y, &ws});
     }
     return wrap(Y);
   });
@@ -405,14 +439,15 @@ PyObject* moe_combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (r->dim() != 2 || r->size(0) != t || r->size(1) != cols)
         refuse("residual has shape %s, expected (%lld, %lld)", shape_of(*r).c_str(), (long long)t, (long long)cols);
     }
-    void* st = stream_of(a[4], device);
+    const Launch launch = launch_of(a[4], device);
     at::Tensor out;
     {
       Unlocked u;
+      Pool pool(launch);
       out = make({t, cols}, at::kBFloat16, device);
       check(fg_moe_combine(Y.data_ptr(), Y.size(0), slots.data_ptr<int32_t>(), w.data_ptr<float>(), r ? r->data_ptr() : nullptr, t,
-                           (int)(k < 1024 ? k : 1024), cols, out.data_ptr(), st));
-      keep(a[4], st, device, {out});
+                           (int)(k < 1024 ? k : 1024), cols, out.data_ptr(), launch.stream));
+      keep(launch, {out}, {&Y, &slots, &w, r});
     }
     return wrap(out);
   });

@@ -7,6 +7,10 @@ The functions check their tensors, allocate their outputs and call the C ABI
 binding: at a few microseconds a call, doing that from Python would take most of
 the time.  There is no fallback: if the binding has not been built, loading it
 raises.  `stream` is a torch stream or a raw handle; None is the current one.
+On another stream than the current one the caller orders only what it passes
+and takes: that stream waits for the inputs, and whoever uses the outputs for
+that stream.  Outputs and workspaces come from that stream's memory, and no
+tensor's memory is reused before both are done with it.
 """
 import ctypes
 import importlib.util
