@@ -211,6 +211,20 @@ def _stream(stream):
     return int(stream)
 
 
+def _empty(shape, dtype, device, stream):
+    """torch.empty of memory for a launch on `stream`: from that stream's pool (a
+    block freed on the current one may still be in use there), and not reused
+    before the current stream, on which the caller uses it, is done with it."""
+    handle = None if stream is None else _stream(stream)
+    handle = 0 if handle == 1 else handle  # 1 (cudaStreamLegacy): the default stream's other name
+    if handle is None or handle == torch._C._cuda_getCurrentRawStream(device.index):
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def set_wait_timeout_ns(ns):
     lib().fg_set_wait_timeout_ns(int(ns))
 
@@ -266,8 +280,8 @@ def preshuffle_b(mode, B, b_scales=None, K=None, stream=None):
         dts, n = _scale_spec(mode, N, K, True)
         _require(b_scales, "b_scales", dts, B.device, numel=n)
     nb, ns = preshuffle_b_size(mode, N, K)
-    data = torch.empty(nb, dtype=torch.uint8, device=B.device)
-    sf = torch.empty(max(ns, 16), dtype=torch.uint8, device=B.device) if ns else None
+    data = _empty(nb, torch.uint8, B.device, stream)
+    sf = _empty(max(ns, 16), torch.uint8, B.device, stream) if ns else None
     desc = BShuf()
     _check(lib().fg_preshuffle_b(mode, _ptr(B), _ptr(b_scales), N, K, _ptr(data), nb, _ptr(sf), ns,
                                  ctypes.byref(desc), _stream(stream)))
@@ -278,16 +292,16 @@ def unshuffle_b(pb, stream=None):
     """Inverse relayout: (B bytes [N][Kb] uint8, scales in the caller layout or None)."""
     mode, N, K = pb.mode, pb.N, pb.K
     kb = K * (2 if mode == FG_BF16 else 1) // (2 if mode in (FG_MXFP4, FG_MXFP4_FP8A) else 1)
-    B = torch.empty((N, kb), dtype=torch.uint8, device=pb.data.device)
+    B = _empty((N, kb), torch.uint8, pb.data.device, stream)
     sc = None
     if mode == FG_FP8_TENSOR:
-        sc = torch.empty(1, dtype=torch.float32, device=B.device)
+        sc = _empty(1, torch.float32, B.device, stream)
     elif mode == FG_FP8_BLOCK128:
-        sc = torch.empty((N // 128, K // 128), dtype=torch.float32, device=B.device)
+        sc = _empty((N // 128, K // 128), torch.float32, B.device, stream)
     elif mode == FG_MXFP8:
-        sc = torch.empty((N, K // 128), dtype=torch.uint8, device=B.device)
+        sc = _empty((N, K // 128), torch.uint8, B.device, stream)
     elif mode in (FG_MXFP4, FG_MXFP8_B32, FG_MXFP4_FP8A):
-        sc = torch.empty((N, K // 32), dtype=torch.uint8, device=B.device)
+        sc = _empty((N, K // 32), torch.uint8, B.device, stream)
     _check(lib().fg_unshuffle_b(ctypes.byref(pb.desc), _ptr(B), _ptr(sc), _stream(stream)))
     return B, sc
 
@@ -311,7 +325,9 @@ def gemm(A, pb, a_scales=None, mode=None, split_k=0, Y=None, workspace=None, fla
 
     A is the device tensor of codes ([M][K] bf16 or uint8, or packed fp4
     [M][K/2]).  A workspace is allocated here when the resolved split needs
-    one and none is given.  Returns Y.
+    one and none is given.  Returns Y.  On another stream than the current one
+    Y and the workspace come from that stream's memory; the caller orders that
+    stream after the inputs, and keeps them until it has read them.
     """
     if mode is None and Y is None and workspace is None and flags == 0 and stream is None:
         # the ordinary call, compiled; None where an argument is amiss, which
@@ -323,14 +339,14 @@ def gemm(A, pb, a_scales=None, mode=None, split_k=0, Y=None, workspace=None, fla
     M = _check_gemm_args(mode, A, pb, a_scales, Y)
     N = pb.N
     if Y is None:
-        Y = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
+        Y = _empty((M, N), torch.bfloat16, A.device, stream)
     if workspace is not None:
         _require(workspace, "workspace", device=A.device)
     ws_bytes = 0
     if workspace is None:
         need = gemm_workspace_size(mode, M, N, pb.K, split_k) if M > 0 else 0
         if need:
-            workspace = torch.empty(need // 4, dtype=torch.float32, device=A.device)
+            workspace = _empty(need // 4, torch.float32, A.device, stream)
     if workspace is not None:
         ws_bytes = workspace.numel() * workspace.element_size()
     _check(lib().fg_gemm(_ptr(A), _ptr(a_scales), M, ctypes.byref(pb.desc), mode, split_k, _ptr(Y),
@@ -360,7 +376,7 @@ def gemm_splitk_reduce(ws, split_k, M, N, a_s=None, b_s=None, Y=None, stream=Non
     if Y is not None:
         _require(Y, "Y", _dtypes("bfloat16", "int16"), ws.device, shape=(M, N))
     if Y is None:
-        Y = torch.empty((M, N), dtype=torch.bfloat16, device=ws.device)
+        Y = _empty((M, N), torch.bfloat16, ws.device, stream)
     _check(lib().fg_gemm_splitk_reduce(_ptr(ws), split_k, M, N, _ptr(a_s), _ptr(b_s), _ptr(Y),
                                        _stream(stream)))
     return Y

@@ -47,8 +47,42 @@ def rows(seed, m, k):
     return torch.randn(m, k, generator=g, device="cuda").to(torch.bfloat16)
 
 
+class Dense:
+    """Preshuffling, product, two-pass product and inverse on one weight, each on the stream that it is given."""
+
+    def __init__(self, mode, m, n, k, seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        self.mode, self.m, self.n, self.k = mode, m, n, k
+        self.a, self.a_s = fg.quantize(mode, torch.randn(m, k, generator=g, device="cuda"))
+        self.b, self.b_s = fg.quantize(mode, torch.randn(n, k, generator=g, device="cuda"))
+        self.pb = fg.preshuffle_b(mode, self.b, self.b_s)
+        self.partials = torch.randn(4 * m * n, generator=g, device="cuda")
+
+    def gemm(self, split_k, **kw):
+        return (fg.gemm(self.a, self.pb, self.a_s, split_k=split_k, **kw),)
+
+    def preshuffle(self, **kw):
+        pb = fg.preshuffle_b(self.mode, self.b, self.b_s, **kw)
+        return pb.data, pb.sf
+
+    def unshuffle(self, **kw):
+        return fg.unshuffle_b(self.pb, **kw)
+
+    def reduce(self, **kw):
+        return (fg.gemm_splitk_reduce(self.partials, 4, self.m, self.n, **kw),)
+
+
+def dense(m, call, split_k=None):
+    def make(seed):
+        d = Dense("mxfp8_b32", m, 2048, 7168, seed)
+        return (lambda **kw: d.gemm(split_k, **kw)) if call == "gemm" else getattr(d, call)
+    return make
+
+
 CALLS = {"quantize": quantize, "norm": norm, "route": route, "grouped_few": grouped(24), "grouped_many": grouped(4096),
-         "combine": combine}
+         "combine": combine, "gemm_one": dense(1, "gemm", 0), "gemm_two_pass": dense(16, "gemm", 16),
+         "gemm_many": dense(1000, "gemm", 0), "preshuffle": dense(16, "preshuffle"), "unshuffle": dense(16, "unshuffle"),
+         "reduce": dense(16, "reduce")}
 
 
 def raw(ts):
