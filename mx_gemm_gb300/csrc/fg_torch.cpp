@@ -92,6 +92,20 @@ int64_t integer(PyObject* o, const char* name) {
   return v;
 }
 
+// ... that fits the C ABI's int, or its 32 bits of flags: cut down to them, 2^32
+// + 1 would pass for 1.
+int small(PyObject* o, const char* name) {
+  const int64_t v = integer(o, name);
+  if (v < INT32_MIN || v > INT32_MAX) refuse("%s=%lld is out of range", name, (long long)v);
+  return static_cast<int>(v);
+}
+
+uint32_t flag_bits(PyObject* o, const char* name) {
+  const int64_t v = integer(o, name);
+  if (v < 0 || v > UINT32_MAX) refuse("%s=%lld is out of range", name, (long long)v);
+  return static_cast<uint32_t>(v);
+}
+
 const at::Tensor& tensor(PyObject* o, const char* name) {
   if (!THPVariable_Check(o)) refuse("%s must be a torch.Tensor, got %s", name, Py_TYPE(o)->tp_name);
   const at::Tensor& t = THPVariable_Unpack(o);
@@ -199,7 +213,7 @@ struct Codes {
   at::Tensor codes, scales;
 };
 
-Codes make_codes(int64_t mode, int64_t m, int64_t k, const at::Device& device) {
+Codes make_codes(int mode, int64_t m, int64_t k, const at::Device& device) {
   Codes c;
   c.codes = mode == FG_MXFP4 ? make({m, k / 2}, at::kByte, device) : make({m, k}, at::kFloat8_e4m3fn, device);
   c.scales = mode == FG_FP8_BLOCK128 ? make({m, k / 128}, at::kFloat, device)
@@ -219,7 +233,7 @@ void arity(Py_ssize_t n, Py_ssize_t want, const char* name) {
 PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     arity(n, 4, "quantize");
-    const int64_t mode = integer(a[0], "mode"), act = integer(a[1], "act");
+    const int mode = small(a[0], "mode"), act = small(a[1], "act");
     const at::Tensor& x = tensor(a[2], "x");
     Rows r = rows_of(x, "x");
     const int type = type_of(x, "x");
@@ -234,7 +248,7 @@ PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
       Unlocked u;
       Pool pool(launch);
       c = make_codes(mode, r.m, r.k, device);
-      check(fg_quantize((int)mode, (int)act, x.data_ptr(), type, r.m, r.k, r.ld, c.codes.data_ptr(), c.scales.data_ptr(),
+      check(fg_quantize(mode, act, x.data_ptr(), type, r.m, r.k, r.ld, c.codes.data_ptr(), c.scales.data_ptr(),
                         launch.stream));
       keep(launch, {c.codes, c.scales}, {&x});
     }
@@ -246,7 +260,7 @@ PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* rmsnorm_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     arity(n, 7, "rmsnorm_quantize");
-    const int64_t mode = integer(a[0], "mode");
+    const int mode = small(a[0], "mode");
     const at::Tensor& x = tensor(a[1], "x");
     const Rows r = rows_of(x, "x");
     const int type = type_of(x, "x");
@@ -280,7 +294,7 @@ PyObject* rmsnorm_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (!plain) c = make_codes(mode, r.m, r.k, device);
       if (res) h = make({r.m, r.k}, x.scalar_type(), device);
       if (normed) y = make({r.m, r.k}, x.scalar_type(), device);
-      check(fg_rmsnorm_quantize((int)mode, x.data_ptr(), r.ld, res ? res->data_ptr() : nullptr, rr.ld, w.data_ptr(), (float)eps,
+      check(fg_rmsnorm_quantize(mode, x.data_ptr(), r.ld, res ? res->data_ptr() : nullptr, rr.ld, w.data_ptr(), (float)eps,
                                 type, r.m, r.k, data(h), data(y), data(c.codes), data(c.scales), launch.stream));
       keep(launch, {c.codes, c.scales, h, y}, {&x, &w, res});
     }
@@ -388,7 +402,7 @@ PyObject* grouped_gemm(PyObject*, PyObject* const* v, Py_ssize_t n) {
       on(ws, "workspace", device);
       contiguous(ws, "workspace");
     }
-    const int64_t flags = integer(v[8], "flags");
+    const uint32_t flags = flag_bits(v[8], "flags");
     const Launch launch = launch_of(v[9], device);
     {
       Unlocked u;
@@ -402,7 +416,7 @@ PyObject* grouped_gemm(PyObject*, PyObject* const* v, Py_ssize_t n) {
       }
       if (!Y.defined()) Y = make({R, N}, at::kBFloat16, device);
       check(fg_grouped_gemm(A.data_ptr(), scales ? scales->data_ptr() : nullptr, T, rows ? rows->data_ptr<int32_t>() : nullptr, R,
-                            offsets.data_ptr<int32_t>(), (int)E, b, mode, Y.data_ptr(), data(ws), bytes, (uint32_t)flags,
+                            offsets.data_ptr<int32_t>(), (int)E, b, mode, Y.data_ptr(), data(ws), bytes, flags,
                             launch.stream));
       keep(launch, {Y}, {&A, &weight, &offsets, scales, rows, &Y, &ws});
     }
