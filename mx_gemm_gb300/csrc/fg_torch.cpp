@@ -106,6 +106,15 @@ uint32_t flag_bits(PyObject* o, const char* name) {
   return static_cast<uint32_t>(v);
 }
 
+bool truth(PyObject* o, const char* name) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) {
+    PyErr_Clear();
+    refuse("%s must be true or false", name);
+  }
+  return v == 1;
+}
+
 const at::Tensor& tensor(PyObject* o, const char* name) {
   if (!THPVariable_Check(o)) refuse("%s must be a torch.Tensor, got %s", name, Py_TYPE(o)->tp_name);
   const at::Tensor& t = THPVariable_Unpack(o);
@@ -284,7 +293,7 @@ PyObject* rmsnorm_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
       PyErr_Clear();
       refuse("eps must be a number");
     }
-    const bool plain = mode == FG_BF16, normed = plain || PyObject_IsTrue(a[5]) == 1;
+    const bool plain = mode == FG_BF16, normed = truth(a[5], "normed") || plain;
     const Launch launch = launch_of(a[6], device);
     Codes c;
     at::Tensor h, y;
@@ -311,7 +320,7 @@ PyObject* moe_route(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int type = type_of(x, "logits");
     const int64_t k = integer(a[1], "top_k");
     if (k < 1 || k > (r.k > 1 ? r.k : 1)) refuse("top_k=%lld outside 1..%lld", (long long)k, (long long)r.k);
-    const bool renormalize = PyObject_IsTrue(a[2]) == 1;
+    const bool renormalize = truth(a[2], "renormalize");
     const at::Device device = x.device();
     const Launch launch = launch_of(a[3], device);
     at::Tensor weights, experts, offsets, rows, slots, ws;

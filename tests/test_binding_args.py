@@ -27,3 +27,18 @@ def test_flags_that_do_not_fit(value):
     c = Experts("mxfp8_b32", [4, 4, 4], 128, 256, 1)
     with pytest.raises(ValueError, match="flags"):
         c.run(flags=value)
+
+
+class NoTruth:
+    def __bool__(self):
+        raise TypeError("neither")
+
+
+@pytest.mark.gpu
+def test_values_without_a_truth_value():
+    x = torch.randn(4, 256, device="cuda")
+    with pytest.raises(ValueError, match="renormalize"):
+        fg.moe_route(x, 2, renormalize=NoTruth())
+    with pytest.raises(ValueError, match="normed"):
+        fg.rmsnorm_quantize("mxfp8_b32", x, x[0].contiguous(), normed=NoTruth())
+    assert fg.moe_route(x, 2, renormalize=1).experts.shape == (4, 2)
