@@ -750,6 +750,7 @@ fg_status check_grouped(int mode, int64_t R, int E, int64_t N, int64_t K) {
   if (E < 1 || E > kMaxExperts) return fail(FG_ERR_SHAPE, "%s: E=%d outside 1..%d", what, E, kMaxExperts);
   if (R < 0 || R > (int64_t(1) << 24)) return fail(FG_ERR_SHAPE, "%s: R=%lld", what, (long long)R);
   if (N <= 0 || N % 128) return fail(FG_ERR_SHAPE, "%s: N=%lld per expert must be a multiple of 128", what, (long long)N);
+  if (N > (int64_t(1) << 24)) return fail(FG_ERR_SHAPE, "%s: N=%lld per expert is too large", what, (long long)N);
   return check_nk(mode, N * E, K);
 }
 

@@ -526,7 +526,7 @@ extern "C" {
 
 fg_status fg_moe_route_workspace_size(int64_t T, int E, uint64_t* bytes) {
   if (!bytes) return fail(FG_ERR_INVALID_ARG, "null output");
-  if (T < 0 || E < 1 || E > kMaxExperts)
+  if (T < 0 || T > (int64_t(1) << 30) || E < 1 || E > kMaxExperts)
     return fail(FG_ERR_SHAPE, "fg_moe_route: T=%lld, E=%d (1..%d experts)", (long long)T, E, kMaxExperts);
   const int blocks = route_blocks(T);
   *bytes = blocks > 1 ? static_cast<uint64_t>(blocks) * ((E + 3) / 4 * 4) * 4 : 0;
@@ -544,7 +544,7 @@ fg_status fg_moe_route(const void* logits, int type, int64_t T, int E, int64_t l
   if (s != FG_OK) return s;
   if (top_k < 1 || top_k > kMaxTopK || top_k > E)
     return fail(FG_ERR_SHAPE, "%s: top_k=%d outside 1..min(%d, E=%d)", what, top_k, kMaxTopK, E);
-  if (T * top_k > (int64_t(1) << 30)) return fail(FG_ERR_SHAPE, "%s: T=%lld too large", what, (long long)T);
+  if (T > (int64_t(1) << 30) / top_k) return fail(FG_ERR_SHAPE, "%s: T=%lld too large", what, (long long)T);
   if (ldl < E) return fail(FG_ERR_SHAPE, "%s: logit rows %lld apart, shorter than E=%d", what, (long long)ldl, E);
   if (!offsets || (T > 0 && (!logits || !weights || !experts || !rows || !slots)))
     return fail(FG_ERR_INVALID_ARG, "%s: null pointer", what);
