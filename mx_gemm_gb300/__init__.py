@@ -331,10 +331,12 @@ def gemm(A, pb, a_scales=None, mode=None, split_k=0, Y=None, workspace=None, fla
     """
     if mode is None and Y is None and workspace is None and flags == 0 and stream is None:
         # the ordinary call, compiled; None where an argument is amiss, which
-        # the checks below name
-        Y = (moe._binding or moe.binding()).gemm(A, pb.data, ctypes.addressof(pb.desc), a_scales, split_k)
-        if Y is not None:
-            return Y
+        # the checks below name.  Without the binding the same call goes from here.
+        compiled = moe._binding or moe.binding_if_built()
+        if compiled is not None:
+            Y = compiled.gemm(A, pb.data, ctypes.addressof(pb.desc), a_scales, split_k)
+            if Y is not None:
+                return Y
     mode = pb.mode if mode is None else _mode(mode)
     M = _check_gemm_args(mode, A, pb, a_scales, Y)
     N = pb.N

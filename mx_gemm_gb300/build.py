@@ -5,6 +5,9 @@ tensor-map encoder is looked up at run time, so the library needs no
 libcuda at link time.  csrc/fg_torch.cpp, the binding that allocates outputs
 through torch, is compiled beside them with g++ into ``_build/fg_torch.so``,
 which finds libfg.so next to itself and torch's libraries in the process.
+The library does not need it: where it cannot be built (no g++, no headers of
+torch or Python) a warning says why, and the operators that live in it raise
+when they are first called.
 """
 import concurrent.futures as cf
 import glob
@@ -12,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -34,16 +38,24 @@ def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _deps():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.cpp")) + \
-        [os.path.join(os.path.dirname(HERE), "include", "fg.h")]
+def _header():
+    return os.path.join(os.path.dirname(HERE), "include", "fg.h")
+
+
+def _newer(target, deps):
+    return os.path.exists(target) and all(os.path.getmtime(d) <= os.path.getmtime(target) for d in deps)
+
+
+def library_up_to_date():
+    return _newer(LIB, _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [_header()])
+
+
+def binding_up_to_date():
+    return _newer(BINDING, [os.path.join(CSRC, "fg_torch.cpp"), _header()])
 
 
 def up_to_date():
-    if not (os.path.exists(LIB) and os.path.exists(BINDING)):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    return library_up_to_date() and binding_up_to_date()
 
 
 def _run(cmd, what):
@@ -75,8 +87,18 @@ def _link_binding(obj):
     os.replace(tmp, BINDING)
 
 
+def _attempt(step, *args):
+    """What went wrong in a step of the binding's build, or None."""
+    try:
+        step(*args)
+    except Exception as e:  # a missing compiler, header or module: the library is built all the same
+        return e
+    return None
+
+
 def build(force=False, verbose=False):
-    if not force and up_to_date():
+    library, binding = force or not library_up_to_date(), force or not binding_up_to_date()
+    if not (library or binding):
         return LIB
     os.makedirs(OUT, exist_ok=True)
     cc = nvcc()
@@ -92,22 +114,24 @@ def build(force=False, verbose=False):
         return obj, r.stderr
 
     srcs = _sources()
-    binding = os.path.join(OUT, "fg_torch.cpp.o")
+    binding_obj = os.path.join(OUT, "fg_torch.cpp.o")
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
-        other = ex.submit(_compile_binding, binding)
-        results = list(ex.map(compile_one, srcs))
-        other.result()
+        other = ex.submit(_attempt, _compile_binding, binding_obj) if binding else None
+        results = list(ex.map(compile_one, srcs)) if library else []
     if verbose:
         for _, log in results:
             sys.stderr.write(log)
-    tmp = LIB + ".tmp.%d" % os.getpid()
-    cmd = [cc] + ARCH + ["-shared", "-o", tmp] + [o for o, _ in results] + ["-lcudart_static", "-ldl", "-lrt",
-                                                                             "-lpthread"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("link failed:\n%s%s" % (r.stdout, r.stderr))
-    os.replace(tmp, LIB)
-    _link_binding(binding)
+    if library:
+        tmp = LIB + ".tmp.%d" % os.getpid()
+        _run([cc] + ARCH + ["-shared", "-o", tmp] + [o for o, _ in results] + ["-lcudart_static", "-ldl", "-lrt", "-lpthread"],
+             "link")
+        os.replace(tmp, LIB)
+    if binding:
+        wrong = other.result() or _attempt(_link_binding, binding_obj)
+        if wrong is not None:
+            if os.path.exists(BINDING):
+                os.remove(BINDING)  # of other sources
+            warnings.warn("fg_torch.so, the binding of the operators around the GEMM, was not built: %s" % wrong)
     return LIB
 
 

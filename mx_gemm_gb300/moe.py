@@ -44,6 +44,11 @@ def binding():
     return _binding
 
 
+def binding_if_built():
+    """The binding, or None where it has not been built."""
+    return binding() if _binding is not None or os.path.exists(BINDING_PATH) else None
+
+
 def _handle(stream):
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else stream
 
