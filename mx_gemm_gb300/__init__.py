@@ -326,15 +326,15 @@ def gemm(A, pb, a_scales=None, mode=None, split_k=0, Y=None, workspace=None, fla
     A is the device tensor of codes ([M][K] bf16 or uint8, or packed fp4
     [M][K/2]).  A workspace is allocated here when the resolved split needs
     one and none is given.  Returns Y.  On another stream than the current one
-    Y and the workspace come from that stream's memory; the caller orders that
-    stream after the inputs, and keeps them until it has read them.
+    Y and the workspace come from that stream's memory, the caller orders that
+    stream after the inputs and keeps them until it has read them.
     """
-    if mode is None and Y is None and workspace is None and flags == 0 and stream is None:
+    if mode is None and Y is None and workspace is None and flags == 0:
         # the ordinary call, compiled; None where an argument is amiss, which
         # the checks below name.  Without the binding the same call goes from here.
         compiled = moe._binding or moe.binding_if_built()
         if compiled is not None:
-            Y = compiled.gemm(A, pb.data, ctypes.addressof(pb.desc), a_scales, split_k)
+            Y = compiled.gemm(A, pb.data, ctypes.addressof(pb.desc), a_scales, split_k, moe._handle(stream))
             if Y is not None:
                 return Y
     mode = pb.mode if mode is None else _mode(mode)

@@ -477,11 +477,11 @@ PyObject* moe_combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // fg_gemm's ordinary call, (A, weight data, descriptor's address, a_scales or
-// None, split_k) -> Y; None where an argument is not as it should be or needs
+// None, split_k, stream) -> Y; None where an argument is not as it should be or needs
 // more than this, which the caller's own checks then name.
 PyObject* gemm(PyObject*, PyObject* const* v, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
-    arity(n, 5, "gemm");
+    arity(n, 6, "gemm");
     if (!THPVariable_Check(v[0]) || !THPVariable_Check(v[1]) || !PyLong_Check(v[4])) Py_RETURN_NONE;
     const at::Tensor &A = THPVariable_Unpack(v[0]), &weight = THPVariable_Unpack(v[1]);
     const fg_bshuf* b = reinterpret_cast<const fg_bshuf*>(static_cast<intptr_t>(integer(v[2], "the descriptor's address")));
@@ -497,9 +497,11 @@ PyObject* gemm(PyObject*, PyObject* const* v, Py_ssize_t n) {
       Py_RETURN_NONE;
     const int64_t M = A.size(0);
     const void* scales = nullptr;
+    const at::Tensor* a_scales = nullptr;
     if (mode != FG_BF16) {
       if (!THPVariable_Check(v[3])) Py_RETURN_NONE;
       const at::Tensor& s = THPVariable_Unpack(v[3]);
+      a_scales = &s;
       const bool fp32 = mode == FG_FP8_TENSOR || mode == FG_FP8_BLOCK128;
       const int64_t want = mode == FG_FP8_TENSOR ? 1 : M * (K / (mode == FG_MXFP8 || mode == FG_FP8_BLOCK128 ? 128 : 32));
       const at::ScalarType t = s.scalar_type();
@@ -513,15 +515,17 @@ PyObject* gemm(PyObject*, PyObject* const* v, Py_ssize_t n) {
     const long split = PyLong_AsLong(v[4]);
     if (PyErr_Occurred()) return nullptr;
     if (split < 0 || split > 16) Py_RETURN_NONE;
-    void* st = c10::cuda::getCurrentCUDAStream(device.index()).stream();
+    const Launch launch = launch_of(v[5], device);
     at::Tensor Y, ws;
     {
       Unlocked u;
+      Pool pool(launch);
       uint64_t need = 0;
       check(fg_gemm_workspace_size(mode, M, b->N, K, (int)split, &need));
       Y = make({M, b->N}, at::kBFloat16, device);
       if (need) ws = make({static_cast<int64_t>(need)}, at::kByte, device);
-      check(fg_gemm(A.data_ptr(), scales, M, b, mode, (int)split, Y.data_ptr(), data(ws), need, 0, st));
+      check(fg_gemm(A.data_ptr(), scales, M, b, mode, (int)split, Y.data_ptr(), data(ws), need, 0, launch.stream));
+      keep(launch, {Y}, {&A, &weight, a_scales});
     }
     return wrap(Y);
   });
