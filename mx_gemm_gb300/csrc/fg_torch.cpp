@@ -209,10 +209,11 @@ struct Pool {
 // not reused before the current stream, on which the caller uses it (after a
 // wait of its own), is done with it, and that of the caller's tensors not before
 // the call's stream is.
-void keep(const Launch& launch, std::initializer_list<at::Tensor> made, std::initializer_list<const at::Tensor*> given) {
+void keep(const Launch& launch, std::initializer_list<const at::Tensor*> made,
+          std::initializer_list<const at::Tensor*> given) {
   if (!launch.other()) return;
-  for (const at::Tensor& t : made)
-    if (t.defined()) t.record_stream(launch.current.unwrap());
+  for (const at::Tensor* t : made)
+    if (t->defined()) t->record_stream(launch.current.unwrap());
   const auto other = c10::cuda::getStreamFromExternal(launch.stream, launch.current.device_index());
   for (const at::Tensor* t : given)
     if (t && t->defined()) t->record_stream(other.unwrap());
@@ -259,7 +260,7 @@ PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
       c = make_codes(mode, r.m, r.k, device);
       check(fg_quantize(mode, act, x.data_ptr(), type, r.m, r.k, r.ld, c.codes.data_ptr(), c.scales.data_ptr(),
                         launch.stream));
-      keep(launch, {c.codes, c.scales}, {&x});
+      keep(launch, {&c.codes, &c.scales}, {&x});
     }
     return Py_BuildValue("(NN)", wrap(c.codes), wrap(c.scales));
   });
@@ -305,7 +306,7 @@ PyObject* rmsnorm_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (normed) y = make({r.m, r.k}, x.scalar_type(), device);
       check(fg_rmsnorm_quantize(mode, x.data_ptr(), r.ld, res ? res->data_ptr() : nullptr, rr.ld, w.data_ptr(), (float)eps,
                                 type, r.m, r.k, data(h), data(y), data(c.codes), data(c.scales), launch.stream));
-      keep(launch, {c.codes, c.scales, h, y}, {&x, &w, res});
+      keep(launch, {&c.codes, &c.scales, &h, &y}, {&x, &w, res});
     }
     return Py_BuildValue("(NNNN)", wrap(c.codes), wrap(c.scales), wrap(h), wrap(y));
   });
@@ -339,7 +340,7 @@ PyObject* moe_route(PyObject*, PyObject* const* a, Py_ssize_t n) {
                          renormalize ? FG_FLAG_RENORMALIZE : 0, weights.data_ptr<float>(), experts.data_ptr<int32_t>(),
                          offsets.data_ptr<int32_t>(), rows.data_ptr<int32_t>(), slots.data_ptr<int32_t>(), data(ws), need,
                          launch.stream));
-      keep(launch, {weights, experts, offsets, rows, slots}, {&x});
+      keep(launch, {&weights, &experts, &offsets, &rows, &slots}, {&x});
     }
     return Py_BuildValue("(NNNNN)", wrap(weights), wrap(experts), wrap(offsets), wrap(rows), wrap(slots));
   });
@@ -427,7 +428,7 @@ PyObject* grouped_gemm(PyObject*, PyObject* const* v, Py_ssize_t n) {
       check(fg_grouped_gemm(A.data_ptr(), scales ? scales->data_ptr() : nullptr, T, rows ? rows->data_ptr<int32_t>() : nullptr, R,
                             offsets.data_ptr<int32_t>(), (int)E, b, mode, Y.data_ptr(), data(ws), bytes, flags,
                             launch.stream));
-      keep(launch, {Y}, {&A, &weight, &offsets, scales, rows, &Y, &ws});
+      keep(launch, {&Y}, {&A, &weight, &offsets, scales, rows, &Y, &ws});
     }
     return wrap(Y);
   });
@@ -470,7 +471,7 @@ PyObject* moe_combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
       out = make({t, cols}, at::kBFloat16, device);
       check(fg_moe_combine(Y.data_ptr(), Y.size(0), slots.data_ptr<int32_t>(), w.data_ptr<float>(), r ? r->data_ptr() : nullptr, t,
                            (int)(k < 1024 ? k : 1024), cols, out.data_ptr(), launch.stream));
-      keep(launch, {out}, {&Y, &slots, &w, r});
+      keep(launch, {&out}, {&Y, &slots, &w, r});
     }
     return wrap(out);
   });
@@ -525,7 +526,7 @@ PyObject* gemm(PyObject*, PyObject* const* v, Py_ssize_t n) {
       Y = make({M, b->N}, at::kBFloat16, device);
       if (need) ws = make({static_cast<int64_t>(need)}, at::kByte, device);
       check(fg_gemm(A.data_ptr(), scales, M, b, mode, (int)split, Y.data_ptr(), data(ws), need, 0, launch.stream));
-      keep(launch, {Y}, {&A, &weight, a_scales});
+      keep(launch, {&Y}, {&A, &weight, a_scales});
     }
     return wrap(Y);
   });
