@@ -22,6 +22,7 @@ CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT, "libfg.so")
 BINDING = os.path.join(OUT, "fg_torch.so")
+MADE_FOR = os.path.join(OUT, "fg_torch.made_for")  # the torch and Python that the binding was compiled against
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-Xcompiler", "-fvisibility=hidden"]
@@ -50,8 +51,23 @@ def library_up_to_date():
     return _newer(LIB, _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [_header()])
 
 
+def running():
+    """The torch and Python of this process, as the binding's build records them."""
+    import torch
+    return "torch %s, Python %d.%d\n" % (torch.__version__, sys.version_info[0], sys.version_info[1])
+
+
+def made_for():
+    """What the binding was compiled against (None: not recorded)."""
+    try:
+        with open(MADE_FOR, encoding="utf-8") as f:
+            return f.read()
+    except OSError:
+        return None
+
+
 def binding_up_to_date():
-    return _newer(BINDING, [os.path.join(CSRC, "fg_torch.cpp"), _header()])
+    return _newer(BINDING, [os.path.join(CSRC, "fg_torch.cpp"), _header()]) and made_for() == running()
 
 
 def up_to_date():
@@ -85,6 +101,8 @@ def _link_binding(obj):
     _run(["g++", "-shared", "-o", tmp, obj, "-L" + OUT, "-l:libfg.so", "-Wl,-rpath,$ORIGIN", "-L" + libs, "-ltorch_python",
           "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-lc10", "-lc10_cuda"], "link of fg_torch.so")
     os.replace(tmp, BINDING)
+    with open(MADE_FOR, "w", encoding="utf-8") as f:
+        f.write(running())
 
 
 def _attempt(step, *args):

@@ -20,6 +20,7 @@ from typing import NamedTuple
 import torch
 
 import mx_gemm_gb300 as _fg
+from mx_gemm_gb300 import build
 
 BINDING_PATH = os.path.join(_fg.HERE, "_build", "fg_torch.so")
 FG_TYPE_F32, FG_TYPE_BF16 = 0, 1
@@ -30,11 +31,14 @@ _binding = None
 
 
 def binding():
-    """Load fg_torch.so (raises if it was not built)."""
+    """Load fg_torch.so (raises if it was not built, or for another torch)."""
     global _binding
     if _binding is None:
         if not os.path.exists(BINDING_PATH):
             raise RuntimeError("fg_torch.so is not built (%s); run mx_gemm_gb300.build.build()" % BINDING_PATH)
+        if build.made_for() != build.running():  # it would be read with the wrong layouts of torch's classes
+            raise RuntimeError("fg_torch.so was built for %s, this is %s; run mx_gemm_gb300.build.build()"
+                               % ((build.made_for() or "another torch").strip(), build.running().strip()))
         _fg.lib()
         spec = importlib.util.spec_from_file_location("fg_torch", BINDING_PATH)
         module = importlib.util.module_from_spec(spec)
@@ -45,8 +49,10 @@ def binding():
 
 
 def binding_if_built():
-    """The binding, or None where it has not been built."""
-    return binding() if _binding is not None or os.path.exists(BINDING_PATH) else None
+    """The binding, or None where it has not been built, or for another torch."""
+    if _binding is None and not (os.path.exists(BINDING_PATH) and build.made_for() == build.running()):
+        return None
+    return binding()
 
 
 def _handle(stream):

@@ -25,7 +25,7 @@ def compilers(monkeypatch, tmp_path):
 
     monkeypatch.setattr(build.subprocess, "run", run)
     monkeypatch.setattr(build, "nvcc", lambda: "/usr/local/cuda/bin/nvcc")
-    for name, path in (("OUT", ""), ("LIB", "libfg.so"), ("BINDING", "fg_torch.so")):
+    for name, path in (("OUT", ""), ("LIB", "libfg.so"), ("BINDING", "fg_torch.so"), ("MADE_FOR", "fg_torch.made_for")):
         monkeypatch.setattr(build, name, str(tmp_path / path) if path else str(tmp_path))
     return rec
 
@@ -50,6 +50,23 @@ def test_the_library_is_built_where_the_binding_cannot_be(compilers, broken):
     with pytest.warns(UserWarning):
         build.build()                                   # the library is not compiled again
     assert not any("nvcc" in c[0] for c in compilers.commands[n:])
+
+
+def test_a_binding_made_for_another_torch_is_stale(compilers, monkeypatch):
+    build.build()
+    n = len(compilers.commands)
+    monkeypatch.setattr(torch, "__version__", "2.0.0+other")
+    assert build.library_up_to_date() and not build.binding_up_to_date() and not build.up_to_date()
+    build.build()                                       # the binding alone
+    assert {c[0] for c in compilers.commands[n:]} == {"g++"} and build.up_to_date()
+
+
+def test_a_binding_made_for_another_torch_is_not_loaded(monkeypatch):
+    monkeypatch.setattr(fg.moe, "_binding", None)
+    monkeypatch.setattr(torch, "__version__", "2.0.0+other")
+    with pytest.raises(RuntimeError, match="2.0.0.other"):
+        fg.moe.binding()
+    assert fg.moe.binding_if_built() is None
 
 
 def test_a_library_that_does_not_compile_is_an_error(compilers):
