@@ -278,17 +278,34 @@ def _code_only(text):
     return tok.sub(lambda m: m.group(0) if m.group(0).startswith('"') else "", text)
 
 
+# What the timed GEMM is compiled from: its kernels and its dispatch, with the
+# headers they include.
+GEMM_UNITS = ("fg_api.cu", "fg_decode.cu", "fg_large.cu", "fg_large_pair.cu", "fg_relayout.cu")
+
+
+def gemm_sources(csrc):
+    """Names of GEMM_UNITS and of the headers in csrc that they include."""
+    import re
+    names, todo = set(), list(GEMM_UNITS)
+    while todo:
+        name = todo.pop()
+        if name not in names:
+            names.add(name)
+            text = open(os.path.join(csrc, name), encoding="utf-8").read()
+            todo += [h for h in re.findall(r'^\s*#\s*include\s+"([^"/]+)"', text, re.M)]
+    return sorted(names)
+
+
 def kernel_sources_digest(fg):
-    """Digest of the library's kernel sources (code only, comments and
-    whitespace ignored), to tell whether a stored ncu traffic figure still
-    describes the kernels being timed."""
+    """Digest of the GEMM's sources (code only, comments and whitespace
+    ignored), to tell whether a stored ncu traffic figure still describes the
+    kernels being timed."""
     import hashlib
     h = hashlib.sha256()
     csrc = os.path.join(os.path.dirname(fg.__file__), "csrc")
-    for name in sorted(os.listdir(csrc)):
-        if name.endswith((".cu", ".cuh")):
-            h.update(name.encode())
-            h.update(_code_only(open(os.path.join(csrc, name), encoding="utf-8").read()).encode())
+    for name in gemm_sources(csrc):
+        h.update(name.encode())
+        h.update(_code_only(open(os.path.join(csrc, name), encoding="utf-8").read()).encode())
     return h.hexdigest()[:16]
 
 
