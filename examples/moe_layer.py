@@ -22,9 +22,7 @@ import mx_gemm_gb300 as fg  # noqa: E402
 
 
 def _weight(mode, w):
-    """Preshuffled weight of fp32 / bf16 w [N][K]."""
-    if mode == "bf16":
-        return fg.preshuffle_b(mode, w.to(torch.bfloat16))
+    """Preshuffled weight of fp32 / bf16 w [N][K] in an MX mode."""
     return fg.preshuffle_b(mode, *fg.quantize("mxfp4" if mode == "mxfp4_fp8a" else mode, w))
 
 

@@ -391,6 +391,8 @@ FG_API fg_status fg_moe_combine(const void* Y, int64_t R, const int32_t* slots, 
  * Synchronises the current device and returns (and clears) the error word
  * the library's kernels write when a bounded wait runs out: FG_OK or
  * FG_ERR_TIMEOUT.  A failed synchronisation returns FG_ERR_CUDA.
+ * After FG_ERR_TIMEOUT capture launches of fg_gemm anew before replaying them
+ * (partials of its large-M form that were not taken stay marked as present).
  */
 FG_API fg_status fg_get_error(void);
 

@@ -823,7 +823,6 @@ fg_status fg_grouped_gemm(const void* A, const void* a_scales, int64_t T, const 
   p.offsets = offsets;
   p.rows = rows;
   p.y = static_cast<__nv_bfloat16*>(Y);
-  p.a_sf = ws;
   p.part = reinterpret_cast<float*>(ws);
   p.tickets = reinterpret_cast<unsigned long long*>(ws + g.part_bytes);
   p.epoch = next_epoch() & ((1ull << 48) - 1);

@@ -22,7 +22,6 @@ struct GroupedParams {
   const int32_t* offsets;     // [E + 1]
   const int32_t* rows;        // [R] or null
   __nv_bfloat16* y;           // [R][N]
-  const uint8_t* a_sf;        // TT = 256, MX: token scale atoms [tile][K step][atom][128-row block][512]
   float* part;                // [blocks][2][TT][128] partials (cut line)
   unsigned long long* tickets;  // [blocks] arrivals at the unit that begins last in the block
   unsigned long long epoch;
