@@ -6,9 +6,11 @@
 // reads both again: at n = 208 that is 86 KB through a 128-byte port, 670
 // cycles, while the tensor core needs 410.  On a pair the tokens are staged
 // half by each SM and the hardware hands each half to both (cta_group::2), so
-// an SM moves 58 KB: 450 cycles.  Measured, 64 experts, 4096 x 7168, 32768 rows:
-// mxfp4 438 us one-SM, 332 now (5.8 PFLOP/s); 32-K mxfp8 795, 640 (3.0); fp8 x fp4
-// 749, 595; bf16 (32 experts, 16384 rows) 725, 596 (1.6, at the power limit).  A
+// an SM moves 58 KB: 450 cycles.  Measured, 64 experts, 4096 x 7168, 32768 rows
+// that lie in place, unevenly routed (the whole call): mxfp4 438 us one-SM, 333 now
+// (5.8 PFLOP/s; 293 where all experts have as many rows); 32-K mxfp8 795, 659 (2.9);
+// fp8 x fp4 749, 606; bf16 (32 experts, 16384 rows) 725, 617 (1.6, at the power limit).
+// Rows gathered by index cost their layout on top: mxfp4 375 to 385 us.  A
 // step takes 520 (bf16) to 640 (mxfp4) cycles, the tensor pipe busy for 430 of
 // them; the rest is the issue of the scale copies and the barriers.  With 64 rows
 // an expert the weights' bytes bound it: mxfp8 301 us, 6.65 TB/s.

@@ -11,7 +11,7 @@
 // merge; up to 256 experts); then top_k times the warp takes the largest head
 // (one reduction for 16-bit logits, two for 32-bit ones) and its lane moves up.
 // Against scanning the lane's keys anew for each choice this took 16383 x 256
-// from 29 us to 11 for this kernel (16.7 us with the second, where 10 MB of HBM
+// from 29 us to 11 for this kernel (16.5 us with the second, where 10 MB of HBM
 // would take 1.6): it is bound by instructions, 475 a token and warp.  One token
 // is bound by the call: 7 us of host time, 2 to 3 of them the launch.
 //

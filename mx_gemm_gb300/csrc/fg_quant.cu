@@ -192,7 +192,7 @@ __device__ __forceinline__ void swiglu2(float& v0, float& v1, float u0, float u1
 
 // Threads (x, y) of a block take eight values of each of ROWS rows, blockDim.y
 // apart: no division, and a warp's lanes never split a scale block.  With many
-// rows a thread takes two: swiglu of 32761 x 2048 in 49.8 us (6.8 TB/s; 52.3 with
+// rows a thread takes two: swiglu of 32761 x 2048 in 49.9 us (6.8 TB/s; 52.3 with
 // four rows, 64.8 with eight, whose loads crowd out other blocks).
 template <int MODE, int ACT, int ROWS, typename T>
 __global__ void __launch_bounds__(256) quantize_kernel(const T* __restrict__ x, int64_t M, int64_t K, int64_t ldx,
