@@ -387,6 +387,128 @@ FG_API fg_status fg_grouped_gemm(const void* A, const void* a_scales, int64_t T,
 FG_API fg_status fg_moe_combine(const void* Y, int64_t R, const int32_t* slots, const float* weights,
                                 const void* residual, int64_t T, int top_k, int64_t N, void* out, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Training a mixture-of-experts layer in 8 bits: what its backward pass needs
+ * beside the products above.  Input gradients are grouped products with the
+ * transposed weight; weight gradients sum over rows, which their operands are
+ * quantised along ("column operands"); activations are kept as 8-bit codes and
+ * scales.  Codes and scales stand for code * scale, rounded to 32 bits.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Codes and scales of E weights w [N][K] (rows ldw, weights `stride` elements
+ * apart) in FP8_BLOCK128's 128 x 128 blocks, ready for fg_preshuffle_b: scale =
+ * amax / 448 (as fg_quantize rounds it; 1 for an all-zero block), code = RNE(w /
+ * scale); a block with a NaN or an infinity gets a NaN scale and zero codes.
+ *  transpose  0: codes [E * N][K], scales [E * N/128][K/128]; else of the
+ *             transposed weights: codes [E * K][N], scales [E * K/128][N/128].
+ * Errors: INVALID_ARG (another mode: fg_quantize does its rows), SHAPE (N or K not
+ * a multiple of 128), ALIGN (w and its rows 16 bytes), UNSUPPORTED_ARCH, CUDA.
+ */
+FG_API fg_status fg_quantize_weight(int mode, const void* w, int type, int E, int64_t N, int64_t K, int64_t ldw,
+                                    int64_t stride, int transpose, void* codes, void* scales, void* stream);
+
+/*
+ * fg_quantize of silu(g) * u, x's rows being (g, u), and in the same pass the
+ * checkpoint of the backward pass: codes and scales of the rows themselves
+ * (saved [M][2K]).  mode: MXFP8, MXFP8_B32, MXFP4_FP8A (its activations) or
+ * FP8_BLOCK128.  Errors as fg_quantize.
+ */
+FG_API fg_status fg_swiglu_checkpoint(int mode, const void* x, int type, int64_t M, int64_t K, int64_t ldx, void* codes,
+                                      void* scales, void* saved, void* saved_scales, void* stream);
+
+/*
+ * Sizes of a column operand of C columns (a multiple of 128) for R rows of E
+ * experts: `places` P = 128 * max(1, R / 128 + min(E, R)), at most 2^20.  Every
+ * expert's rows begin a new slab of 128 places, the rest of its last slab and the
+ * slabs behind the last expert hold zeros.  data and sf are the weight image and
+ * the scale image of an MXFP8_B32 matrix [C][P] (see fg_bshuf): e4m3 codes and one
+ * E8M0 for each column and 32 places; fg_unshuffle_b gives the plain matrix.
+ */
+FG_API fg_status fg_columns_size(int64_t C, int64_t R, int E, int64_t* places, uint64_t* data_bytes, uint64_t* sf_bytes);
+
+/*
+ * Column operand of x's rows: row rows[i] of x [T][C] (clamped into 0..T-1; rows
+ * NULL: row i) is row i of the expert e with offsets[e] <= i < offsets[e+1]
+ * (offsets as for fg_grouped_gemm; NULL with E = 1: one expert with all R rows).
+ *  mode    FG_BF16: x holds values of `type`, rows ldx apart, scales NULL; else x
+ *          holds e4m3 codes (ldx = C) with scales as fg_quantize gives them for
+ *          MXFP8, MXFP8_B32, MXFP4_FP8A or FP8_BLOCK128.
+ * Scales and codes as fg_quantize's 32-blocks, along the places.  Errors:
+ * INVALID_ARG, SHAPE, ALIGN, UNSUPPORTED_ARCH, CUDA.
+ */
+FG_API fg_status fg_quantize_columns(int mode, const void* x, const void* scales, int type, int64_t T, int64_t C,
+                                     int64_t ldx, const int32_t* rows, int64_t R, const int32_t* offsets, int E,
+                                     void* data, void* sf, fg_bshuf* desc_out, void* stream);
+
+/*
+ * Backward pass of y = silu(g) * u from the checkpoint's g and u, for the gradient
+ * dy [R][K] of the experts' rows (type fp32 or bf16, rows ldd apart).  With s = 1 /
+ * (1 + exp(-g)) and w the row's routing weight (1 without weights), in 32 bits:
+ *   dg = w dy u s (1 + g (1 - s)),  du = w dy g s,  act = g s u.
+ *  codes, scales  of (dg, du) [R][2K] in `mode`, which is the checkpoint's too;
+ *  dx             (dg, du) in dy's type (NULL: not wanted);
+ *  dx_data .. dx_desc, act_data .. act_desc  column operands of (dg, du) (2K
+ *                 columns) and of w * act (K columns) by the offsets (all NULL: none);
+ *  weights, rows, slots, T, top_k  as fg_moe_route gives them (all NULL: no
+ *                 weights); then dweights [T][top_k] = sum_i dy[slot][i] act[slot][i]
+ *                 (0 where there is no choice), the gradient of the weights that
+ *                 fg_moe_combine takes;
+ *  offsets        [E + 1] (NULL with E = 1: all rows).  Rows of no expert are not
+ *                 read; their codes and dx are zero, their scales 127 (fp32: 1).
+ *  workspace      fg_swiglu_backward_workspace_size bytes (weighted: weights given).
+ * Errors: INVALID_ARG, SHAPE (K not a multiple of the block, or of 128 with
+ * columns), ALIGN, WORKSPACE, UNSUPPORTED_ARCH, CUDA.
+ */
+FG_API fg_status fg_swiglu_backward_workspace_size(int64_t R, int64_t K, int weighted, uint64_t* bytes);
+FG_API fg_status fg_swiglu_backward(int mode, const void* dy, int type, int64_t R, int64_t K, int64_t ldd, const void* saved,
+                                    const void* saved_scales, const float* weights, const int32_t* rows,
+                                    const int32_t* slots, int64_t T, int top_k, const int32_t* offsets, int E, void* codes,
+                                    void* scales, void* dx, float* dweights, void* dx_data, void* dx_sf, fg_bshuf* dx_desc,
+                                    void* act_data, void* act_sf, fg_bshuf* act_desc, void* workspace,
+                                    uint64_t workspace_bytes, void* stream);
+
+/*
+ * Weight gradients grouped by expert: out[e][n][k] = the sum over the rows i of
+ * expert e of a[i][n] * b[i][k], fp32 accumulation, for column operands a and b
+ * (N and K columns) of the same offsets, R and E.  out [E][N][K] in fp32 or bf16;
+ * accumulate: fp32 out is added to.  An expert without rows has gradient 0.
+ * Errors: INVALID_ARG, SHAPE (operands of another R or E), ALIGN, LAYOUT,
+ * UNSUPPORTED_ARCH, CUDA.
+ */
+FG_API fg_status fg_grouped_wgrad(const fg_bshuf* a, const fg_bshuf* b, const int32_t* offsets, int64_t R, int E, int type,
+                                  int accumulate, void* out, uint32_t flags, void* stream);
+
+/* Workspace of fg_moe_balance_loss: 0 for few tokens, else the blocks' sums. */
+FG_API fg_status fg_moe_balance_loss_workspace_size(int64_t T, int E, uint64_t* bytes);
+
+/*
+ * Balance loss of a routing: with p = softmax of a token's logits (0 where there is
+ * nothing to pick; NaN counts as -infinity), T' the tokens that have something to
+ * pick, counts[e] = offsets[e+1] - offsets[e] (0 where that is negative) and f_e
+ * their share of all counts:
+ *   probs[e] = sum_t p_te / T',  loss = coefficient * E * sum_e f_e probs[e],
+ *   slopes[e] = coefficient * E * f_e / T', the loss's derivative by each p_te.
+ * Errors: INVALID_ARG, SHAPE, ALIGN, WORKSPACE, UNSUPPORTED_ARCH, CUDA.
+ */
+FG_API fg_status fg_moe_balance_loss(const void* logits, int type, int64_t T, int E, int64_t ldl, const int32_t* offsets,
+                                     float coefficient, float* loss, int32_t* counts, float* probs, float* slopes,
+                                     void* workspace, uint64_t workspace_bytes, void* stream);
+
+/*
+ * Gradient of the logits (out [T][E], their type) from the gradients dweights
+ * [T][top_k] of the routing weights of `experts` (both as fg_moe_route orders them;
+ * NULL: none; expert -1 is no choice) and the balance loss's slopes (NULL: none):
+ *   out[t][e] = p_te (slopes[e] - sum_i p_ti slopes[i])
+ *             + q_j (dweights[t][j] - sum_i q_i dweights[t][i])   where e = experts[t][j],
+ * q being the softmax over the chosen experts with FG_FLAG_RENORMALIZE; without it
+ * q_j = p_te, and the last sum is subtracted from every p_te's factor instead.
+ * Errors: INVALID_ARG, SHAPE, ALIGN, UNSUPPORTED_ARCH, CUDA.
+ */
+FG_API fg_status fg_moe_route_backward(const void* logits, int type, int64_t T, int E, int64_t ldl, const int32_t* experts,
+                                       const float* dweights, int top_k, const float* slopes, uint32_t flags, void* out,
+                                       void* stream);
+
 /*
  * Synchronises the current device and returns (and clears) the error word
  * the library's kernels write when a bounded wait runs out: FG_OK or

@@ -74,6 +74,17 @@ def lib():
         "fg_moe_combine": ([vp, i64, vp, vp, vp, i64, i32, i64, vp, vp], i32),
         "fg_grouped_gemm_workspace_size": ([i32, i64, i32, i64, i64, i32, ctypes.POINTER(u64)], i32),
         "fg_grouped_gemm": ([vp, vp, i64, vp, i64, vp, i32, ctypes.POINTER(BShuf), i32, vp, vp, u64, u32, vp], i32),
+        "fg_quantize_weight": ([i32, vp, i32, i32, i64, i64, i64, i64, i32, vp, vp, vp], i32),
+        "fg_swiglu_checkpoint": ([i32, vp, i32, i64, i64, i64, vp, vp, vp, vp, vp], i32),
+        "fg_columns_size": ([i64, i64, i32, ctypes.POINTER(i64), ctypes.POINTER(u64), ctypes.POINTER(u64)], i32),
+        "fg_quantize_columns": ([i32, vp, vp, i32, i64, i64, i64, vp, i64, vp, i32, vp, vp, ctypes.POINTER(BShuf), vp], i32),
+        "fg_swiglu_backward_workspace_size": ([i64, i64, i32, ctypes.POINTER(u64)], i32),
+        "fg_swiglu_backward": ([i32, vp, i32, i64, i64, i64, vp, vp, vp, vp, vp, i64, i32, vp, i32, vp, vp, vp, vp, vp, vp,
+                                ctypes.POINTER(BShuf), vp, vp, ctypes.POINTER(BShuf), vp, u64, vp], i32),
+        "fg_grouped_wgrad": ([ctypes.POINTER(BShuf), ctypes.POINTER(BShuf), vp, i64, i32, i32, i32, vp, u32, vp], i32),
+        "fg_moe_balance_loss_workspace_size": ([i64, i32, ctypes.POINTER(u64)], i32),
+        "fg_moe_balance_loss": ([vp, i32, i64, i32, i64, vp, ctypes.c_float, vp, vp, vp, vp, vp, u64, vp], i32),
+        "fg_moe_route_backward": ([vp, i32, i64, i32, i64, vp, vp, i32, vp, u32, vp, vp], i32),
         "fg_get_error": ([], i32),
         "fg_set_wait_timeout_ns": ([u64], None),
         "fg_debug_override_cc": ([i32, i32], None),
@@ -387,3 +398,7 @@ def gemm_splitk_reduce(ws, split_k, M, N, a_s=None, b_s=None, Y=None, stream=Non
 from . import moe  # noqa: E402
 from .moe import (FG_ACT_NONE, FG_ACT_SWIGLU, FG_TYPE_BF16, FG_TYPE_F32, Routing, grouped_gemm,  # noqa: E402,F401
                   grouped_gemm_workspace_size, moe_combine, moe_route, quantize, rmsnorm_quantize)
+from . import train  # noqa: E402
+from .train import (Balance, Columns, SwigluGrad, columns_size, grouped_wgrad, moe_balance_loss,  # noqa: E402,F401
+                    moe_balance_loss_workspace_size, moe_route_backward, quantize_columns, quantize_weight, swiglu_backward,
+                    swiglu_backward_workspace_size, swiglu_checkpoint)

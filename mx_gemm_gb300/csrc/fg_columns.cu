@@ -1,0 +1,768 @@
+// What the backward pass of an 8-bit layer lays out: weights in 128 x 128 blocks,
+// as they are or transposed; activations as column operands (fg_columns.cuh); and
+// the gated activation's gradient from its 8-bit checkpoint, which leaves both
+// forms at once.
+//
+// Squares.  A warp takes 32 rows x 32 columns: thread (tl, fl) = (lane / 4, lane %
+// 4) rows 4 tl .. + 3 and columns 8 fl .. + 7.  A block of 32 values along either
+// side then lies in one warp.  Its largest magnitude is found by halves: in each
+// exchange a lane gives away the candidates of the half that it does not keep, so
+// seven shuffles leave one column's maximum in each lane (three for rows), and
+// the scale is worked out once, not by every lane.  Eight values along a row are
+// eight bytes of codes, four along a column one word of the transposed image: the
+// transposition costs nothing, the pairs of values that are rounded together are
+// only others.  All stores fill whole 32-byte sectors.
+#include <cuda_bf16.h>
+
+#include "fg_columns.cuh"
+#include "fg_internal.cuh"
+#include "fg_values.cuh"
+
+namespace fg {
+
+namespace {
+
+constexpr int kMaxExperts = 1024;
+constexpr int kMaxTopK = 32;
+constexpr int kWide = 128;    // columns of a block of threads: four squares side by side
+constexpr int kThreads = 128;
+
+using Square = float[4][8];  // a thread's part of one
+
+// ------------------------------------------------------------------ inputs
+
+enum Format { kF32Rows, kBf16Rows, kE8m0By32, kE8m0By128, kF32By128 };
+
+struct Source {
+  const void* x;
+  const void* scales;
+  int64_t ld;    // elements from row to row
+  int64_t cols;
+};
+
+// Eight consecutive values of a row on their way.
+template <int FMT>
+struct Eight {
+  uint2 codes;
+  float scale;
+  __device__ __forceinline__ void load(const Source& s, int64_t row, int64_t col) {
+    codes = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(s.x) + row * s.ld + col));
+    if (FMT == kF32By128)
+      scale = __ldg(static_cast<const float*>(s.scales) + row * (s.cols / 128) + col / 128);
+    else if (FMT == kE8m0By128)
+      scale = e8m0_up(__ldg(static_cast<const uint8_t*>(s.scales) + row * (s.cols / 128) + col / 128));
+    else
+      scale = e8m0_up(__ldg(static_cast<const uint8_t*>(s.scales) + row * (s.cols / 32) + col / 32));
+  }
+  __device__ __forceinline__ void zero() {
+    codes = make_uint2(0, 0);
+    scale = 1.f;
+  }
+  __device__ __forceinline__ void widen(float (&v)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      const uint32_t w = j < 4 ? codes.x : codes.y;
+      const float2 f = e4m3_values(w >> (8 * (j & 3)));
+      v[j] = f.x;
+      v[j + 1] = f.y;
+      mul2(v[j], v[j + 1], scale, scale);
+    }
+  }
+};
+
+template <typename T>
+struct PlainEight {
+  Raw8<T> raw;
+  __device__ __forceinline__ void load(const Source& s, int64_t row, int64_t col) {
+    raw.load_once(static_cast<const T*>(s.x) + row * s.ld + col);
+  }
+  __device__ __forceinline__ void zero() { raw.zero(); }
+  __device__ __forceinline__ void widen(float (&v)[8]) const { raw.widen(v); }
+};
+
+template <>
+struct Eight<kBf16Rows> : PlainEight<__nv_bfloat16> {};
+template <>
+struct Eight<kF32Rows> : PlainEight<float> {};
+
+// ----------------------------------------------------------- column stores
+
+struct Image {
+  uint8_t* data;  // null: not wanted
+  uint8_t* sf;
+  int slabs;      // of a row of 128 columns
+};
+
+__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// One exchange by halves: of the candidates m[0 .. 2 n) a lane keeps the first n,
+// or with bit `bit` of its index the others.
+template <int N>
+__device__ __forceinline__ void halve(uint32_t* m, int bit) {
+  const bool upper = (threadIdx.x & bit) != 0;
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const uint32_t give = upper ? m[j] : m[j + N], keep = upper ? m[j + N] : m[j];
+    m[j] = max(keep, __shfl_xor_sync(0xffffffffu, give, bit));
+  }
+}
+
+// The warp's square as 32 columns x 32 places: columns f0 .. + 31, places 32 b .. of
+// slab `slab`.  The scale's byte goes into byte b of `word`, for the column that
+// this lane keeps.
+__device__ __forceinline__ void store_columns(const Square& v, const Image& im, int f0, int slab, int b, uint32_t& word) {
+  const int lane = threadIdx.x & 31, tl = lane >> 2, fl = lane & 3;
+  uint32_t m[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    m[j] = max(max(magnitude(v[0][j]), magnitude(v[1][j])), max(magnitude(v[2][j]), magnitude(v[3][j])));
+  halve<4>(m, 16);
+  halve<2>(m, 8);
+  halve<1>(m, 4);
+  const bool finite = m[0] < 0x7f800000u;
+  const int c = finite ? e8m0_of(m[0]) : 255;
+  word |= static_cast<uint32_t>(c) << (8 * b);
+  const float mine = e8m0_down(finite ? c : 127);
+  const bool whole = __all_sync(0xffffffffu, finite);
+  const int row = (f0 & 127) + fl * 8;
+  uint8_t* out = im.data + (static_cast<size_t>(f0 >> 7) * im.slabs + slab) * kColumnSlab + row * 128 + (tl & 3) * 4;
+  const int piece = 2 * b + (tl >> 2);  // 16-byte piece of a column's places
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    // the lane that kept column j: bits 16, 8, 4 of its index are those of j
+    const int owner = ((j & 4) << 2) | ((j & 2) << 2) | ((j & 1) << 2) | fl;
+    const float f = __shfl_sync(0xffffffffu, mine, owner);
+    float a[4] = {v[0][j], v[1][j], v[2][j], v[3][j]};
+    if (!whole) {
+      const bool ok = __shfl_sync(0xffffffffu, static_cast<int>(finite), owner) != 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[i] = ok ? a[i] : 0.f;
+    }
+    mul2(a[0], a[1], f, f);
+    mul2(a[2], a[3], f, f);
+    *reinterpret_cast<uint32_t*>(out + j * 128 + ((piece ^ j) << 4)) = e4m3x2(a[0], a[1]) | (e4m3x2(a[2], a[3]) << 16);
+  }
+}
+
+// 32 places of zeros.
+__device__ __forceinline__ void store_no_columns(const Image& im, int f0, int slab, int b, uint32_t& word) {
+  const int lane = threadIdx.x & 31;
+  uint8_t* out = im.data + (static_cast<size_t>(f0 >> 7) * im.slabs + slab) * kColumnSlab + (f0 & 127) * 128;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int row = 16 * h + (lane >> 1), piece = 2 * b + (lane & 1);
+    *reinterpret_cast<uint4*>(out + row * 128 + ((piece ^ (row & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+  }
+  word |= 127u << (8 * b);
+}
+
+// The scales of the column that this lane kept, a slab's four blocks of places.
+__device__ __forceinline__ void store_atoms(const Image& im, int f0, int slab, uint32_t word) {
+  const int lane = threadIdx.x & 31;
+  const int j = ((lane >> 4) & 1) * 4 + ((lane >> 3) & 1) * 2 + ((lane >> 2) & 1);
+  const int f = f0 + (lane & 3) * 8 + j;
+  uint8_t* atom = im.sf + (static_cast<size_t>(f >> 7) * im.slabs + slab) * 512;
+  *reinterpret_cast<uint32_t*>(atom + 16 * (f & 31) + 4 * ((f & 127) >> 5)) = word;
+}
+
+// ------------------------------------------------------- quantise to columns
+
+struct ColumnsParams {
+  Source in;
+  const int32_t* offsets;
+  const int32_t* rows;  // null: row i itself
+  Image image;
+  int T, R, E;
+};
+
+// A block of threads takes one slab's 128 places x 128 columns, 32 places at a time.
+template <int FMT>
+__global__ void __launch_bounds__(kThreads) columns_kernel(const ColumnsParams p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tl = lane >> 2, fl = lane & 3;
+  const int slab = blockIdx.y, f0 = blockIdx.x * kWide + warp * 32;
+  const SlabRows q = slab_rows(p.offsets, p.R, p.E, slab);
+  uint32_t word = 0;
+#pragma unroll 1
+  for (int b = 0; b < 4; ++b) {
+    if (32 * b >= q.count) {
+      store_no_columns(p.image, f0, slab, b, word);
+      continue;
+    }
+    Eight<FMT> raw[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int at = 32 * b + 4 * tl + i;
+      raw[i].zero();
+      if (at < q.count) {
+        int64_t row = q.row0 + at;
+        if (p.rows) row = min(max(__ldg(p.rows + row), 0), p.T - 1);
+        raw[i].load(p.in, row, f0 + fl * 8);
+      }
+    }
+    Square v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) raw[i].widen(v[i]);
+    store_columns(v, p.image, f0, slab, b, word);
+  }
+  store_atoms(p.image, f0, slab, word);
+}
+
+// ------------------------------------------------ gated activation, backward
+
+struct SwigluParams {
+  Source dy;              // [R][K]
+  Source saved;           // [R][2 K]
+  const float* weights;   // [T][k] (null: none)
+  const int32_t* rows;    // [R]
+  const int32_t* slots;   // [T][k]
+  const int32_t* offsets;
+  uint8_t* codes;         // [R][2 K]
+  void* scales;
+  void* dx;               // [R][2 K] (null: not wanted)
+  float* dots;            // [R][blocks of columns] (weights given)
+  Image dx_image, act_image;
+  int T, R, E, K, k;
+};
+
+constexpr int row_block(int fmt) { return fmt == kE8m0By32 ? 32 : 128; }
+
+// Codes and scales of the warp's square along its rows, at column `col0` of the
+// [R][2 K] output; row0: the square's first row, `rows` of them.  Scale blocks of
+// 128 take the maximum over the four warps, through `part` [4][32].
+template <int FMT>
+__device__ __forceinline__ void store_rows(const Square& v, const SwigluParams& p, int row0, int rows, int64_t col0,
+                                           uint32_t (*part)[32]) {
+  const int lane = threadIdx.x & 31, tl = lane >> 2, fl = lane & 3;
+  uint32_t m[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    m[i] = magnitude(v[i][0]);
+#pragma unroll
+    for (int j = 1; j < 8; ++j) m[i] = max(m[i], magnitude(v[i][j]));
+  }
+  halve<2>(m, 1);
+  halve<1>(m, 2);
+  const int keep = ((lane & 1) << 1) | ((lane >> 1) & 1);  // row 4 tl + keep's maximum is here
+  const int mine = 4 * tl + keep;
+  if (FMT != kE8m0By32) {
+    part[threadIdx.x >> 5][mine] = m[0];
+    __syncthreads();
+    m[0] = max(max(part[0][mine], part[1][mine]), max(part[2][mine], part[3][mine]));
+  }
+  const bool finite = m[0] < 0x7f800000u;
+  const int64_t cols = 2 * static_cast<int64_t>(p.K);
+  const int64_t block = (row0 + mine) * (cols / row_block(FMT)) + col0 / row_block(FMT);
+  const bool stores = mine < rows && (FMT == kE8m0By32 || threadIdx.x < 32);
+  float scale;  // what values are multiplied by (E8M0) or divided by
+  if (FMT == kF32By128) {
+    scale = f32_scale_of(finite ? m[0] : 0u);
+    if (stores) static_cast<float*>(p.scales)[block] = finite ? scale : __uint_as_float(0x7fc00000u);
+  } else {
+    const int c = finite ? e8m0_of(m[0]) : 127;
+    scale = e8m0_down(c);
+    if (stores) static_cast<uint8_t*>(p.scales)[block] = static_cast<uint8_t>(finite ? c : 255);
+  }
+  const bool whole = __all_sync(0xffffffffu, finite);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int owner = (lane & ~3) | ((i >> 1) & 1) | ((i & 1) << 1);
+    const float f = __shfl_sync(0xffffffffu, scale, owner);
+    float a[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a[j] = v[i][j];
+    if (!whole) {
+      const bool ok = __shfl_sync(0xffffffffu, static_cast<int>(finite), owner) != 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) a[j] = ok ? a[j] : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      if (FMT == kF32By128) {
+        a[j] = __fdiv_rn(a[j], f);
+        a[j + 1] = __fdiv_rn(a[j + 1], f);
+      } else {
+        mul2(a[j], a[j + 1], f, f);
+      }
+    }
+    uint2 o;
+    o.x = e4m3x2(a[0], a[1]) | (e4m3x2(a[2], a[3]) << 16);
+    o.y = e4m3x2(a[4], a[5]) | (e4m3x2(a[6], a[7]) << 16);
+    if (4 * tl + i < rows) *reinterpret_cast<uint2*>(p.codes + (row0 + 4 * tl + i) * cols + col0 + fl * 8) = o;
+  }
+}
+
+// s = 1 / (1 + exp(-v)) and 1 - s with the fast power and reciprocal (2 ulp each).
+// s is 0 below v = -88.7, and taken of a sixteenth of the sum, which the reciprocal
+// would flush just above that (see fg_quant.cu); 1 - s is exp(-v) s, without the
+// cancellation that a large v would multiply, and 0 where s is 0.
+__device__ __forceinline__ void sigmoid(float v, float& s, float& rest) {
+  float e = v * -1.44269504088896341f;
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e));
+  s = fmaf(e, 0.0625f, 0.0625f);
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(s));
+  s *= 0.0625f;
+  rest = fminf(e, 3.4e38f) * s;  // (a NaN in v is in s)
+}
+
+// With g, u the checkpoint's values, s = sigmoid(g) and w the row's routing weight:
+//   act = g s u,  dots = sum dy act,  dg = w dy u s (1 + g (1 - s)),  du = w dy g s.
+template <int FMT, typename T>
+__global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(const SwigluParams p) {
+  __shared__ uint32_t part[2][2][4][32];
+  __shared__ float dot_sh[2][4][32];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tl = lane >> 2, fl = lane & 3;
+  const int slab = blockIdx.y, f0 = blockIdx.x * kWide + warp * 32;
+  const int64_t cols = 2 * static_cast<int64_t>(p.K);
+  const bool inside = f0 < p.K;  // (32-blocks: the last warps may have no columns)
+  const SlabRows q = slab_rows(p.offsets, p.R, p.E, slab);
+  uint32_t word_g = 0, word_u = 0, word_a = 0;
+#pragma unroll 1
+  for (int b = 0; b < 4; ++b) {
+    if (32 * b >= q.count) {
+      if (p.dx_image.data) {
+        store_no_columns(p.dx_image, f0, slab, b, word_g);
+        store_no_columns(p.dx_image, p.K + f0, slab, b, word_u);
+        store_no_columns(p.act_image, f0, slab, b, word_a);
+      }
+      continue;
+    }
+    const int row0 = q.row0 + 32 * b, rows = min(q.count - 32 * b, 32);
+    // the routing weight of row `lane` of the square: of the choice whose slot it is
+    float w_row = 1.f;
+    if (p.weights) {
+      w_row = 0.f;
+      if (lane < rows) {
+        const int64_t t = min(max(__ldg(p.rows + row0 + lane), 0), p.T - 1);
+        for (int j = 0; j < p.k; ++j)
+          if (__ldg(p.slots + t * p.k + j) == row0 + lane) w_row = __ldg(p.weights + t * p.k + j);
+      }
+    }
+    Eight<sizeof(T) == 2 ? kBf16Rows : kF32Rows> dy_raw[4];
+    Eight<FMT> g_raw[4], u_raw[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      dy_raw[i].zero();
+      g_raw[i].zero();
+      u_raw[i].zero();
+      if (inside && 4 * tl + i < rows) {
+        const int64_t row = row0 + 4 * tl + i;
+        dy_raw[i].load(p.dy, row, f0 + fl * 8);
+        g_raw[i].load(p.saved, row, f0 + fl * 8);
+        u_raw[i].load(p.saved, row, p.K + f0 + fl * 8);
+      }
+    }
+    Square g, u, dy, v;
+    float w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      dy_raw[i].widen(dy[i]);
+      g_raw[i].widen(g[i]);
+      u_raw[i].widen(u[i]);
+      w[i] = __shfl_sync(0xffffffffu, w_row, 4 * tl + i);
+    }
+    // act, and its product with dy
+    float dot[4] = {};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float s, rest;
+        sigmoid(g[i][j], s, rest);
+        const float a = g[i][j] * s * u[i][j];
+        dot[i] = fmaf(dy[i][j], a, dot[i]);
+        v[i][j] = w[i] * a;
+        const float d = w[i] * dy[i][j];
+        dy[i][j] = d * u[i][j] * (s * fmaf(g[i][j], rest, 1.f));  // dg
+        u[i][j] = d * g[i][j] * s;                                   // du
+      }
+    if (p.dots) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        dot[i] += __shfl_xor_sync(0xffffffffu, dot[i], 1);
+        dot[i] += __shfl_xor_sync(0xffffffffu, dot[i], 2);
+        if (fl == i) dot_sh[b & 1][warp][4 * tl + i] = dot[i];
+      }
+      __syncthreads();
+      if (threadIdx.x < rows)
+        p.dots[static_cast<size_t>(row0 + threadIdx.x) * gridDim.x + blockIdx.x] =
+            (dot_sh[b & 1][0][lane] + dot_sh[b & 1][1][lane]) + (dot_sh[b & 1][2][lane] + dot_sh[b & 1][3][lane]);
+    }
+    if (!inside) continue;
+    if (p.dx_image.data) {
+      store_columns(v, p.act_image, f0, slab, b, word_a);
+      store_columns(dy, p.dx_image, f0, slab, b, word_g);
+      store_columns(u, p.dx_image, p.K + f0, slab, b, word_u);
+    }
+    store_rows<FMT>(dy, p, row0, rows, f0, part[b & 1][0]);
+    store_rows<FMT>(u, p, row0, rows, p.K + f0, part[b & 1][1]);
+    if (p.dx) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (4 * tl + i < rows) {
+          T* out = static_cast<T*>(p.dx) + (row0 + 4 * tl + i) * cols + f0 + fl * 8;
+          store8(out, dy[i]);
+          store8(out + p.K, u[i]);
+        }
+      }
+    }
+  }
+  if (p.dx_image.data) {
+    store_atoms(p.dx_image, f0, slab, word_g);
+    store_atoms(p.dx_image, p.K + f0, slab, word_u);
+    store_atoms(p.act_image, f0, slab, word_a);
+  }
+  // Rows that no expert has: zeros.  The slabs are more than the rows / 128, so
+  // that each takes its 128 of them.
+  const int none = q.first + (p.R - q.last);
+  for (int i = slab * kPlaces + warp; i < min(none, (slab + 1) * kPlaces); i += 4) {
+    const int64_t row = i < q.first ? i : q.last + (i - q.first);
+    const int c = blockIdx.x * kWide + lane * 4;
+    if (p.dots && lane == 0) p.dots[row * gridDim.x + blockIdx.x] = 0.f;
+    if (c >= p.K) continue;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t at = row * cols + h * static_cast<int64_t>(p.K) + c;
+      *reinterpret_cast<uint32_t*>(p.codes + at) = 0u;
+      if (p.dx) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) static_cast<T*>(p.dx)[at + j] = T(0.f);
+      }
+      if (c % row_block(FMT) == 0) {
+        if (FMT == kF32By128) static_cast<float*>(p.scales)[at / 128] = 1.f;
+        else static_cast<uint8_t*>(p.scales)[at / row_block(FMT)] = 127;
+      }
+    }
+  }
+}
+
+// dweights[t][j] = the sum of the partial dots of its slot's row, in the order of
+// the columns; 0 where there is no choice.
+__global__ void __launch_bounds__(256) dweights_kernel(const float* __restrict__ dots, const int32_t* __restrict__ slots,
+                                                       int64_t choices, int R, int parts, float* __restrict__ dweights) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  if (i >= choices) return;
+  const int slot = __ldg(slots + i);
+  float sum = 0.f;
+  if (slot >= 0 && slot < R) {
+    const float* d = dots + static_cast<size_t>(slot) * parts;
+    for (int x = 0; x < parts; ++x) sum += __ldcg(d + x);
+  }
+  dweights[i] = sum;
+}
+
+// ------------------------------------------------------------------ weights
+
+// One 128 x 128 block of a weight: its scale and codes, straight or transposed.
+// 256 threads, each two squares' parts.
+template <typename T, bool TRANSPOSE>
+__global__ void __launch_bounds__(256) weight_kernel(const T* __restrict__ w, int64_t ld, int64_t stride, int N, int K,
+                                                     uint8_t* __restrict__ codes, float* __restrict__ scales) {
+  __shared__ uint32_t part[8];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tl = lane >> 2, fl = lane & 3;
+  const int n0 = blockIdx.y * 128, k0 = blockIdx.x * 128;
+  const int64_t e = blockIdx.z;
+  // squares (warp / 4, warp % 4) and two rows of squares further down
+  Raw8<T> raw[2][4];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      raw[h][i].load_once(w + e * stride + (n0 + 64 * h + 32 * (warp >> 2) + 4 * tl + i) * ld + k0 + 32 * (warp & 3) + 8 * fl);
+  uint32_t top = 0;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float v[8];
+      raw[h][i].widen(v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = max(top, magnitude(v[j]));
+    }
+  top = __reduce_max_sync(0xffffffffu, top);
+  if (lane == 0) part[warp] = top;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max(top, part[i]);
+  const bool finite = top < 0x7f800000u;
+  const float s = f32_scale_of(finite ? top : 0u);
+  if (threadIdx.x == 0) {
+    const int64_t at = TRANSPOSE ? (e * (K / 128) + blockIdx.x) * (N / 128) + blockIdx.y
+                                 : (e * (N / 128) + blockIdx.y) * (K / 128) + blockIdx.x;
+    scales[at] = finite ? s : __uint_as_float(0x7fc00000u);
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int n = n0 + 64 * h + 32 * (warp >> 2) + 4 * tl, k = k0 + 32 * (warp & 3) + 8 * fl;
+    Square v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      raw[h][i].widen(v[i]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = __fdiv_rn(finite ? v[i][j] : 0.f, s);
+    }
+    if (TRANSPOSE) {
+      uint8_t* out = codes + (e * K + k) * static_cast<int64_t>(N) + n;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        *reinterpret_cast<uint32_t*>(out + j * static_cast<int64_t>(N)) = e4m3x2(v[0][j], v[1][j]) | (e4m3x2(v[2][j], v[3][j]) << 16);
+    } else {
+      uint8_t* out = codes + (e * N + n) * static_cast<int64_t>(K) + k;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint2 o;
+        o.x = e4m3x2(v[i][0], v[i][1]) | (e4m3x2(v[i][2], v[i][3]) << 16);
+        o.y = e4m3x2(v[i][4], v[i][5]) | (e4m3x2(v[i][6], v[i][7]) << 16);
+        *reinterpret_cast<uint2*>(out + i * static_cast<int64_t>(K)) = o;
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------- launch
+
+template <typename... Params, typename... Args>
+cudaError_t launch(void (*kernel)(Params...), dim3 grid, int threads, cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = pdl_enabled() ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+unsigned tiles_of(int64_t n) { return static_cast<unsigned>((n + kWide - 1) / kWide); }
+
+// The format of a plain (mode FG_BF16) or 8-bit input, -1 for none.
+int format_of(int mode, int type) {
+  switch (mode) {
+    case FG_BF16: return type == FG_TYPE_F32 ? kF32Rows : kBf16Rows;
+    case FG_MXFP8_B32:
+    case FG_MXFP4_FP8A: return kE8m0By32;
+    case FG_MXFP8: return kE8m0By128;
+    case FG_FP8_BLOCK128: return kF32By128;
+    default: return -1;
+  }
+}
+
+fg_status check_plain(const char* what, const char* name, const void* p, int64_t ld, int64_t cols, int type) {
+  if (type != FG_TYPE_F32 && type != FG_TYPE_BF16) return fail(FG_ERR_INVALID_ARG, "%s: bad type %d", what, type);
+  if (!p) return fail(FG_ERR_INVALID_ARG, "%s: null %s", what, name);
+  if (ld < cols)
+    return fail(FG_ERR_SHAPE, "%s: rows of %s are %lld apart, shorter than their %lld values", what, name, (long long)ld,
+                (long long)cols);
+  if (!aligned(p, 16) || ld * (type == FG_TYPE_F32 ? 4 : 2) % 16)
+    return fail(FG_ERR_ALIGN, "%s: %s and its rows must be 16-byte aligned", what, name);
+  return FG_OK;
+}
+
+fg_status check_8bit(const char* what, int mode, const void* codes, const void* scales) {
+  if (!codes || !scales) return fail(FG_ERR_INVALID_ARG, "%s: null codes or scales", what);
+  if (!aligned(codes, 16) || !aligned(scales, mode == FG_FP8_BLOCK128 ? 4 : 1))
+    return fail(FG_ERR_ALIGN, "%s: codes must be 16-byte aligned, fp32 scales 4-byte", what);
+  return FG_OK;
+}
+
+fg_status check_image(const char* what, const void* data, const void* sf, const void* desc) {
+  if (!data || !sf || !desc) return fail(FG_ERR_INVALID_ARG, "%s: null image, scale image or descriptor", what);
+  if (!aligned(data, 16) || !aligned(sf, 16)) return fail(FG_ERR_ALIGN, "%s: images must be 16-byte aligned", what);
+  return FG_OK;
+}
+
+}  // namespace
+
+fg_status check_columns(const char* what, int64_t C, int64_t R, int E) {
+  if (E < 1 || E > kMaxExperts) return fail(FG_ERR_SHAPE, "%s: E=%d outside 1..%d", what, E, kMaxExperts);
+  if (C <= 0 || C % 128 || C > (int64_t(1) << 24))
+    return fail(FG_ERR_SHAPE, "%s: %lld columns (a positive multiple of 128)", what, (long long)C);
+  if (R < 0 || R > (int64_t(1) << 24) || column_slabs(R, E) * kPlaces > (int64_t(1) << 20))
+    return fail(FG_ERR_SHAPE, "%s: R=%lld rows of %d experts need more than 2^20 places", what, (long long)R, E);
+  return FG_OK;
+}
+
+}  // namespace fg
+
+using namespace fg;
+
+extern "C" {
+
+fg_status fg_columns_size(int64_t C, int64_t R, int E, int64_t* places, uint64_t* data_bytes, uint64_t* sf_bytes) {
+  if (!places || !data_bytes || !sf_bytes) return fail(FG_ERR_INVALID_ARG, "null output");
+  fg_status s = check_columns("fg_columns_size", C, R, E);
+  if (s != FG_OK) return s;
+  *places = column_slabs(R, E) * kPlaces;
+  *data_bytes = static_cast<uint64_t>(C) * *places;
+  *sf_bytes = *data_bytes / 32;
+  return FG_OK;
+}
+
+fg_status fg_quantize_columns(int mode, const void* x, const void* scales, int type, int64_t T, int64_t C, int64_t ldx,
+                              const int32_t* rows, int64_t R, const int32_t* offsets, int E, void* data, void* sf,
+                              fg_bshuf* desc_out, void* stream) {
+  const char* what = "fg_quantize_columns";
+  const int fmt = format_of(mode, type);
+  if (fmt < 0) return fail(FG_ERR_INVALID_ARG, "%s: mode %d is neither bf16 (plain values) nor an 8-bit block format", what, mode);
+  fg_status s = check_columns(what, C, R, E);
+  if (s != FG_OK) return s;
+  if (T < 0 || T > (int64_t(1) << 24)) return fail(FG_ERR_SHAPE, "%s: T=%lld", what, (long long)T);
+  if (!rows && T < R) return fail(FG_ERR_SHAPE, "%s: x has %lld rows, fewer than R=%lld", what, (long long)T, (long long)R);
+  if (R > 0 && T == 0) return fail(FG_ERR_SHAPE, "%s: no rows of x to gather from", what);
+  if (R > 0) {
+    if (mode == FG_BF16) {
+      if (scales) return fail(FG_ERR_INVALID_ARG, "%s: plain values take no scales", what);
+      if ((s = check_plain(what, "x", x, ldx, C, type)) != FG_OK) return s;
+    } else {
+      if ((s = check_8bit(what, mode, x, scales)) != FG_OK) return s;
+      if (ldx != C) return fail(FG_ERR_SHAPE, "%s: rows of codes must be contiguous", what);
+    }
+  }
+  if (!offsets && E != 1) return fail(FG_ERR_INVALID_ARG, "%s: null offsets with %d experts", what, E);
+  if (!aligned(offsets, 4) || !aligned(rows, 4)) return fail(FG_ERR_ALIGN, "%s: offsets and rows must be 4-byte aligned", what);
+  if ((s = check_image(what, data, sf, desc_out)) != FG_OK) return s;
+  if ((s = check_arch()) != FG_OK) return s;
+  const int64_t slabs = column_slabs(R, E);
+  ColumnsParams p{{x, scales, ldx, C}, offsets, rows,
+                  {static_cast<uint8_t*>(data), static_cast<uint8_t*>(sf), static_cast<int>(slabs)},
+                  static_cast<int>(T), static_cast<int>(R), E};
+  const dim3 grid(static_cast<unsigned>(C / kWide), static_cast<unsigned>(slabs));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaErrorInvalidValue;
+  switch (fmt) {
+    case kF32Rows: e = launch(columns_kernel<kF32Rows>, grid, kThreads, st, p); break;
+    case kBf16Rows: e = launch(columns_kernel<kBf16Rows>, grid, kThreads, st, p); break;
+    case kE8m0By32: e = launch(columns_kernel<kE8m0By32>, grid, kThreads, st, p); break;
+    case kE8m0By128: e = launch(columns_kernel<kE8m0By128>, grid, kThreads, st, p); break;
+    case kF32By128: e = launch(columns_kernel<kF32By128>, grid, kThreads, st, p); break;
+  }
+  if (e != cudaSuccess) return cuda_fail(e, "column quantiser's launch");
+  column_descriptor(C, slabs * kPlaces, data, sf, desc_out);
+  return FG_OK;
+}
+
+fg_status fg_swiglu_backward_workspace_size(int64_t R, int64_t K, int weighted, uint64_t* bytes) {
+  if (!bytes) return fail(FG_ERR_INVALID_ARG, "null output");
+  if (R < 0 || R > (int64_t(1) << 24) || K <= 0 || K > (int64_t(1) << 20))
+    return fail(FG_ERR_SHAPE, "fg_swiglu_backward: R=%lld, K=%lld", (long long)R, (long long)K);
+  *bytes = weighted ? static_cast<uint64_t>(R) * tiles_of(K) * 4 : 0;
+  return FG_OK;
+}
+
+fg_status fg_swiglu_backward(int mode, const void* dy, int type, int64_t R, int64_t K, int64_t ldd, const void* saved,
+                             const void* saved_scales, const float* weights, const int32_t* rows, const int32_t* slots,
+                             int64_t T, int top_k, const int32_t* offsets, int E, void* codes, void* scales, void* dx,
+                             float* dweights, void* dx_data, void* dx_sf, fg_bshuf* dx_desc, void* act_data, void* act_sf,
+                             fg_bshuf* act_desc, void* workspace, uint64_t workspace_bytes, void* stream) {
+  const char* what = "fg_swiglu_backward";
+  const int fmt = mode == FG_BF16 ? -1 : format_of(mode, type);
+  if (fmt < 0) return fail(FG_ERR_INVALID_ARG, "%s: mode %d keeps no 8-bit blocks", what, mode);
+  if (type != FG_TYPE_F32 && type != FG_TYPE_BF16) return fail(FG_ERR_INVALID_ARG, "%s: bad type %d", what, type);
+  const bool columns = dx_data || act_data, weighted = weights != nullptr;
+  if (E < 1 || E > kMaxExperts) return fail(FG_ERR_SHAPE, "%s: E=%d outside 1..%d", what, E, kMaxExperts);
+  if (!offsets && E != 1) return fail(FG_ERR_INVALID_ARG, "%s: null offsets with %d experts", what, E);
+  uint64_t need = 0;
+  fg_status s = fg_swiglu_backward_workspace_size(R, K, weighted, &need);
+  if (s != FG_OK) return s;
+  if (K % row_block(fmt))
+    return fail(FG_ERR_SHAPE, "%s: K=%lld must be a multiple of %d for %s", what, (long long)K, row_block(fmt), mode_name(mode));
+  if (columns) {
+    if ((s = check_columns(what, K, R, E)) != FG_OK) return s;
+    if ((s = check_image(what, dx_data, dx_sf, dx_desc)) != FG_OK) return s;
+    if ((s = check_image(what, act_data, act_sf, act_desc)) != FG_OK) return s;
+  }
+  const int64_t slabs = column_slabs(R, E);
+  if (slabs > 65535) return fail(FG_ERR_SHAPE, "%s: R=%lld too large", what, (long long)R);
+  if (weighted) {
+    if (!rows || !slots || !dweights) return fail(FG_ERR_INVALID_ARG, "%s: weights need rows, slots and dweights", what);
+    if (top_k < 1 || top_k > kMaxTopK || T < 0 || T > (int64_t(1) << 24) || (R > 0 && T == 0))
+      return fail(FG_ERR_SHAPE, "%s: T=%lld, top_k=%d (1..%d)", what, (long long)T, top_k, kMaxTopK);
+    if (!aligned(weights, 4) || !aligned(rows, 4) || !aligned(slots, 4) || !aligned(dweights, 4))
+      return fail(FG_ERR_ALIGN, "%s: a pointer is not aligned to its type", what);
+    if (need && (!workspace || workspace_bytes < need))
+      return fail(FG_ERR_WORKSPACE, "%s: needs a %llu-byte workspace", what, (unsigned long long)need);
+    if (!aligned(workspace, 4)) return fail(FG_ERR_ALIGN, "%s: workspace must be 4-byte aligned", what);
+  } else if (dweights) {
+    return fail(FG_ERR_INVALID_ARG, "%s: dweights without weights", what);
+  }
+  if (R > 0) {
+    if ((s = check_plain(what, "dy", dy, ldd, K, type)) != FG_OK) return s;
+    if ((s = check_8bit(what, mode, saved, saved_scales)) != FG_OK) return s;
+    if ((s = check_8bit(what, mode, codes, scales)) != FG_OK) return s;
+    if (!aligned(dx, 16)) return fail(FG_ERR_ALIGN, "%s: dx must be 16-byte aligned", what);
+  }
+  if (!aligned(offsets, 4)) return fail(FG_ERR_ALIGN, "%s: offsets must be 4-byte aligned", what);
+  if (R == 0 && !columns && !weighted) return FG_OK;
+  if ((s = check_arch()) != FG_OK) return s;
+  const Image none{nullptr, nullptr, 0};
+  SwigluParams p{{dy, nullptr, ldd, K}, {saved, saved_scales, 2 * K, 2 * K}, weights, rows, slots, offsets,
+                 static_cast<uint8_t*>(codes), scales, dx, weighted ? static_cast<float*>(workspace) : nullptr,
+                 columns ? Image{static_cast<uint8_t*>(dx_data), static_cast<uint8_t*>(dx_sf), static_cast<int>(slabs)} : none,
+                 columns ? Image{static_cast<uint8_t*>(act_data), static_cast<uint8_t*>(act_sf), static_cast<int>(slabs)} : none,
+                 static_cast<int>(T), static_cast<int>(R), E, static_cast<int>(K), top_k};
+  const dim3 grid(tiles_of(K), static_cast<unsigned>(slabs));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaErrorInvalidValue;
+#define FG_B(FMT_)                                                                                     \
+  case FMT_:                                                                                           \
+    e = type == FG_TYPE_BF16 ? launch(swiglu_backward_kernel<FMT_, __nv_bfloat16>, grid, kThreads, st, p) \
+                             : launch(swiglu_backward_kernel<FMT_, float>, grid, kThreads, st, p);     \
+    break;
+  switch (fmt) { FG_B(kE8m0By32) FG_B(kE8m0By128) FG_B(kF32By128) }
+#undef FG_B
+  if (e != cudaSuccess) return cuda_fail(e, "gated activation's backward launch");
+  if (weighted && T > 0) {
+    const int64_t choices = T * top_k;
+    e = launch(dweights_kernel, dim3(static_cast<unsigned>((choices + 255) / 256)), 256, st, static_cast<const float*>(p.dots), slots,
+               choices, p.R, static_cast<int>(grid.x), dweights);
+    if (e != cudaSuccess) return cuda_fail(e, "routing weights' gradient launch");
+  }
+  if (columns) {
+    column_descriptor(2 * K, slabs * kPlaces, dx_data, dx_sf, dx_desc);
+    column_descriptor(K, slabs * kPlaces, act_data, act_sf, act_desc);
+  }
+  return FG_OK;
+}
+
+fg_status fg_quantize_weight(int mode, const void* w, int type, int E, int64_t N, int64_t K, int64_t ldw, int64_t stride,
+                             int transpose, void* codes, void* scales, void* stream) {
+  const char* what = "fg_quantize_weight";
+  if (mode != FG_FP8_BLOCK128)
+    return fail(FG_ERR_INVALID_ARG, "%s: mode %d has no 128 x 128 blocks (fg_quantize does its rows)", what, mode);
+  if (E < 1 || E > kMaxExperts) return fail(FG_ERR_SHAPE, "%s: E=%d outside 1..%d", what, E, kMaxExperts);
+  if (N <= 0 || K <= 0 || N % 128 || K % 128 || N > (int64_t(1) << 20) || K > (int64_t(1) << 20))
+    return fail(FG_ERR_SHAPE, "%s: N=%lld and K=%lld must be multiples of 128 up to 2^20", what, (long long)N, (long long)K);
+  fg_status s = check_plain(what, "w", w, ldw, K, type);
+  if (s != FG_OK) return s;
+  if (E > 1 && (stride < 0 || stride * (type == FG_TYPE_F32 ? 4 : 2) % 16))
+    return fail(FG_ERR_ALIGN, "%s: experts %lld elements apart (16-byte aligned, not negative)", what, (long long)stride);
+  if ((s = check_8bit(what, mode, codes, scales)) != FG_OK) return s;
+  if ((s = check_arch()) != FG_OK) return s;
+  const dim3 grid(static_cast<unsigned>(K / 128), static_cast<unsigned>(N / 128), static_cast<unsigned>(E));
+  uint8_t* c = static_cast<uint8_t*>(codes);
+  float* sc = static_cast<float*>(scales);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int n = static_cast<int>(N), k = static_cast<int>(K);
+  cudaError_t e;
+  if (type == FG_TYPE_BF16) {
+    const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(w);
+    e = transpose ? launch(weight_kernel<__nv_bfloat16, true>, grid, 256, st, x, ldw, stride, n, k, c, sc)
+                  : launch(weight_kernel<__nv_bfloat16, false>, grid, 256, st, x, ldw, stride, n, k, c, sc);
+  } else {
+    const float* x = static_cast<const float*>(w);
+    e = transpose ? launch(weight_kernel<float, true>, grid, 256, st, x, ldw, stride, n, k, c, sc)
+                  : launch(weight_kernel<float, false>, grid, 256, st, x, ldw, stride, n, k, c, sc);
+  }
+  return e == cudaSuccess ? FG_OK : cuda_fail(e, "weight quantiser's launch");
+}
+
+}  // extern "C"

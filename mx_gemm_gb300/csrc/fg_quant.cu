@@ -29,6 +29,7 @@
 #include "fg_host.cuh"
 #include "fg_internal.cuh"
 #include "fg_ptx.cuh"
+#include "fg_values.cuh"
 
 namespace fg {
 
@@ -37,69 +38,6 @@ namespace {
 constexpr int kVec = 8;  // consecutive values per thread
 
 // ------------------------------------------------------------ loads, codes
-
-// Eight values as they lie in memory: loads are issued together and widened
-// when they are used.  once: not read again, so kept out of the caches' way.
-template <typename T>
-struct Raw8 {
-  uint4 q[sizeof(T) / 2];
-  __device__ __forceinline__ void load(const T* p) {
-#pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) q[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
-  }
-  __device__ __forceinline__ void load_once(const T* p) {
-#pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) q[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
-  }
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) q[i] = make_uint4(0, 0, 0, 0);
-  }
-  __device__ __forceinline__ void widen(float (&v)[kVec]) const {
-#pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) {
-      const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if constexpr (sizeof(T) == 2) {
-          v[2 * j] = __uint_as_float(w[j] << 16);
-          v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-        } else {
-          v[4 * i + j] = __uint_as_float(w[j]);
-        }
-      }
-    }
-  }
-};
-
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[kVec]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&b);
-  }
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-__device__ __forceinline__ void store8(float* p, const float (&v)[kVec]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-}
-
-// a0 *= b0, a1 *= b1 in one instruction, each rounded once.
-__device__ __forceinline__ void mul2(float& a0, float& a1, float b0, float b1) {
-  asm("{\n .reg .b64 a, b;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %3};\n mul.rn.f32x2 a, a, b;\n mov.b64 {%0, %1}, a;\n}"
-      : "+f"(a0), "+f"(a1)
-      : "f"(b0), "f"(b1));
-}
-
-// Two codes, `lo` in the lower half.
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 
 // Eight e2m1 codes, v[0] in the lowest four bits.
 __device__ __forceinline__ uint32_t e2m1x8(const float (&v)[kVec]) {
@@ -132,14 +70,10 @@ __device__ __forceinline__ void quantize8(float (&v)[kVec], bool live, size_t ch
   const bool finite = amax < 0x7f800000u;
   const bool first = (threadIdx.x & (LANES - 1)) == 0;
   if (MODE == kBlock) {
-    // Below 2^-132 the quotient has nine bits at most, or is zero: there, on the
-    // bits as multiples of 2^-149, it is rounded up, so that nothing is divided
-    // by zero and no code saturates.  The NaN scale is put in after the divisions,
-    // which take zeros then: chosen before them it costs four registers, and the
-    // norm of 32761 x 4096 an eighth of its warps (170 us; 145 so).
-    const uint32_t top = finite ? amax : 0u;
-    const float s = top == 0 ? 1.f
-                             : (top < (1u << 17) ? __uint_as_float((top + 447u) / 448u) : __fdiv_rn(__uint_as_float(top), 448.f));
+    // The NaN scale is put in after the divisions, which take zeros then: chosen
+    // before them it costs four registers, and the norm of 32761 x 4096 an eighth
+    // of its warps (170 us; 145 so).
+    const float s = f32_scale_of(finite ? amax : 0u);
 #pragma unroll
     for (int i = 0; i < kVec; ++i) v[i] = __fdiv_rn(finite ? v[i] : 0.f, s);
     if (live && first) static_cast<float*>(scales)[chunk / LANES] = finite ? s : __uint_as_float(0x7fc00000u);
@@ -229,6 +163,40 @@ __global__ void __launch_bounds__(256) quantize_kernel(const T* __restrict__ x, 
     }
     quantize8<MODE>(v, row < M && c < cpr, static_cast<size_t>(row * cpr + c), codes, scales);
   }
+}
+
+// The gated activation with its checkpoint: codes and scales of silu(g) * u, and
+// of g and u themselves, as the forward pass of a training step keeps them.  One
+// pass: 4 bytes read and 3 written per value of the activation, where three calls
+// of the quantiser read 8.  Bound by HBM: 32761 x 2048 in 32-K blocks in 93 us
+// (5.1 TB/s).
+template <int MODE, typename T>
+__global__ void __launch_bounds__(256) checkpoint_kernel(const T* __restrict__ x, int64_t M, int64_t K, int64_t ldx,
+                                                         void* __restrict__ codes, void* __restrict__ scales,
+                                                         void* __restrict__ saved, void* __restrict__ saved_scales) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t cpr = K / kVec;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+  const int64_t c = static_cast<int64_t>(blockIdx.y) * blockDim.x + threadIdx.x;
+  const bool live = row < M && c < cpr;
+  Raw8<T> a, b;
+  a.zero();
+  b.zero();
+  if (live) {
+    const T* src = x + row * ldx + c * kVec;
+    a.load_once(src);
+    b.load_once(src + K);
+  }
+  float v[kVec], u[kVec];
+  a.widen(v);
+  b.widen(u);
+#pragma unroll
+  for (int j = 0; j < kVec; j += 2) swiglu2(v[j], v[j + 1], u[j], u[j + 1]);
+  quantize8<MODE>(v, live, static_cast<size_t>(row * cpr + c), codes, scales);
+  a.widen(v);
+  quantize8<MODE>(v, live, static_cast<size_t>(2 * row * cpr + c), saved, saved_scales);
+  quantize8<MODE>(u, live, static_cast<size_t>((2 * row + 1) * cpr + c), saved, saved_scales);
 }
 
 // -------------------------------------------------------- RMS norm, quantise
@@ -342,16 +310,33 @@ void pdl_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute& attr, dim3 grid, d
   cfg.numAttrs = pdl_enabled() ? 1 : 0;
 }
 
+// Columns of threads for rows of cpr chunks: the widest of 16..256 that wastes no
+// more of a row than the narrowest does.
+int thread_columns(int64_t cpr) {
+  int bx = 16;
+  for (int b = 32; b <= 256; b *= 2)
+    if ((cpr + b - 1) / b * b <= (cpr + 15) / 16 * 16) bx = b;
+  return bx;
+}
+
+template <int MODE, typename T>
+cudaError_t launch_checkpoint(const void* x, int64_t M, int64_t K, int64_t ldx, void* codes, void* scales, void* saved,
+                              void* saved_scales, cudaStream_t st) {
+  const int64_t cpr = K / kVec;
+  const int bx = thread_columns(cpr), by = 256 / bx;
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr;
+  pdl_config(cfg, attr, dim3(static_cast<unsigned>((M + by - 1) / by), static_cast<unsigned>((cpr + bx - 1) / bx)), dim3(bx, by),
+             st);
+  return cudaLaunchKernelEx(&cfg, checkpoint_kernel<MODE, T>, static_cast<const T*>(x), M, K, ldx, codes, scales, saved,
+                            saved_scales);
+}
+
 template <int MODE, int ACT, typename T>
 cudaError_t launch_quantize(const void* x, int64_t M, int64_t K, int64_t ldx, void* codes, void* scales,
                             cudaStream_t st) {
   const int64_t cpr = K / kVec;
-  // columns of threads: the widest of 16..256 that wastes no more of a row
-  // than the narrowest does
-  int bx = 16;
-  for (int b = 32; b <= 256; b *= 2)
-    if ((cpr + b - 1) / b * b <= (cpr + 15) / 16 * 16) bx = b;
-  const int by = 256 / bx;
+  const int bx = thread_columns(cpr), by = 256 / bx;
   const int64_t cols = (cpr + bx - 1) / bx;
   // two rows a thread once that leaves eight blocks for every SM
   const bool many = (M + 2 * by - 1) / (2 * by) * cols >= 8 * sm_count();
@@ -454,6 +439,31 @@ fg_status fg_quantize(int mode, int act, const void* x, int type, int64_t M, int
   }
 #undef FG_Q
   return e == cudaSuccess ? FG_OK : cuda_fail(e, "quantise launch");
+}
+
+fg_status fg_swiglu_checkpoint(int mode, const void* x, int type, int64_t M, int64_t K, int64_t ldx, void* codes,
+                               void* scales, void* saved, void* saved_scales, void* stream) {
+  const char* what = "fg_swiglu_checkpoint";
+  if (!mode_ok(mode) || !quant_mode(mode) || mode == FG_MXFP4)
+    return fail(FG_ERR_INVALID_ARG, "%s: mode %d keeps no 8-bit blocks", what, mode);
+  fg_status s = check_rows(what, mode, M, K, type);
+  if (s != FG_OK) return s;
+  if (M == 0) return FG_OK;
+  if ((s = check_input(what, "x", x, ldx, 2 * K, type)) != FG_OK) return s;
+  if ((s = check_codes(what, mode, codes, scales)) != FG_OK) return s;
+  if ((s = check_codes(what, mode, saved, saved_scales)) != FG_OK) return s;
+  if ((s = check_arch()) != FG_OK) return s;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaErrorInvalidValue;
+#define FG_C(MODE_)                                                                                                      \
+  case MODE_:                                                                                                            \
+    e = type == FG_TYPE_BF16                                                                                             \
+            ? launch_checkpoint<MODE_, __nv_bfloat16>(x, M, K, ldx, codes, scales, saved, saved_scales, st)              \
+            : launch_checkpoint<MODE_, float>(x, M, K, ldx, codes, scales, saved, saved_scales, st);                     \
+    break;
+  switch (mode == FG_MXFP4_FP8A ? FG_MXFP8_B32 : mode) { FG_C(FG_FP8_BLOCK128) FG_C(FG_MXFP8) FG_C(FG_MXFP8_B32) }
+#undef FG_C
+  return e == cudaSuccess ? FG_OK : cuda_fail(e, "checkpoint launch");
 }
 
 fg_status fg_rmsnorm_quantize(int mode, const void* x, int64_t ldx, const void* residual, int64_t ldr,

@@ -1,0 +1,435 @@
+// The router's side of a training step: the balance loss with the counts that it
+// weighs, and the gradient of the logits.
+//
+// With p = softmax(l_t) (0 in rows with nothing to pick: NaN counts as -infinity),
+// T' the tokens with something to pick and f_e expert e's share of all choices:
+//   P_e = sum_t p_te / T',  loss = c E sum_e f_e P_e,  slope_e = c E f_e / T',
+// the loss's derivative by each token's p_te (f is piecewise constant).  The
+// gradient of a token's logits from the slopes and from those of its routing
+// weights, dw_j:
+//   dl_e = p_e (slope_e - sum_i p_i slope_i) + q_j (dw_j - sum_i q_i dw_i)   [e = expert j]
+// where q is the softmax over the chosen ones; with weights that are shares of all
+// experts q_j = p_j and the last sum is subtracted from every p_e instead.
+//
+// A warp takes a token, its logits in registers.  The sums over tokens stay in
+// registers to the end of a warp's tokens, go over shared memory in the order of
+// the warps, and over the blocks' partials in theirs: the same call gives the same
+// bits.
+#include <cuda_bf16.h>
+
+#include <type_traits>
+
+#include "fg_host.cuh"
+#include "fg_internal.cuh"
+#include "fg_logits.cuh"
+#include "fg_ptx.cuh"
+
+namespace fg {
+
+namespace {
+
+constexpr int kMaxExperts = 1024;
+constexpr int kMaxTopK = 32;
+
+struct BalanceParams {
+  const void* logits;
+  const int32_t* offsets;  // [E + 1]
+  float* part;             // [blocks][E + 1]: sums of p, tokens (more than one block only)
+  float* loss;             // [1]
+  int32_t* counts;         // [E]
+  float* probs;            // [E]
+  float* slopes;           // [E]
+  int64_t T, ldl;
+  float coefficient;
+  int E, whole;
+};
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) v += __shfl_xor_sync(0xffffffffu, v, d);
+  return v;
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+  return v;
+}
+
+// p of a lane's logits, and their largest (-infinity: nothing to pick, all p 0).
+template <typename T, int VPL>
+__device__ __forceinline__ float softmax(const Logits<T, VPL>& l, float (&p)[VPL]) {
+  float top = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    p[i] = __uint_as_float(sizeof(T) == 2 ? l.bits[i] << 16 : l.bits[i]);
+    top = fmaxf(top, p[i]);  // (a NaN is not kept)
+  }
+  top = warp_max(top);
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    p[i] = p[i] > -INFINITY ? exp_below(p[i], top) : 0.f;
+    sum += p[i];
+  }
+  sum = warp_sum(sum);
+  const float r = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) p[i] *= r;
+  return top;
+}
+
+// Loss, counts, mean probabilities and slopes from the sums of `blocks` rows of
+// [E + 1], by the whole block.
+__device__ void finish(const BalanceParams& p, const float* part, int blocks) {
+  __shared__ float sum_sh[32];
+  __shared__ int count_sh[32];
+  __shared__ float tokens_sh;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int stride = p.E + 1;
+  int mine = 0;
+  for (int e = threadIdx.x; e < p.E; e += blockDim.x) mine += max(__ldg(p.offsets + e + 1) - __ldg(p.offsets + e), 0);
+  mine = __reduce_add_sync(0xffffffffu, mine);
+  if (lane == 0) count_sh[warp] = mine;
+  if (warp == 0) {
+    float n = 0.f;  // whole numbers below 2^24 in each partial: exact up to T = 2^24
+    for (int b = lane; b < blocks; b += 32) n += part[static_cast<size_t>(b) * stride + p.E];
+    n = warp_sum(n);
+    if (lane == 0) tokens_sh = n;
+  }
+  __syncthreads();
+  int total = 0;
+  for (int w = 0; w < warps; ++w) total += count_sh[w];
+  const float per_choice = total > 0 ? 1.f / static_cast<float>(total) : 0.f;
+  const float per_token = tokens_sh > 0.f ? 1.f / tokens_sh : 0.f;
+  const float c = p.coefficient * static_cast<float>(p.E);
+  float loss = 0.f;
+  for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
+    float s[4] = {};
+    int b = 0;
+    for (; b + 16 <= blocks; b += 16) {
+      float v[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = part[static_cast<size_t>(b + i) * stride + e];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[i & 3] += v[i];
+    }
+    for (; b < blocks; ++b) s[b & 3] += part[static_cast<size_t>(b) * stride + e];
+    const float prob = ((s[0] + s[1]) + (s[2] + s[3])) * per_token;
+    const int n = max(__ldg(p.offsets + e + 1) - __ldg(p.offsets + e), 0);
+    const float f = static_cast<float>(n) * per_choice;
+    p.probs[e] = prob;
+    p.counts[e] = n;
+    p.slopes[e] = c * f * per_token;
+    loss = fmaf(f, prob, loss);
+  }
+  loss = warp_sum(loss);
+  if (lane == 0) sum_sh[warp] = loss;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float all = 0.f;
+    for (int w = 0; w < warps; ++w) all += sum_sh[w];
+    *p.loss = c * all;
+  }
+}
+
+// Blocks' sums of p; alone (one block) also the rest.  Dynamic shared memory:
+// [warps][E + 1].
+template <typename T, int VPL>
+__global__ void __launch_bounds__(512) balance_kernel(const BalanceParams p) {
+  extern __shared__ float sums_sh[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int stride = p.E + 1;
+  pdl_wait();
+  pdl_launch_dependents();
+  float acc[VPL] = {};
+  int tokens = 0;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * warps;
+  int64_t t = static_cast<int64_t>(blockIdx.x) * warps + warp;
+  Logits<T, VPL> next;
+  if (t < p.T) next.load(p, t, lane);
+  for (; t < p.T; t += step) {
+    const Logits<T, VPL> now = next;
+    if (t + step < p.T) next.load(p, t + step, lane);  // on its way during this token's work
+    float v[VPL];
+    tokens += softmax(now, v) > -INFINITY;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) acc[i] += v[i];
+  }
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int e = Logits<T, VPL>::expert(i, lane);
+    if (e < p.E) sums_sh[warp * stride + e] = acc[i];
+  }
+  if (lane == 0) sums_sh[warp * stride + p.E] = static_cast<float>(tokens);
+  __syncthreads();
+  float* to = gridDim.x > 1 ? p.part + static_cast<size_t>(blockIdx.x) * stride : sums_sh;
+  for (int e = threadIdx.x; e <= p.E; e += blockDim.x) {
+    float s = 0.f;
+    for (int w = 0; w < warps; ++w) s += sums_sh[w * stride + e];
+    to[e] = s;
+  }
+  if (gridDim.x > 1) return;
+  __syncthreads();
+  finish(p, sums_sh, 1);
+}
+
+__global__ void __launch_bounds__(1024) balance_finish_kernel(const BalanceParams p, int blocks) {
+  pdl_wait();
+  pdl_launch_dependents();
+  finish(p, p.part, blocks);
+}
+
+// ----------------------------------------------------------- logits' gradient
+
+struct BackwardParams {
+  const void* logits;
+  const int32_t* experts;  // [T][k] (dweights given)
+  const float* dweights;   // [T][k] or null
+  const float* slopes;     // [E] or null
+  void* out;               // [T][E]
+  int64_t T, ldl;
+  int E, k, renormalize, whole, whole_out;
+};
+
+// Dynamic shared memory: a row of E values for each warp, zero between tokens.
+template <typename T, int VPL>
+__global__ void __launch_bounds__(256) route_backward_kernel(const BackwardParams p) {
+  using L = Logits<T, VPL>;
+  extern __shared__ float rows_sh[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  float* row = rows_sh + warp * p.E;
+  for (int e = lane; e < p.E; e += 32) row[e] = 0.f;
+  __syncwarp();
+  pdl_wait();
+  pdl_launch_dependents();
+  float slope[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int e = L::expert(i, lane);
+    slope[i] = p.slopes && e < p.E ? __ldg(p.slopes + e) : 0.f;
+  }
+  const int64_t step = static_cast<int64_t>(gridDim.x) * warps;
+  int64_t t = static_cast<int64_t>(blockIdx.x) * warps + warp;
+  L next;
+  if (t < p.T) next.load(p, t, lane);
+  for (; t < p.T; t += step) {
+    const L now = next;
+    int expert = -1;
+    float dw = 0.f, chosen = -INFINITY;
+    if (p.dweights && lane < p.k) {
+      expert = __ldg(p.experts + t * p.k + lane);
+      dw = __ldg(p.dweights + t * p.k + lane);
+      if (expert >= p.E) expert = -1;
+      if (expert >= 0) {
+        const T* l = static_cast<const T*>(p.logits) + t * p.ldl + expert;
+        chosen = static_cast<float>(*l);
+      }
+    }
+    if (t + step < p.T) next.load(p, t + step, lane);
+    float v[VPL];
+    const float top = softmax(now, v);
+    float dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) dot = fmaf(v[i], slope[i], dot);
+    dot = warp_sum(dot);
+    if (p.dweights) {
+      // q over the chosen; a share of all experts is scaled by what the others hold
+      float q = expert >= 0 && chosen > -INFINITY ? exp_below(chosen, top) : 0.f;
+      float sum;
+      if (p.renormalize) {
+        sum = warp_sum(q);
+      } else {
+        float all = 0.f;  // the softmax's sum again, from its largest p = 1 / sum
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) all = fmaxf(all, v[i]);
+        all = warp_max(all);
+        sum = all > 0.f ? 1.f / all : 0.f;
+      }
+      q = sum > 0.f ? q / sum : 0.f;
+      const float mean = warp_sum(q * dw);
+      if (p.renormalize) {
+        if (expert >= 0) atomicAdd(row + expert, q * (dw - mean));
+      } else {
+        if (expert >= 0) atomicAdd(row + expert, q * dw);
+        dot += mean;
+      }
+      __syncwarp();
+    }
+    T* out = static_cast<T*>(p.out) + t * p.E;
+#pragma unroll
+    for (int c = 0; c < VPL; c += L::V) {
+      const int e0 = L::expert(c, lane);
+      float d[L::V];
+#pragma unroll
+      for (int i = 0; i < L::V; ++i) {
+        d[i] = v[c + i] * (slope[c + i] - dot);
+        if (p.dweights && e0 + i < p.E) {
+          d[i] += row[e0 + i];
+          row[e0 + i] = 0.f;
+        }
+      }
+      if (p.whole_out && e0 + L::V <= p.E) {
+        constexpr int BYTES = L::V * sizeof(T);
+        alignas(16) T o[L::V];
+#pragma unroll
+        for (int i = 0; i < L::V; ++i) o[i] = static_cast<T>(d[i]);
+        if constexpr (BYTES == 16) *reinterpret_cast<uint4*>(out + e0) = *reinterpret_cast<const uint4*>(o);
+        else if constexpr (BYTES == 8) *reinterpret_cast<uint2*>(out + e0) = *reinterpret_cast<const uint2*>(o);
+        else if constexpr (BYTES == 4) *reinterpret_cast<uint32_t*>(out + e0) = *reinterpret_cast<const uint32_t*>(o);
+        else out[e0] = o[0];
+      } else {
+#pragma unroll
+        for (int i = 0; i < L::V; ++i)
+          if (e0 + i < p.E) out[e0 + i] = static_cast<T>(d[i]);
+      }
+    }
+    __syncwarp();
+  }
+}
+
+// ------------------------------------------------------------------- launch
+
+void config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute& attr, int64_t blocks, int threads, int smem, cudaStream_t st) {
+  cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = pdl_enabled() ? 1 : 0;
+}
+
+// Calls f with the kernel for a lane's share of E experts.
+template <typename F>
+cudaError_t by_share(int E, F f) {
+  const int vpl = (E + 31) / 32;
+  if (vpl <= 1) return f(std::integral_constant<int, 1>());
+  if (vpl <= 2) return f(std::integral_constant<int, 2>());
+  if (vpl <= 4) return f(std::integral_constant<int, 4>());
+  if (vpl <= 8) return f(std::integral_constant<int, 8>());
+  if (vpl <= 16) return f(std::integral_constant<int, 16>());
+  return f(std::integral_constant<int, 32>());
+}
+
+// Warps of a block whose rows of E values fit 32 KB.
+int warps_for(int E, int most) {
+  int w = most;
+  while (w > 4 && w * (E + 1) * 4 > 33 * 1024) w /= 2;
+  return w;
+}
+
+constexpr int kBalanceWarps = 16, kBackwardWarps = 8;
+
+// One block alone up to four tokens a warp, else up to two blocks an SM.
+int balance_blocks(int64_t T, int E) {
+  const int warps = warps_for(E, kBalanceWarps);
+  if (T <= 4 * warps) return 1;
+  const int64_t want = (T + 2 * warps - 1) / (2 * warps), most = sm_count();
+  return static_cast<int>(want < most ? want : most);
+}
+
+// Whether rows of logits can be read a lane's chunk at a time (see Logits).
+int whole_rows(const void* p, int type, int64_t T, int E, int64_t ld) {
+  const int es = type == FG_TYPE_F32 ? 4 : 2;
+  int vpl = 1;
+  while (vpl < (E + 31) / 32) vpl *= 2;
+  const int chunk = vpl * es < 16 ? vpl * es : 16;
+  return aligned(p, chunk) && (T <= 1 || ld * es % chunk == 0) ? 1 : 0;
+}
+
+fg_status check_logits(const char* what, const void* logits, int type, int64_t T, int E, int64_t ldl) {
+  if (type != FG_TYPE_F32 && type != FG_TYPE_BF16) return fail(FG_ERR_INVALID_ARG, "%s: bad type %d", what, type);
+  if (T < 0 || T > (int64_t(1) << 24) || E < 1 || E > kMaxExperts)
+    return fail(FG_ERR_SHAPE, "%s: T=%lld (up to 2^24), E=%d (1..%d experts)", what, (long long)T, E, kMaxExperts);
+  if (T == 0) return FG_OK;
+  if (ldl < E) return fail(FG_ERR_SHAPE, "%s: logit rows %lld apart, shorter than E=%d", what, (long long)ldl, E);
+  if (!logits) return fail(FG_ERR_INVALID_ARG, "%s: null logits", what);
+  if (!aligned(logits, type == FG_TYPE_F32 ? 4 : 2)) return fail(FG_ERR_ALIGN, "%s: logits are not aligned to their type", what);
+  return FG_OK;
+}
+
+}  // namespace
+
+}  // namespace fg
+
+using namespace fg;
+
+extern "C" {
+
+fg_status fg_moe_balance_loss_workspace_size(int64_t T, int E, uint64_t* bytes) {
+  if (!bytes) return fail(FG_ERR_INVALID_ARG, "null output");
+  if (T < 0 || T > (int64_t(1) << 24) || E < 1 || E > kMaxExperts)
+    return fail(FG_ERR_SHAPE, "fg_moe_balance_loss: T=%lld (up to 2^24), E=%d (1..%d experts)", (long long)T, E, kMaxExperts);
+  const int blocks = balance_blocks(T, E);
+  *bytes = blocks > 1 ? static_cast<uint64_t>(blocks) * (E + 1) * 4 : 0;
+  return FG_OK;
+}
+
+fg_status fg_moe_balance_loss(const void* logits, int type, int64_t T, int E, int64_t ldl, const int32_t* offsets,
+                              float coefficient, float* loss, int32_t* counts, float* probs, float* slopes,
+                              void* workspace, uint64_t workspace_bytes, void* stream) {
+  const char* what = "fg_moe_balance_loss";
+  fg_status s = check_logits(what, logits, type, T, E, ldl);
+  if (s != FG_OK) return s;
+  if (!offsets || !loss || !counts || !probs || !slopes) return fail(FG_ERR_INVALID_ARG, "%s: null pointer", what);
+  if (!aligned(offsets, 4) || !aligned(loss, 4) || !aligned(counts, 4) || !aligned(probs, 4) || !aligned(slopes, 4))
+    return fail(FG_ERR_ALIGN, "%s: a pointer is not aligned to its type", what);
+  uint64_t need = 0;
+  if ((s = fg_moe_balance_loss_workspace_size(T, E, &need)) != FG_OK) return s;
+  if (need && (!workspace || workspace_bytes < need))
+    return fail(FG_ERR_WORKSPACE, "%s: T=%lld, E=%d need a %llu-byte workspace", what, (long long)T, E, (unsigned long long)need);
+  if (need && !aligned(workspace, 4)) return fail(FG_ERR_ALIGN, "%s: workspace must be 4-byte aligned", what);
+  if ((s = check_arch()) != FG_OK) return s;
+  BalanceParams p{logits, offsets, static_cast<float*>(workspace), loss, counts, probs, slopes, T, ldl, coefficient, E,
+                  whole_rows(logits, type, T, E, ldl)};
+  const int blocks = balance_blocks(T, E);
+  int warps = warps_for(E, kBalanceWarps);
+  if (T < warps) warps = T < 4 ? 4 : static_cast<int>(T);
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr;
+  config(cfg, attr, blocks, 32 * warps, warps * (E + 1) * 4, static_cast<cudaStream_t>(stream));
+  cudaError_t e = by_share(E, [&](auto share) {
+    constexpr int VPL = decltype(share)::value;
+    return type == FG_TYPE_F32 ? cudaLaunchKernelEx(&cfg, balance_kernel<float, VPL>, p)
+                               : cudaLaunchKernelEx(&cfg, balance_kernel<__nv_bfloat16, VPL>, p);
+  });
+  if (e == cudaSuccess && blocks > 1) {
+    config(cfg, attr, 1, E <= 256 ? 256 : 1024, 0, static_cast<cudaStream_t>(stream));
+    e = cudaLaunchKernelEx(&cfg, balance_finish_kernel, p, blocks);
+  }
+  return e == cudaSuccess ? FG_OK : cuda_fail(e, "balance loss launch");
+}
+
+fg_status fg_moe_route_backward(const void* logits, int type, int64_t T, int E, int64_t ldl, const int32_t* experts,
+                                const float* dweights, int top_k, const float* slopes, uint32_t flags, void* out,
+                                void* stream) {
+  const char* what = "fg_moe_route_backward";
+  if (flags & ~FG_FLAG_RENORMALIZE) return fail(FG_ERR_INVALID_ARG, "%s: unknown flags 0x%x", what, flags);
+  fg_status s = check_logits(what, logits, type, T, E, ldl);
+  if (s != FG_OK) return s;
+  if (dweights && (top_k < 1 || top_k > kMaxTopK || top_k > E))
+    return fail(FG_ERR_SHAPE, "%s: top_k=%d outside 1..min(%d, E=%d)", what, top_k, kMaxTopK, E);
+  if (T == 0) return FG_OK;
+  if (!out || (dweights && !experts)) return fail(FG_ERR_INVALID_ARG, "%s: null pointer", what);
+  if (!aligned(out, type == FG_TYPE_F32 ? 4 : 2) || !aligned(experts, 4) || !aligned(dweights, 4) || !aligned(slopes, 4))
+    return fail(FG_ERR_ALIGN, "%s: a pointer is not aligned to its type", what);
+  if ((s = check_arch()) != FG_OK) return s;
+  BackwardParams p{logits, experts, dweights, slopes, out, T, ldl, E, top_k, (flags & FG_FLAG_RENORMALIZE) ? 1 : 0,
+                   whole_rows(logits, type, T, E, ldl), whole_rows(out, type, T, E, E)};
+  const int warps = warps_for(E, kBackwardWarps);
+  const int64_t want = (T + warps - 1) / warps, most = 8 * static_cast<int64_t>(sm_count());
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr;
+  config(cfg, attr, want < most ? want : most, 32 * warps, warps * E * 4, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = by_share(E, [&](auto share) {
+    constexpr int VPL = decltype(share)::value;
+    return type == FG_TYPE_F32 ? cudaLaunchKernelEx(&cfg, route_backward_kernel<float, VPL>, p)
+                               : cudaLaunchKernelEx(&cfg, route_backward_kernel<__nv_bfloat16, VPL>, p);
+  });
+  return e == cudaSuccess ? FG_OK : cuda_fail(e, "logits' gradient launch");
+}
+
+}  // extern "C"

@@ -1,5 +1,5 @@
-// Python binding of the operators around the GEMM (mx_gemm_gb300/moe.py) and of
-// the GEMM's ordinary call: the checks of their tensors, their outputs'
+// Python binding of the operators around the GEMM (mx_gemm_gb300/moe.py, train.py)
+// and of the GEMM's ordinary call: the checks of their tensors, their outputs'
 // allocation, and the call of the C ABI.  A call of theirs on one token keeps the GPU busy for 2 to 5 us, while
 // allocating each output from Python takes 1.5 us and a ctypes call of fifteen
 // arguments as much again (routing: 17 us a call that way); from here the same
@@ -7,6 +7,7 @@
 //
 // Errors: ValueError for tensors that the library would misread, the package's
 // FgError for a status of the C ABI, and torch's own for the allocations.
+#define PY_SSIZE_T_CLEAN  // "y#" takes a Py_ssize_t
 #include <Python.h>
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
@@ -532,6 +533,349 @@ PyObject* gemm(PyObject*, PyObject* const* v, Py_ssize_t n) {
   });
 }
 
+// ------------------------------------------------- training in 8 bits
+
+// A 1-D or 2-D int32 index tensor of the operands' device.
+const at::Tensor* indexes(PyObject* o, const char* name, const at::Device& device) {
+  if (o == Py_None) return nullptr;
+  const at::Tensor& t = tensor(o, name);
+  on(t, name, device);
+  contiguous(t, name);
+  typed(t, name, t.scalar_type() == at::kInt, "torch.int32");
+  return &t;
+}
+
+const at::Tensor* floats(PyObject* o, const char* name, const at::Device& device) {
+  if (o == Py_None) return nullptr;
+  const at::Tensor& t = tensor(o, name);
+  on(t, name, device);
+  contiguous(t, name);
+  typed(t, name, t.scalar_type() == at::kFloat, "torch.float32");
+  return &t;
+}
+
+const int32_t* ints(const at::Tensor* t) { return t ? t->data_ptr<int32_t>() : nullptr; }
+
+// Experts of offsets [E + 1]; 1 without any.
+int experts_of(const at::Tensor* offsets) {
+  if (!offsets) return 1;
+  if (offsets->dim() != 1 || offsets->numel() < 2 || offsets->numel() > INT32_MAX)
+    refuse("offsets must hold E + 1 values, got shape %s", shape_of(*offsets).c_str());
+  return static_cast<int>(offsets->numel() - 1);
+}
+
+// Codes [M][K] of an 8-bit mode and their scales, as quantize() makes them.
+void check_codes(int mode, const at::Tensor& codes, const at::Tensor& scales, const char* name, const at::Device& device,
+                 int64_t m, int64_t k) {
+  on(codes, name, device);
+  contiguous(codes, name);
+  typed(codes, name, is_bytes(codes.scalar_type()) || codes.scalar_type() == at::kFloat8_e4m3fn, "torch.float8_e4m3fn or bytes");
+  if (codes.dim() != 2 || codes.size(0) != m || codes.size(1) != k)
+    refuse("%s has shape %s, expected (%lld, %lld)", name, shape_of(codes).c_str(), (long long)m, (long long)k);
+  on(scales, "its scales", device);
+  contiguous(scales, "its scales");
+  const at::ScalarType s = scales.scalar_type();
+  if (mode == FG_FP8_BLOCK128) typed(scales, "its scales", s == at::kFloat, "torch.float32");
+  else typed(scales, "its scales", is_bytes(s) || s == at::kFloat8_e8m0fnu, "torch.float8_e8m0fnu or bytes");
+  const int64_t want = m * (k / (mode == FG_MXFP8 || mode == FG_FP8_BLOCK128 ? 128 : 32));
+  if (scales.numel() != want)
+    refuse("%s of shape (%lld, %lld) has %lld scales, expected %lld", name, (long long)m, (long long)k, (long long)scales.numel(),
+           (long long)want);
+}
+
+struct ColumnOperand {
+  at::Tensor data, sf;
+  fg_bshuf desc;
+};
+
+void make_columns(ColumnOperand& c, int64_t columns, int64_t rows, int experts, const at::Device& device) {
+  int64_t places = 0;
+  uint64_t data_bytes = 0, sf_bytes = 0;
+  check(fg_columns_size(columns, rows, experts, &places, &data_bytes, &sf_bytes));
+  c.data = make({static_cast<int64_t>(data_bytes)}, at::kByte, device);
+  c.sf = make({static_cast<int64_t>(sf_bytes)}, at::kByte, device);
+}
+
+PyObject* wrap(const ColumnOperand& c) {
+  return Py_BuildValue("(NNy#)", wrap(c.data), wrap(c.sf), reinterpret_cast<const char*>(&c.desc),
+                       static_cast<Py_ssize_t>(sizeof c.desc));
+}
+
+// (mode, w, transpose, stream) -> (codes, scales)
+PyObject* quantize_weight(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    arity(n, 4, "quantize_weight");
+    const int mode = small(a[0], "mode");
+    const at::Tensor& w = tensor(a[1], "w");
+    const int type = type_of(w, "w");
+    if (w.dim() != 2 && w.dim() != 3) refuse("w must be [N][K] or [E][N][K], got shape %s", shape_of(w).c_str());
+    const int64_t d = w.dim(), E = d == 3 ? w.size(0) : 1, N = w.size(d - 2), K = w.size(d - 1);
+    if (w.stride(d - 1) != 1 && K > 1) refuse("w must have contiguous rows (shape %s)", shape_of(w).c_str());
+    if (E < 1 || E > INT32_MAX) refuse("w has no experts (shape %s)", shape_of(w).c_str());
+    const int64_t ld = N > 1 ? w.stride(d - 2) : K, stride = d == 3 ? w.stride(0) : 0;
+    const bool transpose = truth(a[2], "transpose");
+    const at::Device device = w.device();
+    const Launch launch = launch_of(a[3], device);
+    at::Tensor codes, scales;
+    {
+      Unlocked u;
+      Pool pool(launch);
+      const int64_t rows = transpose ? K : N, cols = transpose ? N : K;
+      codes = make({E * rows, cols}, at::kFloat8_e4m3fn, device);
+      scales = make({E * rows / 128, cols / 128}, at::kFloat, device);
+      check(fg_quantize_weight(mode, w.data_ptr(), type, (int)E, N, K, ld, stride, transpose, codes.data_ptr(), scales.data_ptr(),
+                               launch.stream));
+      keep(launch, {&codes, &scales}, {&w});
+    }
+    return Py_BuildValue("(NN)", wrap(codes), wrap(scales));
+  });
+}
+
+// (mode, x, stream) -> (codes, scales, saved, saved scales)
+PyObject* swiglu_checkpoint(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    arity(n, 3, "swiglu_checkpoint");
+    const int mode = small(a[0], "mode");
+    if (mode == FG_MXFP4) refuse("mode mxfp4 keeps no 8-bit blocks");  // (its codes would be made half as wide)
+    const at::Tensor& x = tensor(a[1], "x");
+    const Rows r = rows_of(x, "x");
+    const int type = type_of(x, "x");
+    if (r.k % 2) refuse("x must have rows (g, u) of two equal halves, got %lld columns", (long long)r.k);
+    const at::Device device = x.device();
+    const Launch launch = launch_of(a[2], device);
+    Codes c, s;
+    {
+      Unlocked u;
+      Pool pool(launch);
+      c = make_codes(mode, r.m, r.k / 2, device);
+      s = make_codes(mode, r.m, r.k, device);
+      check(fg_swiglu_checkpoint(mode, x.data_ptr(), type, r.m, r.k / 2, r.ld, c.codes.data_ptr(), c.scales.data_ptr(),
+                                 s.codes.data_ptr(), s.scales.data_ptr(), launch.stream));
+      keep(launch, {&c.codes, &c.scales, &s.codes, &s.scales}, {&x});
+    }
+    return Py_BuildValue("(NNNN)", wrap(c.codes), wrap(c.scales), wrap(s.codes), wrap(s.scales));
+  });
+}
+
+// (x, offsets or None, scales or None, rows or None, stream) -> ((data, sf, descriptor), R, E)
+PyObject* quantize_columns(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    arity(n, 5, "quantize_columns");
+    const at::Tensor& x = tensor(a[0], "x");
+    const at::Device device = x.device();
+    const Rows r = rows_of(x, "x");
+    const at::Tensor* offsets = indexes(a[1], "offsets", device);
+    const int E = experts_of(offsets);
+    const at::Tensor* scales = nullptr;
+    int mode = FG_BF16, type = FG_TYPE_BF16;
+    if (a[2] == Py_None) {
+      type = type_of(x, "x");
+    } else {
+      scales = &tensor(a[2], "scales");
+      mode = scales->scalar_type() == at::kFloat ? FG_FP8_BLOCK128
+             : scales->numel() * 128 == r.m * r.k && r.m * r.k > 0 ? FG_MXFP8 : FG_MXFP8_B32;
+      check_codes(mode, x, *scales, "x", device, r.m, r.k);
+    }
+    const at::Tensor* rows = indexes(a[3], "rows", device);
+    const int64_t R = rows ? rows->numel() : r.m;
+    const Launch launch = launch_of(a[4], device);
+    ColumnOperand c;
+    {
+      Unlocked u;
+      Pool pool(launch);
+      make_columns(c, r.k, R, E, device);
+      check(fg_quantize_columns(mode, x.data_ptr(), scales ? scales->data_ptr() : nullptr, type, r.m, r.k, scales ? r.k : r.ld,
+                                ints(rows), R, ints(offsets), E, c.data.data_ptr(), c.sf.data_ptr(), &c.desc, launch.stream));
+      keep(launch, {&c.data, &c.sf}, {&x, offsets, scales, rows});
+    }
+    return Py_BuildValue("(NLi)", wrap(c), (long long)R, E);
+  });
+}
+
+// (mode, dy, saved, saved scales, weights, rows, slots, offsets (None: without routing), columns, plain, stream)
+//   -> (codes, scales, dx, dweights, dx's columns or None, act's columns or None, R, E)
+PyObject* swiglu_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    arity(n, 11, "swiglu_backward");
+    const int mode = small(a[0], "mode");
+    if (mode != FG_MXFP8 && mode != FG_MXFP8_B32 && mode != FG_MXFP4_FP8A && mode != FG_FP8_BLOCK128)
+      refuse("mode %d keeps no 8-bit blocks", mode);
+    const at::Tensor& dy = tensor(a[1], "dy");
+    const at::Device device = dy.device();
+    const Rows r = rows_of(dy, "dy");
+    const int type = type_of(dy, "dy");
+    const at::Tensor &saved = tensor(a[2], "saved"), &saved_scales = tensor(a[3], "saved_scales");
+    check_codes(mode, saved, saved_scales, "saved", device, r.m, 2 * r.k);
+    const at::Tensor* weights = floats(a[4], "weights", device);
+    const at::Tensor* rows = indexes(a[5], "rows", device);
+    const at::Tensor* slots = indexes(a[6], "slots", device);
+    const at::Tensor* offsets = indexes(a[7], "offsets", device);
+    const int E = experts_of(offsets);
+    int64_t T = 0, k = 0;
+    if (weights) {
+      if (!rows || !slots || !offsets) refuse("weights need rows, slots and offsets");
+      if (slots->dim() != 2 || weights->sizes() != slots->sizes())
+        refuse("weights and slots must be [T][top_k], got shapes %s and %s", shape_of(*weights).c_str(), shape_of(*slots).c_str());
+      T = slots->size(0);
+      k = slots->size(1);
+      if (rows->numel() != r.m || T * k != r.m)
+        refuse("dy has %lld rows, the routing %lld choices and %lld rows", (long long)r.m, (long long)(T * k), (long long)rows->numel());
+    }
+    const bool columns = truth(a[8], "columns"), plain = truth(a[9], "plain");
+    const Launch launch = launch_of(a[10], device);
+    Codes c;
+    at::Tensor dx, dweights, ws;
+    ColumnOperand dxc, actc;
+    {
+      Unlocked u;
+      Pool pool(launch);
+      uint64_t need = 0;
+      if (r.m > 0 || columns) check(fg_swiglu_backward_workspace_size(r.m, r.k, weights != nullptr, &need));
+      if (need) ws = make({static_cast<int64_t>(need)}, at::kByte, device);
+      c = make_codes(mode, r.m, 2 * r.k, device);
+      if (plain) dx = make({r.m, 2 * r.k}, dy.scalar_type(), device);
+      if (weights) dweights = make({T, k}, at::kFloat, device);
+      if (columns) {
+        make_columns(dxc, 2 * r.k, r.m, E, device);
+        make_columns(actc, r.k, r.m, E, device);
+      }
+      check(fg_swiglu_backward(mode, dy.data_ptr(), type, r.m, r.k, r.ld, saved.data_ptr(), saved_scales.data_ptr(),
+                               weights ? weights->data_ptr<float>() : nullptr, ints(rows), ints(slots), T,
+                               (int)(k < 1024 ? k : 1024), ints(offsets), E, c.codes.data_ptr(), c.scales.data_ptr(), data(dx),
+                               dweights.defined() ? dweights.data_ptr<float>() : nullptr, data(dxc.data), data(dxc.sf), &dxc.desc,
+                               data(actc.data), data(actc.sf), &actc.desc, data(ws), need, launch.stream));
+      keep(launch, {&c.codes, &c.scales, &dx, &dweights, &dxc.data, &dxc.sf, &actc.data, &actc.sf},
+           {&dy, &saved, &saved_scales, weights, rows, slots, offsets});
+    }
+    PyObject* of_dx = columns ? wrap(dxc) : Py_NewRef(Py_None);
+    PyObject* of_act = columns ? wrap(actc) : Py_NewRef(Py_None);
+    return Py_BuildValue("(NNNNNNLi)", wrap(c.codes), wrap(c.scales), wrap(dx), wrap(dweights), of_dx, of_act, (long long)r.m, E);
+  });
+}
+
+// (a's data, sf and descriptor's address, b's, offsets, R, E, out or None, accumulate, type, flags, stream) -> out
+PyObject* grouped_wgrad(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    arity(n, 14, "grouped_wgrad");
+    const at::Tensor* t[4];
+    const fg_bshuf* d[2];
+    const at::Device device = tensor(v[0], "a").device();
+    for (int i = 0; i < 2; ++i) {
+      t[2 * i] = &tensor(v[3 * i], i ? "b" : "a");
+      t[2 * i + 1] = &tensor(v[3 * i + 1], "the scale image");
+      on(*t[2 * i], i ? "b" : "a", device);
+      on(*t[2 * i + 1], "the scale image", device);
+      d[i] = reinterpret_cast<const fg_bshuf*>(static_cast<intptr_t>(integer(v[3 * i + 2], "the descriptor's address")));
+      if (d[i]->data != t[2 * i]->data_ptr() || d[i]->sf != t[2 * i + 1]->data_ptr())
+        refuse("the column operand's tensors are not those of its descriptor");
+    }
+    const at::Tensor* offsets = indexes(v[6], "offsets", device);
+    if (!offsets) refuse("offsets must be a torch.Tensor");
+    const int64_t R = integer(v[7], "rows");
+    const int E = small(v[8], "experts");
+    if (experts_of(offsets) != E) refuse("offsets hold %d experts, the operands %d", experts_of(offsets), E);
+    const int64_t N = d[0]->N, K = d[1]->N;
+    const bool accumulate = truth(v[10], "accumulate");
+    const int type = small(v[11], "dtype");
+    at::Tensor out;
+    if (v[9] != Py_None) {
+      out = tensor(v[9], "out");
+      on(out, "out", device);
+      contiguous(out, "out");
+      typed(out, "out", out.scalar_type() == (type == FG_TYPE_F32 ? at::kFloat : at::kBFloat16), "that of dtype");
+      if (out.dim() != 3 || out.size(0) != E || out.size(1) != N || out.size(2) != K)
+        refuse("out has shape %s, expected (%d, %lld, %lld)", shape_of(out).c_str(), E, (long long)N, (long long)K);
+    } else if (accumulate) {
+      refuse("accumulate needs out");
+    }
+    const uint32_t flags = flag_bits(v[12], "flags");
+    const Launch launch = launch_of(v[13], device);
+    {
+      Unlocked u;
+      Pool pool(launch);
+      if (!out.defined()) out = make({E, N, K}, type == FG_TYPE_F32 ? at::kFloat : at::kBFloat16, device);
+      check(fg_grouped_wgrad(d[0], d[1], ints(offsets), R, E, type, accumulate, out.data_ptr(), flags, launch.stream));
+      keep(launch, {&out}, {t[0], t[1], t[2], t[3], offsets, &out});
+    }
+    return wrap(out);
+  });
+}
+
+// (logits, offsets, coefficient, stream) -> (loss, counts, probs, slopes)
+PyObject* moe_balance_loss(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    arity(n, 4, "moe_balance_loss");
+    const at::Tensor& x = tensor(a[0], "logits");
+    const Rows r = rows_of(x, "logits");
+    const int type = type_of(x, "logits");
+    const at::Device device = x.device();
+    const at::Tensor* offsets = indexes(a[1], "offsets", device);
+    if (!offsets || offsets->dim() != 1 || offsets->numel() != r.k + 1)
+      refuse("offsets must hold E + 1 = %lld values", (long long)(r.k + 1));
+    const double coefficient = PyFloat_AsDouble(a[2]);
+    if (coefficient == -1.0 && PyErr_Occurred()) {
+      PyErr_Clear();
+      refuse("coefficient must be a number");
+    }
+    const Launch launch = launch_of(a[3], device);
+    at::Tensor loss, counts, probs, slopes, ws;
+    {
+      Unlocked u;
+      Pool pool(launch);
+      const int E = (int)(r.k < (1 << 30) ? r.k : 1 << 30);
+      uint64_t need = 0;
+      check(fg_moe_balance_loss_workspace_size(r.m, E, &need));
+      if (need) ws = make({static_cast<int64_t>(need)}, at::kByte, device);
+      loss = make({}, at::kFloat, device);
+      counts = make({r.k}, at::kInt, device);
+      probs = make({r.k}, at::kFloat, device);
+      slopes = make({r.k}, at::kFloat, device);
+      check(fg_moe_balance_loss(x.data_ptr(), type, r.m, E, r.ld, ints(offsets), (float)coefficient, loss.data_ptr<float>(),
+                                counts.data_ptr<int32_t>(), probs.data_ptr<float>(), slopes.data_ptr<float>(), data(ws), need,
+                                launch.stream));
+      keep(launch, {&loss, &counts, &probs, &slopes}, {&x, offsets});
+    }
+    return Py_BuildValue("(NNNN)", wrap(loss), wrap(counts), wrap(probs), wrap(slopes));
+  });
+}
+
+// (logits, experts or None, dweights or None, slopes or None, renormalize, stream) -> gradient of the logits
+PyObject* moe_route_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    arity(n, 6, "moe_route_backward");
+    const at::Tensor& x = tensor(a[0], "logits");
+    const Rows r = rows_of(x, "logits");
+    const int type = type_of(x, "logits");
+    const at::Device device = x.device();
+    const at::Tensor* experts = indexes(a[1], "experts", device);
+    const at::Tensor* dweights = floats(a[2], "dweights", device);
+    const at::Tensor* slopes = floats(a[3], "slopes", device);
+    int64_t k = 0;
+    if (dweights) {
+      if (!experts || experts->dim() != 2 || experts->size(0) != r.m || dweights->sizes() != experts->sizes())
+        refuse("dweights has shape %s, expected that of the routing's experts, [%lld][top_k]", shape_of(*dweights).c_str(),
+               (long long)r.m);
+      k = experts->size(1);
+    }
+    if (slopes && (slopes->dim() != 1 || slopes->numel() != r.k))
+      refuse("slopes has shape %s, expected (%lld,)", shape_of(*slopes).c_str(), (long long)r.k);
+    const bool renormalize = truth(a[4], "renormalize");
+    const Launch launch = launch_of(a[5], device);
+    at::Tensor out;
+    {
+      Unlocked u;
+      Pool pool(launch);
+      out = make({r.m, r.k}, x.scalar_type(), device);
+      check(fg_moe_route_backward(x.data_ptr(), type, r.m, (int)(r.k < (1 << 30) ? r.k : 1 << 30), r.ld, ints(experts),
+                                  dweights ? dweights->data_ptr<float>() : nullptr, (int)(k < 1024 ? k : 1024),
+                                  slopes ? slopes->data_ptr<float>() : nullptr, renormalize ? FG_FLAG_RENORMALIZE : 0,
+                                  out.data_ptr(), launch.stream));
+      keep(launch, {&out}, {&x, experts, dweights, slopes});
+    }
+    return wrap(out);
+  });
+}
+
 PyObject* set_error(PyObject*, PyObject* cls) {
   Py_INCREF(cls);
   Py_XDECREF(g_error);
@@ -550,6 +894,13 @@ PyMethodDef methods[] = {fast<quantize>("quantize"),
                          fast<grouped_gemm>("grouped_gemm"),
                          fast<moe_combine>("moe_combine"),
                          fast<gemm>("gemm"),
+                         fast<quantize_weight>("quantize_weight"),
+                         fast<swiglu_checkpoint>("swiglu_checkpoint"),
+                         fast<quantize_columns>("quantize_columns"),
+                         fast<swiglu_backward>("swiglu_backward"),
+                         fast<grouped_wgrad>("grouped_wgrad"),
+                         fast<moe_balance_loss>("moe_balance_loss"),
+                         fast<moe_route_backward>("moe_route_backward"),
                          {"set_error", set_error, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 
