@@ -22,7 +22,8 @@
 //    reads again: the gathered rows one after the other (tensor copies of four
 //    indexed rows each took three times as long as the product itself: 1797 us
 //    against 624 us for 32768 mxfp4 rows, 4096 x 7168), and the token scales as
-//    the atoms the tensor core reads.
+//    the atoms the tensor core reads.  FP8_BLOCK128: units of 128 rows and two
+//    weight tiles on one SM (TT = 128, fg_grouped_block.cu).
 //  - Few (TT = 32, decoding; this file): bound by the weights' bytes from HBM,
 //    whatever the rows.  Where dealing whole units to the blocks would leave
 //    much idle, the K steps of all units form one line that is cut evenly over
@@ -41,6 +42,7 @@
 // caller's E8M0 bytes; the others take the results out.
 #include <cuda_bf16.h>
 
+#include <algorithm>
 #include <cstring>
 
 #include "fg_grouped.cuh"
@@ -548,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
   if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
 }
 
-// What TT = 256 lays out first: the gathered rows of A (a_rows) and the token
+// What TT = 128 and 256 lay out first: the gathered rows of A (a_rows) and the token
 // scale atoms (a_sf), each where wanted.
 struct PrepParams {
   const uint8_t* a;
@@ -697,13 +699,16 @@ cudaError_t launch_prep(PrepParams p, int64_t tiles, cudaStream_t stream) {
 }
 
 // Token tile, blocks (two for each pair of SMs) and workspace of a call: partials
-// and tickets (tt 32), or scale atoms and gathered rows (tt 256), in this order.
+// and tickets (tt 32), or scale atoms and gathered rows (tt 128, 256), in this order.
 struct GroupedPlan {
   int tt, blocks;
   int64_t tiles;  // no more token tiles than this, however the rows fall
   int atoms;      // scale atoms of a 128-row block
   uint64_t part_bytes, ticket_bytes, sf_bytes, rows_bytes;
-  uint64_t total() const { return part_bytes + ticket_bytes + sf_bytes + rows_bytes; }
+  uint64_t total() const {
+    const uint64_t line = part_bytes + ticket_bytes, laid = sf_bytes + rows_bytes;
+    return std::max(line, laid);
+  }
 };
 
 GroupedPlan grouped_plan(int mode, int64_t R, int64_t E, int64_t N, int64_t K, bool gather) {
@@ -724,17 +729,29 @@ GroupedPlan grouped_plan(int mode, int64_t R, int64_t E, int64_t N, int64_t K, b
   // 256, 9 rows, 2 steps: 11 against 19; 8 of 2048 x 7168, 15 rows: 29 and 29).
   const int64_t wpairs = (N / 128 + 1) / 2, active = E < R ? E : R;
   const bool few = R * wpairs < 8000 && (active * wpairs < grouped_pair_clusters() || KB <= 8);
-  // FP8_BLOCK128's fold is built for 32-row tiles only.
-  g.tt = R <= 8 * E || few || mode == FG_FP8_BLOCK128 ? 32 : 256;
+  const bool block = mode == FG_FP8_BLOCK128;
+  g.tt = R <= 8 * E || few ? 32 : 256;
+  // FP8_BLOCK128: tiles of 128 rows on one SM above 32 rows an expert, where 32-row
+  // tiles read the weights again (64 experts, 4096 x 7168: 32 rows each 279 us with
+  // 32 and 287 with 128, 48 rows 346 and 291, 512 rows 2640 and 805), if there are
+  // units for a third of the SMs: below that the cut line wins (8 experts of 512 x
+  // 7168, 128 rows: 25 us against 30; 2048 x 4096, 64 rows, 96 units: 19 and 20; 97
+  // rows 33 and 20).
+  if (block) g.tt = R > 32 * E && (R / 128 + active) * wpairs >= 48 ? 128 : 32;
   g.tiles = R / g.tt + active;
-  const int64_t units = g.tiles * (g.tt == 256 ? wpairs : N / 128);
-  const int64_t most = g.tt == 32 ? kBlocksPerSm * static_cast<int64_t>(sm_count()) : grouped_pair_clusters();
-  const int64_t want = g.tt == 32 ? (units * KB + kMinSlabs - 1) / kMinSlabs : units;
-  g.blocks = static_cast<int>(want < most ? want : most) * (g.tt == 256 ? 2 : 1);
-  if (g.tt == 32) {
-    g.part_bytes = static_cast<uint64_t>(g.blocks) * 2 * g.tt * 128 * 4;
-    g.ticket_bytes = static_cast<uint64_t>(g.blocks) * 8;
-  } else {
+  const int64_t units = g.tiles * (g.tt == 32 ? N / 128 : wpairs);
+  const int64_t line = ((R / 32 + active) * (N / 128) * KB + kMinSlabs - 1) / kMinSlabs;  // blocks of a line of 32-row tiles
+  const int64_t most = kBlocksPerSm * static_cast<int64_t>(sm_count());
+  g.blocks = static_cast<int>(g.tt == 32    ? std::min(line, most)
+                              : g.tt == 128 ? std::min<int64_t>(units, sm_count())
+                                            : 2 * std::min<int64_t>(units, grouped_pair_clusters()));
+  if (g.tt == 32 || block) {
+    // (FP8_BLOCK128's workspace is never less than with 32-row tiles alone: in
+    // 128-row tiles the gathered rows begin where its partials would)
+    g.part_bytes = static_cast<uint64_t>(std::min(line, most)) * 2 * 32 * 128 * 4;
+    g.ticket_bytes = static_cast<uint64_t>(std::min(line, most)) * 8;
+  }
+  if (g.tt != 32) {
     if (is_mx(mode)) {
       g.atoms = static_cast<int>((mx_sf_cols(mode, K) + 3) / 4);
       g.sf_bytes = static_cast<uint64_t>(g.tiles) * g.atoms * 1024;
@@ -841,6 +858,10 @@ fg_status fg_grouped_gemm(const void* A, const void* a_scales, int64_t T, const 
                  g.sf_bytes ? ws : nullptr, p.T, p.R, E, static_cast<int>(rb),
                  is_mx(mode) ? static_cast<int>(mx_sf_cols(mode, K)) : 0, g.atoms, 0};
     if ((e = launch_prep(q, g.tiles, st)) != cudaSuccess) return cuda_fail(e, "grouped product's layout launch");
+  }
+  if (g.tt == 128) {
+    e = launch_grouped_block(a_maps, p, g.blocks, st);
+    return e == cudaSuccess ? FG_OK : cuda_fail(e, "grouped product launch");
   }
   if (g.tt == 256) {
     if (g.blocks == 0) return fail(FG_ERR_CUDA, "%s: no room for a pair of SMs", what);

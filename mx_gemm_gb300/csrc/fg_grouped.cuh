@@ -136,4 +136,7 @@ int grouped_pair_clusters();
 cudaError_t launch_grouped_pair(int mode, const AMaps& a_maps, const CUtensorMap& tmap_w, const CUtensorMap& tmap_wsf,
                                 const CUtensorMap& tmap_asf, const GroupedParams& p, int ctas, cudaStream_t stream);
 
+// Token tiles of 128 rows in FP8_BLOCK128 (fg_grouped_block.cu).
+cudaError_t launch_grouped_block(const AMaps& a_maps, const GroupedParams& p, int ctas, cudaStream_t stream);
+
 }  // namespace fg
