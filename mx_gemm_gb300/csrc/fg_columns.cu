@@ -27,7 +27,9 @@ constexpr int kMaxTopK = 32;
 constexpr int kWide = 128;    // columns of a block of threads: four squares side by side
 constexpr int kThreads = 128;
 
-using Square = float[4][8];  // a thread's part of one
+struct Square {  // a thread's part of one: rows i, columns 2 q and 2 q + 1
+  Pair p[4][4];
+};
 
 // ------------------------------------------------------------------ inputs
 
@@ -39,6 +41,15 @@ struct Source {
   int64_t ld;    // elements from row to row
   int64_t cols;
 };
+
+// What eight codes and their scale stand for.
+__device__ __forceinline__ void decode(uint2 codes, float scale, Pair (&v)[4]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const float2 f = e4m3_values((q < 2 ? codes.x : codes.y) >> (16 * (q & 1)));
+    v[q] = mul(pair_of(f.x, f.y), pair_of(scale, scale));
+  }
+}
 
 // Eight consecutive values of a row on their way.
 template <int FMT>
@@ -58,16 +69,7 @@ struct Eight {
     codes = make_uint2(0, 0);
     scale = 1.f;
   }
-  __device__ __forceinline__ void widen(float (&v)[8]) const {
-#pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-      const uint32_t w = j < 4 ? codes.x : codes.y;
-      const float2 f = e4m3_values(w >> (8 * (j & 3)));
-      v[j] = f.x;
-      v[j + 1] = f.y;
-      mul2(v[j], v[j + 1], scale, scale);
-    }
-  }
+  __device__ __forceinline__ void widen(Pair (&v)[4]) const { decode(codes, scale, v); }
 };
 
 template <typename T>
@@ -77,7 +79,12 @@ struct PlainEight {
     raw.load_once(static_cast<const T*>(s.x) + row * s.ld + col);
   }
   __device__ __forceinline__ void zero() { raw.zero(); }
-  __device__ __forceinline__ void widen(float (&v)[8]) const { raw.widen(v); }
+  __device__ __forceinline__ void widen(Pair (&v)[4]) const {
+    float f[8];
+    raw.widen(f);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = pair_of(f[2 * q], f[2 * q + 1]);
+  }
 };
 
 template <>
@@ -92,8 +99,6 @@ struct Image {
   uint8_t* sf;
   int slabs;      // of a row of 128 columns
 };
-
-__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
 // One exchange by halves: of the candidates m[0 .. 2 n) a lane keeps the first n,
 // or with bit `bit` of its index the others.
@@ -114,8 +119,11 @@ __device__ __forceinline__ void store_columns(const Square& v, const Image& im, 
   const int lane = threadIdx.x & 31, tl = lane >> 2, fl = lane & 3;
   uint32_t m[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    m[j] = max(max(magnitude(v[0][j]), magnitude(v[1][j])), max(magnitude(v[2][j]), magnitude(v[3][j])));
+  for (int q = 0; q < 4; ++q) {
+    const float2 x[4] = {halves(v.p[0][q]), halves(v.p[1][q]), halves(v.p[2][q]), halves(v.p[3][q])};
+    m[2 * q] = __float_as_uint(largest(largest(x[0].x, x[1].x, x[2].x), x[3].x, x[3].x));
+    m[2 * q + 1] = __float_as_uint(largest(largest(x[0].y, x[1].y, x[2].y), x[3].y, x[3].y));
+  }
   halve<4>(m, 16);
   halve<2>(m, 8);
   halve<1>(m, 4);
@@ -128,19 +136,23 @@ __device__ __forceinline__ void store_columns(const Square& v, const Image& im, 
   uint8_t* out = im.data + (static_cast<size_t>(f0 >> 7) * im.slabs + slab) * kColumnSlab + row * 128 + (tl & 3) * 4;
   const int piece = 2 * b + (tl >> 2);  // 16-byte piece of a column's places
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  for (int q = 0; q < 4; ++q) {
     // the lane that kept column j: bits 16, 8, 4 of its index are those of j
-    const int owner = ((j & 4) << 2) | ((j & 2) << 2) | ((j & 1) << 2) | fl;
-    const float f = __shfl_sync(0xffffffffu, mine, owner);
-    float a[4] = {v[0][j], v[1][j], v[2][j], v[3][j]};
-    if (!whole) {
-      const bool ok = __shfl_sync(0xffffffffu, static_cast<int>(finite), owner) != 0;
+    const int owner = ((q & 2) << 3) | ((q & 1) << 3) | fl;
+    const Pair f = pair_of(__shfl_sync(0xffffffffu, mine, owner), __shfl_sync(0xffffffffu, mine, owner | 4));
+    float2 x[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) a[i] = ok ? a[i] : 0.f;
+    for (int i = 0; i < 4; ++i) x[i] = halves(mul(v.p[i][q], f));
+    if (!whole) {
+      const bool lo = __shfl_sync(0xffffffffu, static_cast<int>(finite), owner) != 0;
+      const bool hi = __shfl_sync(0xffffffffu, static_cast<int>(finite), owner | 4) != 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = make_float2(lo ? x[i].x : 0.f, hi ? x[i].y : 0.f);
     }
-    mul2(a[0], a[1], f, f);
-    mul2(a[2], a[3], f, f);
-    *reinterpret_cast<uint32_t*>(out + j * 128 + ((piece ^ j) << 4)) = e4m3x2(a[0], a[1]) | (e4m3x2(a[2], a[3]) << 16);
+    *reinterpret_cast<uint32_t*>(out + 2 * q * 128 + ((piece ^ (2 * q)) << 4)) =
+        e4m3x2(x[0].x, x[1].x) | (e4m3x2(x[2].x, x[3].x) << 16);
+    *reinterpret_cast<uint32_t*>(out + (2 * q + 1) * 128 + ((piece ^ (2 * q + 1)) << 4)) =
+        e4m3x2(x[0].y, x[1].y) | (e4m3x2(x[2].y, x[3].y) << 16);
   }
 }
 
@@ -203,7 +215,7 @@ __global__ void __launch_bounds__(kThreads) columns_kernel(const ColumnsParams p
     }
     Square v;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) raw[i].widen(v[i]);
+    for (int i = 0; i < 4; ++i) raw[i].widen(v.p[i]);
     store_columns(v, p.image, f0, slab, b, word);
   }
   store_atoms(p.image, f0, slab, word);
@@ -221,7 +233,7 @@ struct SwigluParams {
   uint8_t* codes;         // [R][2 K]
   void* scales;
   void* dx;               // [R][2 K] (null: not wanted)
-  float* dots;            // [R][blocks of columns] (weights given)
+  float* dots;            // [R][column tiles] (weights given)
   Image dx_image, act_image;
   int T, R, E, K, k;
 };
@@ -238,9 +250,8 @@ __device__ __forceinline__ void store_rows(const Square& v, const SwigluParams& 
   uint32_t m[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    m[i] = magnitude(v[i][0]);
-#pragma unroll
-    for (int j = 1; j < 8; ++j) m[i] = max(m[i], magnitude(v[i][j]));
+    const float2 x[4] = {halves(v.p[i][0]), halves(v.p[i][1]), halves(v.p[i][2]), halves(v.p[i][3])};
+    m[i] = __float_as_uint(largest(largest(largest(x[0].x, x[0].y, x[1].x), x[1].y, x[2].x), largest(x[2].y, x[3].x, x[3].y), 0.f));
   }
   halve<2>(m, 1);
   halve<1>(m, 2);
@@ -269,171 +280,243 @@ __device__ __forceinline__ void store_rows(const Square& v, const SwigluParams& 
   for (int i = 0; i < 4; ++i) {
     const int owner = (lane & ~3) | ((i >> 1) & 1) | ((i & 1) << 1);
     const float f = __shfl_sync(0xffffffffu, scale, owner);
-    float a[8];
+    const bool ok = whole || __shfl_sync(0xffffffffu, static_cast<int>(finite), owner) != 0;
+    uint32_t w[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) a[j] = v[i][j];
-    if (!whole) {
-      const bool ok = __shfl_sync(0xffffffffu, static_cast<int>(finite), owner) != 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) a[j] = ok ? a[j] : 0.f;
+    for (int q = 0; q < 4; ++q) {
+      float2 x = halves(FMT == kF32By128 ? v.p[i][q] : mul(v.p[i][q], pair_of(f, f)));
+      if (FMT == kF32By128) x = make_float2(__fdiv_rn(x.x, f), __fdiv_rn(x.y, f));
+      if (!whole) x = make_float2(ok ? x.x : 0.f, ok ? x.y : 0.f);
+      w[q] = e4m3x2(x.x, x.y);
     }
-#pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-      if (FMT == kF32By128) {
-        a[j] = __fdiv_rn(a[j], f);
-        a[j + 1] = __fdiv_rn(a[j + 1], f);
-      } else {
-        mul2(a[j], a[j + 1], f, f);
-      }
-    }
-    uint2 o;
-    o.x = e4m3x2(a[0], a[1]) | (e4m3x2(a[2], a[3]) << 16);
-    o.y = e4m3x2(a[4], a[5]) | (e4m3x2(a[6], a[7]) << 16);
+    const uint2 o = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
     if (4 * tl + i < rows) *reinterpret_cast<uint2*>(p.codes + (row0 + 4 * tl + i) * cols + col0 + fl * 8) = o;
   }
 }
 
-// s = 1 / (1 + exp(-v)) and 1 - s with the fast power and reciprocal (2 ulp each).
-// s is 0 below v = -88.7, and taken of a sixteenth of the sum, which the reciprocal
-// would flush just above that (see fg_quant.cu); 1 - s is exp(-v) s, without the
-// cancellation that a large v would multiply, and 0 where s is 0.
-__device__ __forceinline__ void sigmoid(float v, float& s, float& rest) {
-  float e = v * -1.44269504088896341f;
-  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e));
-  s = fmaf(e, 0.0625f, 0.0625f);
-  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(s));
-  s *= 0.0625f;
-  rest = fminf(e, 3.4e38f) * s;  // (a NaN in v is in s)
+// What a thread's loads for one square have landed in: its own bytes alone, so that
+// nobody waits for another.
+template <typename T>
+struct Landing {
+  uint4 dy[4][sizeof(T) / 2][kThreads];
+  uint2 g[4][kThreads], u[4][kThreads];
+};
+
+// 16 or 8 bytes to shared memory, zeros where there are none to read.
+__device__ __forceinline__ void fetch16(void* dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void fetch8(void* dst, const void* src, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 8 : 0) : "memory");
 }
 
 // With g, u the checkpoint's values, s = sigmoid(g) and w the row's routing weight:
 //   act = g s u,  dots = sum dy act,  dg = w dy u s (1 + g (1 - s)),  du = w dy g s.
+// e = exp(-g) and 16 s = 1 / (1/16 + e/16) come from the fast power and reciprocal (2
+// ulp each); the reciprocal of the sum itself would be flushed for g between -88.7,
+// below which s is 0, and -87.3.  g (1 - s) is g s e, without the cancellation of 1 - s
+// that a large g would multiply.
+//
+// A block of threads takes one slab's 128 rows x 128 columns at a time, 32 rows in
+// turn, and asks for the next 32 rows' bytes before it works on these: with four
+// blocks an SM, whose registers they fill, nothing else covers the loads.  32760 x
+// 2048 with columns in 232 us; 371 without that, and with the values not kept as
+// pairs.
 template <int FMT, typename T>
-__global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(const SwigluParams p) {
+__global__ void __launch_bounds__(kThreads, 4) swiglu_backward_kernel(const SwigluParams p) {
   __shared__ uint32_t part[2][2][4][32];
   __shared__ float dot_sh[2][4][32];
+  __shared__ float weight_sh[kPlaces];
+  extern __shared__ uint8_t landing_sh[];
+  Landing<T>* landing = reinterpret_cast<Landing<T>*>(landing_sh);
   pdl_wait();
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tl = lane >> 2, fl = lane & 3;
-  const int slab = blockIdx.y, f0 = blockIdx.x * kWide + warp * 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, tl = lane >> 2, fl = lane & 3;
+  const int slab = blockIdx.y, tiles = (p.K + kWide - 1) / kWide;
   const int64_t cols = 2 * static_cast<int64_t>(p.K);
-  const bool inside = f0 < p.K;  // (32-blocks: the last warps may have no columns)
   const SlabRows q = slab_rows(p.offsets, p.R, p.E, slab);
+  const int squares = (q.count + 31) / 32;  // of this slab's rows
+  // square n of this block's: rows 32 (n % squares), column tile n / squares
+  const int count = squares * ((tiles - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
+  if (squares > 0) {
+    // the slab's routing weights: a row's is that of the choice whose slot it is
+    float w = 1.f;
+    if (p.weights) {
+      w = 0.f;
+      if (tid < q.count) {
+        const int64_t t = min(max(__ldg(p.rows + q.row0 + tid), 0), p.T - 1);
+        for (int j = 0; j < p.k; ++j)
+          if (__ldg(p.slots + t * p.k + j) == q.row0 + tid) w = __ldg(p.weights + t * p.k + j);
+      }
+    }
+    weight_sh[tid] = w;
+  }
+  __syncthreads();
+  // the checkpoint's scales of row `lane` of the next square, and its bytes
+  float gs_next = 1.f, us_next = 1.f;
+  auto ask = [&](int n) {
+    const int b = n % squares, f0 = (blockIdx.x + n / squares * gridDim.x) * kWide + warp * 32;
+    const int row0 = q.row0 + 32 * b, rows = min(q.count - 32 * b, 32);
+    Landing<T>& to = landing[n & 1];
+    const bool inside = f0 < p.K;  // (32-blocks: the last warps may have no columns)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool there = inside && 4 * tl + i < rows;
+      const int64_t row = there ? row0 + 4 * tl + i : q.row0;
+      const int c = inside ? f0 + fl * 8 : 0;
+      const T* dy = static_cast<const T*>(p.dy.x) + row * p.dy.ld + c;
+      const uint8_t* saved = static_cast<const uint8_t*>(p.saved.x) + row * cols + c;
+#pragma unroll
+      for (int h = 0; h < static_cast<int>(sizeof(T) / 2); ++h) fetch16(&to.dy[i][h][tid], dy + 8 * h / static_cast<int>(sizeof(T) / 2), there);
+      fetch8(&to.g[i][tid], saved, there);
+      fetch8(&to.u[i][tid], saved + p.K, there);
+    }
+    gs_next = us_next = 1.f;
+    if (inside && lane < rows) {
+      constexpr int S = row_block(FMT);
+      const int64_t g_at = (row0 + lane) * (cols / S) + f0 / S, u_at = g_at + p.K / S;
+      if (FMT == kF32By128) {
+        gs_next = __ldg(static_cast<const float*>(p.saved.scales) + g_at);
+        us_next = __ldg(static_cast<const float*>(p.saved.scales) + u_at);
+      } else {
+        gs_next = e8m0_up(__ldg(static_cast<const uint8_t*>(p.saved.scales) + g_at));
+        us_next = e8m0_up(__ldg(static_cast<const uint8_t*>(p.saved.scales) + u_at));
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if (count > 0) ask(0);
   uint32_t word_g = 0, word_u = 0, word_a = 0;
 #pragma unroll 1
-  for (int b = 0; b < 4; ++b) {
-    if (32 * b >= q.count) {
-      if (p.dx_image.data) {
-        store_no_columns(p.dx_image, f0, slab, b, word_g);
-        store_no_columns(p.dx_image, p.K + f0, slab, b, word_u);
-        store_no_columns(p.act_image, f0, slab, b, word_a);
-      }
-      continue;
-    }
+  for (int n = 0; n < count; ++n) {
+    const int b = n % squares, tile = blockIdx.x + n / squares * gridDim.x, f0 = tile * kWide + warp * 32;
     const int row0 = q.row0 + 32 * b, rows = min(q.count - 32 * b, 32);
-    // the routing weight of row `lane` of the square: of the choice whose slot it is
-    float w_row = 1.f;
-    if (p.weights) {
-      w_row = 0.f;
-      if (lane < rows) {
-        const int64_t t = min(max(__ldg(p.rows + row0 + lane), 0), p.T - 1);
-        for (int j = 0; j < p.k; ++j)
-          if (__ldg(p.slots + t * p.k + j) == row0 + lane) w_row = __ldg(p.weights + t * p.k + j);
-      }
+    const bool inside = f0 < p.K;
+    const float gs_row = gs_next, us_row = us_next;
+    if (n + 1 < count) {
+      ask(n + 1);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    } else {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
-    Eight<sizeof(T) == 2 ? kBf16Rows : kF32Rows> dy_raw[4];
-    Eight<FMT> g_raw[4], u_raw[4];
+    const Landing<T>& from = landing[n & 1];
+    Square act, dg, du;
+    float dot[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      dy_raw[i].zero();
-      g_raw[i].zero();
-      u_raw[i].zero();
-      if (inside && 4 * tl + i < rows) {
-        const int64_t row = row0 + 4 * tl + i;
-        dy_raw[i].load(p.dy, row, f0 + fl * 8);
-        g_raw[i].load(p.saved, row, f0 + fl * 8);
-        u_raw[i].load(p.saved, row, p.K + f0 + fl * 8);
+      const float w = weight_sh[32 * b + 4 * tl + i];
+      const float gs = __shfl_sync(0xffffffffu, gs_row, 4 * tl + i), us = __shfl_sync(0xffffffffu, us_row, 4 * tl + i);
+      Pair g[4], u[4], dy[4];
+      decode(from.g[i][tid], gs, g);
+      decode(from.u[i][tid], us, u);
+      Eight<sizeof(T) == 2 ? kBf16Rows : kF32Rows> raw;
+#pragma unroll
+      for (int h = 0; h < static_cast<int>(sizeof(T) / 2); ++h) raw.raw.q[h] = from.dy[i][h][tid];
+      raw.widen(dy);
+      Pair sum = pair_of(0.f, 0.f);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        constexpr float kLog2e = 1.44269504088896341f;
+        float2 e = halves(mul(g[c], pair_of(-kLog2e, -kLog2e)));
+        asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.x));
+        asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.y));
+        float2 h = halves(fma(pair_of(e.x, e.y), pair_of(0.0625f, 0.0625f), pair_of(0.0625f, 0.0625f)));
+        asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(h.x));
+        asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(h.y));
+        const Pair sg = mul(pair_of(h.x, h.y), pair_of(0.0625f, 0.0625f)), gs_ = mul(g[c], sg);
+        const Pair up = fma(gs_, pair_of(fminf(e.x, 3.4e38f), fminf(e.y, 3.4e38f)), pair_of(1.f, 1.f));  // 1 + g (1 - s)
+        const Pair a = mul(gs_, u[c]), d = mul(dy[c], pair_of(w, w));
+        sum = fma(dy[c], a, sum);
+        act.p[i][c] = mul(a, pair_of(w, w));
+        dg.p[i][c] = mul(mul(d, u[c]), mul(sg, up));
+        du.p[i][c] = mul(d, gs_);
       }
+      const float2 s = halves(sum);
+      dot[i] = s.x + s.y;
     }
-    Square g, u, dy, v;
-    float w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      dy_raw[i].widen(dy[i]);
-      g_raw[i].widen(g[i]);
-      u_raw[i].widen(u[i]);
-      w[i] = __shfl_sync(0xffffffffu, w_row, 4 * tl + i);
-    }
-    // act, and its product with dy
-    float dot[4] = {};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        float s, rest;
-        sigmoid(g[i][j], s, rest);
-        const float a = g[i][j] * s * u[i][j];
-        dot[i] = fmaf(dy[i][j], a, dot[i]);
-        v[i][j] = w[i] * a;
-        const float d = w[i] * dy[i][j];
-        dy[i][j] = d * u[i][j] * (s * fmaf(g[i][j], rest, 1.f));  // dg
-        u[i][j] = d * g[i][j] * s;                                   // du
-      }
     if (p.dots) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         dot[i] += __shfl_xor_sync(0xffffffffu, dot[i], 1);
         dot[i] += __shfl_xor_sync(0xffffffffu, dot[i], 2);
-        if (fl == i) dot_sh[b & 1][warp][4 * tl + i] = dot[i];
+        if (fl == i) dot_sh[n & 1][warp][4 * tl + i] = dot[i];
       }
       __syncthreads();
-      if (threadIdx.x < rows)
-        p.dots[static_cast<size_t>(row0 + threadIdx.x) * gridDim.x + blockIdx.x] =
-            (dot_sh[b & 1][0][lane] + dot_sh[b & 1][1][lane]) + (dot_sh[b & 1][2][lane] + dot_sh[b & 1][3][lane]);
+      if (tid < rows)
+        p.dots[static_cast<size_t>(row0 + tid) * tiles + tile] =
+            (dot_sh[n & 1][0][lane] + dot_sh[n & 1][1][lane]) + (dot_sh[n & 1][2][lane] + dot_sh[n & 1][3][lane]);
     }
-    if (!inside) continue;
-    if (p.dx_image.data) {
-      store_columns(v, p.act_image, f0, slab, b, word_a);
-      store_columns(dy, p.dx_image, f0, slab, b, word_g);
-      store_columns(u, p.dx_image, p.K + f0, slab, b, word_u);
-    }
-    store_rows<FMT>(dy, p, row0, rows, f0, part[b & 1][0]);
-    store_rows<FMT>(u, p, row0, rows, p.K + f0, part[b & 1][1]);
-    if (p.dx) {
+    if (inside) {
+      if (p.dx_image.data) {
+        store_columns(act, p.act_image, f0, slab, b, word_a);
+        store_columns(dg, p.dx_image, f0, slab, b, word_g);
+        store_columns(du, p.dx_image, p.K + f0, slab, b, word_u);
+      }
+      store_rows<FMT>(dg, p, row0, rows, f0, part[n & 1][0]);
+      store_rows<FMT>(du, p, row0, rows, p.K + f0, part[n & 1][1]);
+      if (p.dx) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (4 * tl + i < rows) {
-          T* out = static_cast<T*>(p.dx) + (row0 + 4 * tl + i) * cols + f0 + fl * 8;
-          store8(out, dy[i]);
-          store8(out + p.K, u[i]);
+        for (int i = 0; i < 4; ++i) {
+          if (4 * tl + i < rows) {
+            T* out = static_cast<T*>(p.dx) + (row0 + 4 * tl + i) * cols + f0 + fl * 8;
+            float x[8], y[8];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              *reinterpret_cast<float2*>(&x[2 * c]) = halves(dg.p[i][c]);
+              *reinterpret_cast<float2*>(&y[2 * c]) = halves(du.p[i][c]);
+            }
+            store8(out, x);
+            store8(out + p.K, y);
+          }
         }
       }
     }
-  }
-  if (p.dx_image.data) {
-    store_atoms(p.dx_image, f0, slab, word_g);
-    store_atoms(p.dx_image, p.K + f0, slab, word_u);
-    store_atoms(p.act_image, f0, slab, word_a);
+    if (p.dx_image.data && b == squares - 1) {
+      // the slab's rest, and its scales
+      for (int r = squares; r < 4; ++r) {
+        store_no_columns(p.dx_image, f0, slab, r, word_g);
+        store_no_columns(p.dx_image, p.K + f0, slab, r, word_u);
+        store_no_columns(p.act_image, f0, slab, r, word_a);
+      }
+      store_atoms(p.dx_image, f0, slab, word_g);
+      store_atoms(p.dx_image, p.K + f0, slab, word_u);
+      store_atoms(p.act_image, f0, slab, word_a);
+      word_g = word_u = word_a = 0;
+    }
   }
   // Rows that no expert has: zeros.  The slabs are more than the rows / 128, so
-  // that each takes its 128 of them.
+  // that each takes its 128 of them.  And a slab without rows is zeros.
   const int none = q.first + (p.R - q.last);
-  for (int i = slab * kPlaces + warp; i < min(none, (slab + 1) * kPlaces); i += 4) {
-    const int64_t row = i < q.first ? i : q.last + (i - q.first);
-    const int c = blockIdx.x * kWide + lane * 4;
-    if (p.dots && lane == 0) p.dots[row * gridDim.x + blockIdx.x] = 0.f;
-    if (c >= p.K) continue;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int64_t at = row * cols + h * static_cast<int64_t>(p.K) + c;
-      *reinterpret_cast<uint32_t*>(p.codes + at) = 0u;
-      if (p.dx) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) static_cast<T*>(p.dx)[at + j] = T(0.f);
+  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    if (squares == 0 && p.dx_image.data) {
+      const int f0 = tile * kWide + warp * 32;
+      for (int r = 0; r < 4; ++r) {
+        store_no_columns(p.dx_image, f0, slab, r, word_g);
+        store_no_columns(p.dx_image, p.K + f0, slab, r, word_u);
+        store_no_columns(p.act_image, f0, slab, r, word_a);
       }
-      if (c % row_block(FMT) == 0) {
-        if (FMT == kF32By128) static_cast<float*>(p.scales)[at / 128] = 1.f;
-        else static_cast<uint8_t*>(p.scales)[at / row_block(FMT)] = 127;
+      store_atoms(p.dx_image, f0, slab, word_g);
+      store_atoms(p.dx_image, p.K + f0, slab, word_u);
+      store_atoms(p.act_image, f0, slab, word_a);
+      word_g = word_u = word_a = 0;
+    }
+    for (int i = slab * kPlaces + warp; i < min(none, (slab + 1) * kPlaces); i += 4) {
+      const int64_t row = i < q.first ? i : q.last + (i - q.first);
+      const int c = tile * kWide + lane * 4;
+      if (p.dots && lane == 0) p.dots[row * tiles + tile] = 0.f;
+      if (c >= p.K) continue;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int64_t at = row * cols + h * static_cast<int64_t>(p.K) + c;
+        *reinterpret_cast<uint32_t*>(p.codes + at) = 0u;
+        if (p.dx) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) static_cast<T*>(p.dx)[at + j] = T(0.f);
+        }
+        if (c % row_block(FMT) == 0) {
+          if (FMT == kF32By128) static_cast<float*>(p.scales)[at / 128] = 1.f;
+          else static_cast<uint8_t*>(p.scales)[at / row_block(FMT)] = 127;
+        }
       }
     }
   }
@@ -484,7 +567,7 @@ __global__ void __launch_bounds__(256) weight_kernel(const T* __restrict__ w, in
       float v[8];
       raw[h][i].widen(v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) top = max(top, magnitude(v[j]));
+      for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[j]) & 0x7fffffffu);
     }
   top = __reduce_max_sync(0xffffffffu, top);
   if (lane == 0) part[warp] = top;
@@ -501,7 +584,7 @@ __global__ void __launch_bounds__(256) weight_kernel(const T* __restrict__ w, in
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int n = n0 + 64 * h + 32 * (warp >> 2) + 4 * tl, k = k0 + 32 * (warp & 3) + 8 * fl;
-    Square v;
+    float v[4][8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       raw[h][i].widen(v[i]);
@@ -529,10 +612,11 @@ __global__ void __launch_bounds__(256) weight_kernel(const T* __restrict__ w, in
 // ------------------------------------------------------------------- launch
 
 template <typename... Params, typename... Args>
-cudaError_t launch(void (*kernel)(Params...), dim3 grid, int threads, cudaStream_t st, Args... args) {
+cudaError_t launch_smem(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t st, Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -540,6 +624,16 @@ cudaError_t launch(void (*kernel)(Params...), dim3 grid, int threads, cudaStream
   cfg.attrs = &attr;
   cfg.numAttrs = pdl_enabled() ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <typename... Params, typename... Args>
+cudaError_t launch(void (*kernel)(Params...), dim3 grid, int threads, cudaStream_t st, Args... args) {
+  return launch_smem(kernel, grid, threads, 0, st, args...);
+}
+
+cudaError_t launch_backward(void (*kernel)(SwigluParams), size_t smem, dim3 grid, cudaStream_t st, const SwigluParams& p) {
+  const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), static_cast<int>(smem));
+  return e == cudaSuccess ? launch_smem(kernel, grid, kThreads, smem, st, p) : e;
 }
 
 unsigned tiles_of(int64_t n) { return static_cast<unsigned>((n + kWide - 1) / kWide); }
@@ -709,13 +803,16 @@ fg_status fg_swiglu_backward(int mode, const void* dy, int type, int64_t R, int6
                  columns ? Image{static_cast<uint8_t*>(dx_data), static_cast<uint8_t*>(dx_sf), static_cast<int>(slabs)} : none,
                  columns ? Image{static_cast<uint8_t*>(act_data), static_cast<uint8_t*>(act_sf), static_cast<int>(slabs)} : none,
                  static_cast<int>(T), static_cast<int>(R), E, static_cast<int>(K), top_k};
-  const dim3 grid(tiles_of(K), static_cast<unsigned>(slabs));
+  // column tiles are shared out over blocks until there are eight for an SM
+  const int64_t tiles = tiles_of(K), shares = (8 * sm_count() + slabs - 1) / slabs;
+  const dim3 grid(static_cast<unsigned>(tiles < shares ? tiles : shares), static_cast<unsigned>(slabs));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaErrorInvalidValue;
-#define FG_B(FMT_)                                                                                     \
-  case FMT_:                                                                                           \
-    e = type == FG_TYPE_BF16 ? launch(swiglu_backward_kernel<FMT_, __nv_bfloat16>, grid, kThreads, st, p) \
-                             : launch(swiglu_backward_kernel<FMT_, float>, grid, kThreads, st, p);     \
+#define FG_B(FMT_)                                                                                           \
+  case FMT_:                                                                                                 \
+    e = type == FG_TYPE_BF16 ? launch_backward(swiglu_backward_kernel<FMT_, __nv_bfloat16>,                  \
+                                               2 * sizeof(Landing<__nv_bfloat16>), grid, st, p)              \
+                             : launch_backward(swiglu_backward_kernel<FMT_, float>, 2 * sizeof(Landing<float>), grid, st, p); \
     break;
   switch (fmt) { FG_B(kE8m0By32) FG_B(kE8m0By128) FG_B(kF32By128) }
 #undef FG_B
@@ -723,7 +820,7 @@ fg_status fg_swiglu_backward(int mode, const void* dy, int type, int64_t R, int6
   if (weighted && T > 0) {
     const int64_t choices = T * top_k;
     e = launch(dweights_kernel, dim3(static_cast<unsigned>((choices + 255) / 256)), 256, st, static_cast<const float*>(p.dots), slots,
-               choices, p.R, static_cast<int>(grid.x), dweights);
+               choices, p.R, static_cast<int>(tiles), dweights);
     if (e != cudaSuccess) return cuda_fail(e, "routing weights' gradient launch");
   }
   if (columns) {
