@@ -345,15 +345,18 @@ __global__ void __launch_bounds__(kThreads, 4) swiglu_backward_kernel(const Swig
       w = 0.f;
       if (tid < q.count) {
         const int64_t t = min(max(__ldg(p.rows + q.row0 + tid), 0), p.T - 1);
-        for (int j = 0; j < p.k; ++j)
-          if (__ldg(p.slots + t * p.k + j) == q.row0 + tid) w = __ldg(p.weights + t * p.k + j);
+        for (int j0 = 0; j0 < p.k; j0 += 8) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j0 + j < p.k && __ldg(p.slots + t * p.k + j0 + j) == q.row0 + tid) w = __ldg(p.weights + t * p.k + j0 + j);
+        }
       }
     }
     weight_sh[tid] = w;
   }
   __syncthreads();
-  // the checkpoint's scales of row `lane` of the next square, and its bytes
-  float gs_next = 1.f, us_next = 1.f;
+  // the checkpoint's scales of row `lane` of the next square, as they lie in memory
+  uint32_t gs_next = 0, us_next = 0;
   auto ask = [&](int n) {
     const int b = n % squares, f0 = (blockIdx.x + n / squares * gridDim.x) * kWide + warp * 32;
     const int row0 = q.row0 + 32 * b, rows = min(q.count - 32 * b, 32);
@@ -371,28 +374,36 @@ __global__ void __launch_bounds__(kThreads, 4) swiglu_backward_kernel(const Swig
       fetch8(&to.g[i][tid], saved, there);
       fetch8(&to.u[i][tid], saved + p.K, there);
     }
-    gs_next = us_next = 1.f;
-    if (inside && lane < rows) {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto ask_scales = [&](int n) {
+    const int b = n % squares, f0 = (blockIdx.x + n / squares * gridDim.x) * kWide + warp * 32;
+    const int row0 = q.row0 + 32 * b, rows = min(q.count - 32 * b, 32);
+    gs_next = us_next = 0;  // (rows that are not there have codes 0)
+    if (f0 < p.K && lane < rows) {
       constexpr int S = row_block(FMT);
       const int64_t g_at = (row0 + lane) * (cols / S) + f0 / S, u_at = g_at + p.K / S;
       if (FMT == kF32By128) {
-        gs_next = __ldg(static_cast<const float*>(p.saved.scales) + g_at);
-        us_next = __ldg(static_cast<const float*>(p.saved.scales) + u_at);
+        gs_next = __ldg(static_cast<const uint32_t*>(p.saved.scales) + g_at);
+        us_next = __ldg(static_cast<const uint32_t*>(p.saved.scales) + u_at);
       } else {
-        gs_next = e8m0_up(__ldg(static_cast<const uint8_t*>(p.saved.scales) + g_at));
-        us_next = e8m0_up(__ldg(static_cast<const uint8_t*>(p.saved.scales) + u_at));
+        gs_next = __ldg(static_cast<const uint8_t*>(p.saved.scales) + g_at);
+        us_next = __ldg(static_cast<const uint8_t*>(p.saved.scales) + u_at);
       }
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  if (count > 0) ask(0);
+  if (count > 0) {
+    ask(0);
+    ask_scales(0);
+  }
   uint32_t word_g = 0, word_u = 0, word_a = 0;
 #pragma unroll 1
   for (int n = 0; n < count; ++n) {
     const int b = n % squares, tile = blockIdx.x + n / squares * gridDim.x, f0 = tile * kWide + warp * 32;
     const int row0 = q.row0 + 32 * b, rows = min(q.count - 32 * b, 32);
     const bool inside = f0 < p.K;
-    const float gs_row = gs_next, us_row = us_next;
+    auto scale = [](uint32_t x) { return FMT == kF32By128 ? __uint_as_float(x) : e8m0_up(x); };
+    const uint32_t gs_row = gs_next, us_row = us_next;
     if (n + 1 < count) {
       ask(n + 1);
       asm volatile("cp.async.wait_group 1;" ::: "memory");
@@ -405,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 4) swiglu_backward_kernel(const Swig
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float w = weight_sh[32 * b + 4 * tl + i];
-      const float gs = __shfl_sync(0xffffffffu, gs_row, 4 * tl + i), us = __shfl_sync(0xffffffffu, us_row, 4 * tl + i);
+      const float gs = scale(__shfl_sync(0xffffffffu, gs_row, 4 * tl + i)), us = scale(__shfl_sync(0xffffffffu, us_row, 4 * tl + i));
       Pair g[4], u[4], dy[4];
       decode(from.g[i][tid], gs, g);
       decode(from.u[i][tid], us, u);
@@ -446,9 +457,13 @@ __global__ void __launch_bounds__(kThreads, 4) swiglu_backward_kernel(const Swig
         p.dots[static_cast<size_t>(row0 + tid) * tiles + tile] =
             (dot_sh[n & 1][0][lane] + dot_sh[n & 1][1][lane]) + (dot_sh[n & 1][2][lane] + dot_sh[n & 1][3][lane]);
     }
+    if (inside && p.dx_image.data) store_columns(act, p.act_image, f0, slab, b, word_a);
+    // Only now, with the activation's values gone: scales asked for together with the
+    // rows would live in registers that there are none of, and spilling them waits
+    // for the load.
+    if (n + 1 < count) ask_scales(n + 1);
     if (inside) {
       if (p.dx_image.data) {
-        store_columns(act, p.act_image, f0, slab, b, word_a);
         store_columns(dg, p.dx_image, f0, slab, b, word_g);
         store_columns(du, p.dx_image, p.K + f0, slab, b, word_u);
       }
@@ -803,8 +818,8 @@ fg_status fg_swiglu_backward(int mode, const void* dy, int type, int64_t R, int6
                  columns ? Image{static_cast<uint8_t*>(dx_data), static_cast<uint8_t*>(dx_sf), static_cast<int>(slabs)} : none,
                  columns ? Image{static_cast<uint8_t*>(act_data), static_cast<uint8_t*>(act_sf), static_cast<int>(slabs)} : none,
                  static_cast<int>(T), static_cast<int>(R), E, static_cast<int>(K), top_k};
-  // column tiles are shared out over blocks until there are eight for an SM
-  const int64_t tiles = tiles_of(K), shares = (8 * sm_count() + slabs - 1) / slabs;
+  // column tiles are shared out over blocks until there are sixteen for an SM
+  const int64_t tiles = tiles_of(K), shares = (16 * sm_count() + slabs - 1) / slabs;
   const dim3 grid(static_cast<unsigned>(tiles < shares ? tiles : shares), static_cast<unsigned>(slabs));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaErrorInvalidValue;

@@ -78,6 +78,44 @@ __device__ __forceinline__ SlabRows slab_rows(const int32_t* offsets, int R, int
   return q;
 }
 
+// The clamped offsets offs[0..E] and the slabs before each expert, slabs[0..E], by
+// one warp (offsets null: one expert with all R rows); never more than `most` slabs.
+__device__ __forceinline__ void read_slabs(const int32_t* offsets, int R, int E, int most, int* offs, int* slabs) {
+  const int lane = threadIdx.x & 31;
+  if (!offsets) {
+    if (lane < 2) {
+      offs[lane] = lane * R;
+      slabs[lane] = lane * min((R + kPlaces - 1) / kPlaces, most);
+    }
+    return;
+  }
+  int top = 0, before_all = 0;
+  for (int e0 = 0; e0 <= E; e0 += 32) {
+    const int e = e0 + lane;
+    int o = e <= E ? min(max(__ldg(offsets + e), 0), R) : 0;
+    o = max(o, top);
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int x = __shfl_up_sync(0xffffffffu, o, d);
+      if (lane >= d) o = max(o, x);
+    }
+    int before = __shfl_up_sync(0xffffffffu, o, 1);
+    if (lane == 0) before = e0 == 0 ? o : top;
+    int sum = (o - before + kPlaces - 1) / kPlaces;  // of expert e - 1
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int x = __shfl_up_sync(0xffffffffu, sum, d);
+      if (lane >= d) sum += x;
+    }
+    if (e <= E) {
+      offs[e] = o;
+      slabs[e] = min(before_all + sum, most);
+    }
+    top = __shfl_sync(0xffffffffu, o, 31);
+    before_all += __shfl_sync(0xffffffffu, sum, 31);
+  }
+}
+
 // Descriptor of a column operand with C columns and P places.
 inline void column_descriptor(int64_t C, int64_t P, void* data, void* sf, fg_bshuf* out) {
   fg_bshuf d;

@@ -116,36 +116,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   }
   pdl_wait();
   if (threadIdx.x == 0) pdl_launch_dependents();
-  // The offsets as the quantiser of the operands reads them: clamped, each at
-  // least the one before it; and never more slabs than the operands have.
-  if (warp == 2) {
-    int top = 0, slabs = 0;
-    for (int e0 = 0; e0 <= p.E; e0 += 32) {
-      const int e = e0 + lane;
-      int o = e <= p.E ? min(max(__ldg(p.offsets + e), 0), p.R) : 0;
-      o = max(o, top);
-#pragma unroll
-      for (int d = 1; d < 32; d *= 2) {
-        const int x = __shfl_up_sync(0xffffffffu, o, d);
-        if (lane >= d) o = max(o, x);
-      }
-      int before = __shfl_up_sync(0xffffffffu, o, 1);
-      if (lane == 0) before = e0 == 0 ? o : top;
-      int n = (o - before + kPlaces - 1) / kPlaces;  // of expert e - 1
-      int sum = n;
-#pragma unroll
-      for (int d = 1; d < 32; d *= 2) {
-        const int x = __shfl_up_sync(0xffffffffu, sum, d);
-        if (lane >= d) sum += x;
-      }
-      if (e <= p.E) {
-        offs_sh[e] = o;
-        slab_sh[e] = min(slabs + sum, p.slabs);
-      }
-      top = __shfl_sync(0xffffffffu, o, 31);
-      slabs += __shfl_sync(0xffffffffu, sum, 31);
-    }
-  }
+  // the offsets as the quantiser of the operands reads them
+  if (warp == 2) read_slabs(p.offsets, p.R, p.E, p.slabs, offs_sh, slab_sh);
   tc_fence_before();
   __syncthreads();
   // both SMs' barriers exist before either's copies or commits reach them
