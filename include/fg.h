@@ -434,7 +434,7 @@ FG_API fg_status fg_columns_size(int64_t C, int64_t R, int E, int64_t* places, u
  *          holds e4m3 codes (ldx = C) with scales as fg_quantize gives them for
  *          MXFP8, MXFP8_B32, MXFP4_FP8A or FP8_BLOCK128.
  * Scales and codes as fg_quantize's 32-blocks, along the places.  Errors:
- * INVALID_ARG, SHAPE, ALIGN, UNSUPPORTED_ARCH, CUDA.
+ * INVALID_ARG, SHAPE, ALIGN (x and its rows 16 bytes, data 128, sf 16), UNSUPPORTED_ARCH, CUDA.
  */
 FG_API fg_status fg_quantize_columns(int mode, const void* x, const void* scales, int type, int64_t T, int64_t C,
                                      int64_t ldx, const int32_t* rows, int64_t R, const int32_t* offsets, int E,
@@ -443,7 +443,8 @@ FG_API fg_status fg_quantize_columns(int mode, const void* x, const void* scales
 /*
  * Backward pass of y = silu(g) * u from the checkpoint's g and u, for the gradient
  * dy [R][K] of the experts' rows (type fp32 or bf16, rows ldd apart).  With s = 1 /
- * (1 + exp(-g)) and w the row's routing weight (1 without weights), in 32 bits:
+ * (1 + exp(-g)), 0 where that is under 2^-126, and w the row's routing weight (1
+ * without weights), in 32 bits:
  *   dg = w dy u s (1 + g (1 - s)),  du = w dy g s,  act = g s u.
  *  codes, scales  of (dg, du) [R][2K] in `mode`, which is the checkpoint's too;
  *  dx             (dg, du) in dy's type (NULL: not wanted);

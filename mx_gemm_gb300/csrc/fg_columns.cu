@@ -133,8 +133,9 @@ __device__ __forceinline__ void store_columns(const Square& v, const Image& im, 
   const float mine = e8m0_down(finite ? c : 127);
   const bool whole = __all_sync(0xffffffffu, finite);
   const int row = (f0 & 127) + fl * 8;
-  uint8_t* out = im.data + (static_cast<size_t>(f0 >> 7) * im.slabs + slab) * kColumnSlab + row * 128 + (tl & 3) * 4;
-  const int piece = 2 * b + (tl >> 2);  // 16-byte piece of a column's places
+  // 16-byte piece 2 b + tl / 4 of a column's places; column j has it at piece ^ j
+  const uintptr_t out = reinterpret_cast<uintptr_t>(im.data) + (static_cast<size_t>(f0 >> 7) * im.slabs + slab) * kColumnSlab +
+                        row * 128 + (2 * b + (tl >> 2)) * 16 + (tl & 3) * 4;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     // the lane that kept column j: bits 16, 8, 4 of its index are those of j
@@ -149,9 +150,9 @@ __device__ __forceinline__ void store_columns(const Square& v, const Image& im, 
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[i] = make_float2(lo ? x[i].x : 0.f, hi ? x[i].y : 0.f);
     }
-    *reinterpret_cast<uint32_t*>(out + 2 * q * 128 + ((piece ^ (2 * q)) << 4)) =
+    *reinterpret_cast<uint32_t*>((out ^ (2 * q * 16)) + 2 * q * 128) =
         e4m3x2(x[0].x, x[1].x) | (e4m3x2(x[2].x, x[3].x) << 16);
-    *reinterpret_cast<uint32_t*>(out + (2 * q + 1) * 128 + ((piece ^ (2 * q + 1)) << 4)) =
+    *reinterpret_cast<uint32_t*>((out ^ ((2 * q + 1) * 16)) + (2 * q + 1) * 128) =
         e4m3x2(x[0].y, x[1].y) | (e4m3x2(x[2].y, x[3].y) << 16);
   }
 }
@@ -312,10 +313,9 @@ __device__ __forceinline__ void fetch8(void* dst, const void* src, bool there) {
 
 // With g, u the checkpoint's values, s = sigmoid(g) and w the row's routing weight:
 //   act = g s u,  dots = sum dy act,  dg = w dy u s (1 + g (1 - s)),  du = w dy g s.
-// e = exp(-g) and 16 s = 1 / (1/16 + e/16) come from the fast power and reciprocal (2
-// ulp each); the reciprocal of the sum itself would be flushed for g between -88.7,
-// below which s is 0, and -87.3.  g (1 - s) is g s e, without the cancellation of 1 - s
-// that a large g would multiply.
+// e = exp(-g), held below 2^128, and s = 1 / (1 + e) come from the fast power and
+// reciprocal (2 ulp each), so s is 0 below g = -87.3, where it is under 2^-126.  g (1 -
+// s) is g s e, without the cancellation of 1 - s that a large g would multiply.
 //
 // A block of threads takes one slab's 128 rows x 128 columns at a time, 32 rows in
 // turn, and asks for the next 32 rows' bytes before it works on these: with four
@@ -429,13 +429,14 @@ __global__ void __launch_bounds__(kThreads, 4) swiglu_backward_kernel(const Swig
       for (int c = 0; c < 4; ++c) {
         constexpr float kLog2e = 1.44269504088896341f;
         float2 e = halves(mul(g[c], pair_of(-kLog2e, -kLog2e)));
+        e = make_float2(fminf(e.x, 127.9f), fminf(e.y, 127.9f));  // (a NaN is in g too)
         asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.x));
         asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.y));
-        float2 h = halves(fma(pair_of(e.x, e.y), pair_of(0.0625f, 0.0625f), pair_of(0.0625f, 0.0625f)));
+        const Pair ee = pair_of(e.x, e.y), one = pair_of(1.f, 1.f);
+        float2 h = halves(add(ee, one));
         asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(h.x));
         asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(h.y));
-        const Pair sg = mul(pair_of(h.x, h.y), pair_of(0.0625f, 0.0625f)), gs_ = mul(g[c], sg);
-        const Pair up = fma(gs_, pair_of(fminf(e.x, 3.4e38f), fminf(e.y, 3.4e38f)), pair_of(1.f, 1.f));  // 1 + g (1 - s)
+        const Pair sg = pair_of(h.x, h.y), gs_ = mul(g[c], sg), up = fma(gs_, ee, one);  // up: 1 + g (1 - s)
         const Pair a = mul(gs_, u[c]), d = mul(dy[c], pair_of(w, w));
         sum = fma(dy[c], a, sum);
         act.p[i][c] = mul(a, pair_of(w, w));
@@ -685,7 +686,7 @@ fg_status check_8bit(const char* what, int mode, const void* codes, const void* 
 
 fg_status check_image(const char* what, const void* data, const void* sf, const void* desc) {
   if (!data || !sf || !desc) return fail(FG_ERR_INVALID_ARG, "%s: null image, scale image or descriptor", what);
-  if (!aligned(data, 16) || !aligned(sf, 16)) return fail(FG_ERR_ALIGN, "%s: images must be 16-byte aligned", what);
+  if (!aligned(data, 128) || !aligned(sf, 16)) return fail(FG_ERR_ALIGN, "%s: images must be 128-byte aligned, scale images 16-byte", what);
   return FG_OK;
 }
 

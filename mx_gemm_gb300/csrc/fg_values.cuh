@@ -83,6 +83,11 @@ __device__ __forceinline__ Pair mul(Pair a, Pair b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(p) : "l"(a), "l"(b));
   return p;
 }
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
+  Pair p;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(p) : "l"(a), "l"(b));
+  return p;
+}
 __device__ __forceinline__ Pair fma(Pair a, Pair b, Pair c) {
   Pair p;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p) : "l"(a), "l"(b), "l"(c));

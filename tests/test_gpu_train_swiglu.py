@@ -23,21 +23,21 @@ def formula(dy, g, u, w):
     """fp64 (dg, du), act, dots and the magnitudes that their errors are measured by.
 
     exp(-g)'s exponent, -g log2(e), is rounded once: by up to 2^-24 of itself, which
-    multiplies the result by up to 1 + 2^-24 |g| = 1 + REL |g| / 64.  Below g = -88.7 it
-    is past 32 bits and s, under 2^-127, counts as 0."""
+    multiplies the result by up to 1 + 2^-24 |g| = 1 + REL |g| / 64.  Where s is under
+    2^-126 = REL 2^-108 it counts as 0."""
     s = torch.sigmoid(g)
     rest = torch.sigmoid(-g)
     act = g * s * u
     dg = w * dy * u * s * (1 + g * rest)
     du = w * dy * g * s
     mag = torch.cat([(w * dy * u * s).abs() * (1 + (g * rest).abs()), du.abs()], dim=1)
-    mag = mag * (1 + g.abs().repeat(1, 2) / 64) + (w * dy * (1 + g.abs()) * (1 + u.abs())).abs().repeat(1, 2) * 2.0 ** -109
+    mag = mag * (1 + g.abs().repeat(1, 2) / 64) + (w * dy * (1 + g.abs()) * (1 + u.abs())).abs().repeat(1, 2) * 2.0 ** -108
     return torch.cat([dg, du], dim=1), mag, act, (dy * act)
 
 
 def act_mag(g, u, w=1.0):
     """The magnitude for w * act, likewise."""
-    return (w * (g * torch.sigmoid(g) * u)).abs() * (1 + g.abs() / 64) + w * (g * u).abs() * 2.0 ** -109
+    return (w * (g * torch.sigmoid(g) * u)).abs() * (1 + g.abs() / 64) + w * (g * u).abs() * 2.0 ** -108
 
 
 def slot_weights(r, rows):

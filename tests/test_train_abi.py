@@ -58,7 +58,7 @@ def columns(fg, mode=0, x=P, scales=0, type=1, T=40, C=256, ldx=256, rows=2 * P,
     (dict(E=1025), "SHAPE"), (dict(C=192, ldx=192), "SHAPE"), (dict(C=0), "SHAPE"), (dict(R=-1), "SHAPE"), (dict(T=0), "SHAPE"),
     (dict(T=-1), "SHAPE"), (dict(rows=0), "SHAPE"), (dict(R=1 << 21), "SHAPE"), (dict(ldx=128), "SHAPE"),
     (dict(mode=5, scales=P, ldx=512), "SHAPE"), (dict(x=P + 8), "ALIGN"), (dict(ldx=257), "ALIGN"), (dict(rows=P + 2), "ALIGN"),
-    (dict(offsets=P + 2), "ALIGN"), (dict(data=P + 8), "ALIGN"), (dict(sf=P + 8), "ALIGN"),
+    (dict(offsets=P + 2), "ALIGN"), (dict(data=P + 64), "ALIGN"), (dict(sf=P + 8), "ALIGN"),
     (dict(mode=2, scales=P + 2), "ALIGN"),
 ])
 def test_columns_refusals(fg, bad, status):  # noqa: F811
@@ -95,7 +95,7 @@ def backward(fg, mode=5, dy=P, type=1, R=80, K=256, ldd=256, saved=2 * P, saved_
     (dict(K=160, ldd=160), "SHAPE"), (dict(mode=2, K=96, ldd=96, dxd=0, dxs=0, ad=0, asf=0), "SHAPE"), (dict(ldd=128), "SHAPE"),
     (dict(k=0), "SHAPE"), (dict(k=33), "SHAPE"), (dict(T=0), "SHAPE"), (dict(T=-1), "SHAPE"), (dict(R=1 << 21), "SHAPE"),
     (dict(dy=P + 8), "ALIGN"), (dict(ldd=257), "ALIGN"), (dict(saved=P + 8), "ALIGN"), (dict(codes=P + 8), "ALIGN"),
-    (dict(dx=P + 8), "ALIGN"), (dict(weights=P + 2), "ALIGN"), (dict(offsets=P + 2), "ALIGN"), (dict(dxd=P + 8), "ALIGN"),
+    (dict(dx=P + 8), "ALIGN"), (dict(weights=P + 2), "ALIGN"), (dict(offsets=P + 2), "ALIGN"), (dict(dxd=P + 64), "ALIGN"),
     (dict(ws=P + 2), "ALIGN"), (dict(ws=0), "WORKSPACE"), (dict(bytes=64), "WORKSPACE"),
 ])
 def test_backward_refusals(fg, bad, status):  # noqa: F811
