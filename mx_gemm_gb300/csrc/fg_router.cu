@@ -50,15 +50,26 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-__device__ __forceinline__ float warp_max(float v) {
+// N sums over the warp, their steps next to one another.
+template <int N>
+__device__ __forceinline__ void warp_sums(float (&v)[N]) {
 #pragma unroll
-  for (int d = 16; d > 0; d /= 2) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
-  return v;
+  for (int d = 16; d > 0; d /= 2) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
+  }
 }
 
-// p of a lane's logits, and their largest (-infinity: nothing to pick, all p 0).
+__device__ __forceinline__ float warp_max(float v) {
+  float m;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+  return m;
+}
+
+// exp(l - top) of a lane's logits (0 for -infinity and NaN) and the largest, `top`
+// (-infinity: nothing to pick).
 template <typename T, int VPL>
-__device__ __forceinline__ float softmax(const Logits<T, VPL>& l, float (&p)[VPL]) {
+__device__ __forceinline__ float exponentials(const Logits<T, VPL>& l, float (&p)[VPL]) {
   float top = -INFINITY;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
@@ -66,22 +77,15 @@ __device__ __forceinline__ float softmax(const Logits<T, VPL>& l, float (&p)[VPL
     top = fmaxf(top, p[i]);  // (a NaN is not kept)
   }
   top = warp_max(top);
-  float sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    p[i] = p[i] > -INFINITY ? exp_below(p[i], top) : 0.f;
-    sum += p[i];
-  }
-  sum = warp_sum(sum);
-  const float r = sum > 0.f ? 1.f / sum : 0.f;
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) p[i] *= r;
+  for (int i = 0; i < VPL; ++i) p[i] = p[i] > -INFINITY ? exp_below(p[i], top) : 0.f;
   return top;
 }
 
 // Loss, counts, mean probabilities and slopes from the sums of `blocks` rows of
 // [E + 1], by the whole block.
 __device__ void finish(const BalanceParams& p, const float* part, int blocks) {
+  __shared__ float group_sh[1024];
   __shared__ float sum_sh[32];
   __shared__ int count_sh[32];
   __shared__ float tokens_sh;
@@ -103,25 +107,37 @@ __device__ void finish(const BalanceParams& p, const float* part, int blocks) {
   const float per_choice = total > 0 ? 1.f / static_cast<float>(total) : 0.f;
   const float per_token = tokens_sh > 0.f ? 1.f / tokens_sh : 0.f;
   const float c = p.coefficient * static_cast<float>(p.E);
+  // the blocks' rows are shared out over groups of threads, one thread an expert
+  const int width = (p.E + 31) / 32 * 32, groups = max(1, static_cast<int>(blockDim.x) / width);
+  const int g = threadIdx.x / width;
   float loss = 0.f;
-  for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
-    float s[4] = {};
-    int b = 0;
-    for (; b + 16 <= blocks; b += 16) {
-      float v[16];
+  for (int e0 = 0; e0 < p.E; e0 += groups > 1 ? width : static_cast<int>(blockDim.x)) {
+    const int e = e0 + (groups > 1 ? threadIdx.x - g * width : threadIdx.x);
+    float s = 0.f;
+    if (g < groups && e < p.E) {
+      for (int b = g; b < blocks; b += 8 * groups) {
+        float v[8];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = part[static_cast<size_t>(b + i) * stride + e];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) s[i & 3] += v[i];
+        for (int i = 0; i < 8; ++i) v[i] = b + i * groups < blocks ? part[static_cast<size_t>(b + i * groups) * stride + e] : 0.f;
+        s += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+      }
     }
-    for (; b < blocks; ++b) s[b & 3] += part[static_cast<size_t>(b) * stride + e];
-    const float prob = ((s[0] + s[1]) + (s[2] + s[3])) * per_token;
-    const int n = max(__ldg(p.offsets + e + 1) - __ldg(p.offsets + e), 0);
-    const float f = static_cast<float>(n) * per_choice;
-    p.probs[e] = prob;
-    p.counts[e] = n;
-    p.slopes[e] = c * f * per_token;
-    loss = fmaf(f, prob, loss);
+    if (groups > 1) {
+      group_sh[threadIdx.x] = s;
+      __syncthreads();
+      if (g == 0) {
+        for (int i = 1; i < groups; ++i) s += group_sh[i * width + threadIdx.x];
+      }
+    }
+    if ((groups == 1 || g == 0) && e < p.E) {
+      const float prob = s * per_token;
+      const int n = max(__ldg(p.offsets + e + 1) - __ldg(p.offsets + e), 0);
+      const float f = static_cast<float>(n) * per_choice;
+      p.probs[e] = prob;
+      p.counts[e] = n;
+      p.slopes[e] = c * f * per_token;
+      loss = fmaf(f, prob, loss);
+    }
   }
   loss = warp_sum(loss);
   if (lane == 0) sum_sh[warp] = loss;
@@ -133,10 +149,14 @@ __device__ void finish(const BalanceParams& p, const float* part, int blocks) {
   }
 }
 
+// Warps of a block at most: with 32 a thread has 64 registers, which sums of more
+// than eight experts a lane outgrow.
+constexpr int balance_warps(int vpl) { return vpl <= 8 ? 32 : (vpl <= 16 ? 16 : 8); }
+
 // Blocks' sums of p; alone (one block) also the rest.  Dynamic shared memory:
 // [warps][E + 1].
 template <typename T, int VPL>
-__global__ void __launch_bounds__(512) balance_kernel(const BalanceParams p) {
+__global__ void __launch_bounds__(32 * balance_warps(VPL)) balance_kernel(const BalanceParams p) {
   extern __shared__ float sums_sh[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int stride = p.E + 1;
@@ -151,10 +171,14 @@ __global__ void __launch_bounds__(512) balance_kernel(const BalanceParams p) {
   for (; t < p.T; t += step) {
     const Logits<T, VPL> now = next;
     if (t + step < p.T) next.load(p, t + step, lane);  // on its way during this token's work
-    float v[VPL];
-    tokens += softmax(now, v) > -INFINITY;
+    float v[VPL], sum = 0.f;
+    tokens += exponentials(now, v) > -INFINITY;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) acc[i] += v[i];
+    for (int i = 0; i < VPL; ++i) sum += v[i];
+    sum = warp_sum(sum);
+    const float r = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) acc[i] = fmaf(v[i], r, acc[i]);
   }
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
@@ -228,32 +252,35 @@ __global__ void __launch_bounds__(256) route_backward_kernel(const BackwardParam
     }
     if (t + step < p.T) next.load(p, t + step, lane);
     float v[VPL];
-    const float top = softmax(now, v);
-    float dot = 0.f;
+    const float top = exponentials(now, v);
+    // sums of the exponentials, of their products with the slopes, and of the chosen
+    // ones' and theirs with dweights
+    const float q = expert >= 0 && chosen > -INFINITY ? exp_below(chosen, top) : 0.f;
+    float sums[4] = {0.f, 0.f, q, q * dw};
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) dot = fmaf(v[i], slope[i], dot);
-    dot = warp_sum(dot);
+    for (int i = 0; i < VPL; ++i) {
+      sums[0] += v[i];
+      sums[1] = fmaf(v[i], slope[i], sums[1]);
+    }
+    warp_sums(sums);
+    const float r = sums[0] > 0.f ? 1.f / sums[0] : 0.f;
+    const float share = p.renormalize ? (sums[2] > 0.f ? 1.f / sums[2] : 0.f) : r;
+    const float mean = sums[3] * share;
+    const float dot = fmaf(sums[1], r, p.renormalize ? 0.f : mean);
     if (p.dweights) {
-      // q over the chosen; a share of all experts is scaled by what the others hold
-      float q = expert >= 0 && chosen > -INFINITY ? exp_below(chosen, top) : 0.f;
-      float sum;
-      if (p.renormalize) {
-        sum = warp_sum(q);
-      } else {
-        float all = 0.f;  // the softmax's sum again, from its largest p = 1 / sum
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) all = fmaxf(all, v[i]);
-        all = warp_max(all);
-        sum = all > 0.f ? 1.f / all : 0.f;
+      float add = q * share * (p.renormalize ? dw - mean : dw);
+      // an expert that a token names twice (routing never does) takes both, in their order
+      const unsigned peers = __match_any_sync(0xffffffffu, expert);
+      const bool twice = expert >= 0 && (peers & (peers - 1)) != 0;
+      if (__any_sync(0xffffffffu, twice)) {
+        float sum = 0.f;
+        for (int j = 0; j < 32; ++j) {
+          const float other = __shfl_sync(0xffffffffu, add, j);
+          if ((peers >> j) & 1u) sum += other;
+        }
+        add = sum;
       }
-      q = sum > 0.f ? q / sum : 0.f;
-      const float mean = warp_sum(q * dw);
-      if (p.renormalize) {
-        if (expert >= 0) atomicAdd(row + expert, q * (dw - mean));
-      } else {
-        if (expert >= 0) atomicAdd(row + expert, q * dw);
-        dot += mean;
-      }
+      if (expert >= 0) row[expert] = add;
       __syncwarp();
     }
     T* out = static_cast<T*>(p.out) + t * p.E;
@@ -263,11 +290,8 @@ __global__ void __launch_bounds__(256) route_backward_kernel(const BackwardParam
       float d[L::V];
 #pragma unroll
       for (int i = 0; i < L::V; ++i) {
-        d[i] = v[c + i] * (slope[c + i] - dot);
-        if (p.dweights && e0 + i < p.E) {
-          d[i] += row[e0 + i];
-          row[e0 + i] = 0.f;
-        }
+        d[i] = v[c + i] * r * (slope[c + i] - dot);
+        if (p.dweights && e0 + i < p.E) d[i] += row[e0 + i];
       }
       if (p.whole_out && e0 + L::V <= p.E) {
         constexpr int BYTES = L::V * sizeof(T);
@@ -284,6 +308,8 @@ __global__ void __launch_bounds__(256) route_backward_kernel(const BackwardParam
           if (e0 + i < p.E) out[e0 + i] = static_cast<T>(d[i]);
       }
     }
+    __syncwarp();
+    if (expert >= 0) row[expert] = 0.f;
     __syncwarp();
   }
 }
@@ -314,18 +340,21 @@ cudaError_t by_share(int E, F f) {
   return f(std::integral_constant<int, 32>());
 }
 
-// Warps of a block whose rows of E values fit 32 KB.
+// Warps of a block of the gradient whose rows of E values fit 32 KB.
 int warps_for(int E, int most) {
   int w = most;
   while (w > 4 && w * (E + 1) * 4 > 33 * 1024) w /= 2;
   return w;
 }
 
-constexpr int kBalanceWarps = 16, kBackwardWarps = 8;
+constexpr int kBackwardWarps = 8;
 
-// One block alone up to four tokens a warp, else up to two blocks an SM.
+// Warps of a block of the balance loss for E experts (their rows fit 33 KB).
+int warps_of_balance(int E) { return E <= 256 ? balance_warps(8) : (E <= 512 ? balance_warps(16) : balance_warps(32)); }
+
+// One block alone up to four tokens a warp, else up to one an SM.
 int balance_blocks(int64_t T, int E) {
-  const int warps = warps_for(E, kBalanceWarps);
+  const int warps = warps_of_balance(E);
   if (T <= 4 * warps) return 1;
   const int64_t want = (T + 2 * warps - 1) / (2 * warps), most = sm_count();
   return static_cast<int>(want < most ? want : most);
@@ -386,7 +415,7 @@ fg_status fg_moe_balance_loss(const void* logits, int type, int64_t T, int E, in
   BalanceParams p{logits, offsets, static_cast<float*>(workspace), loss, counts, probs, slopes, T, ldl, coefficient, E,
                   whole_rows(logits, type, T, E, ldl)};
   const int blocks = balance_blocks(T, E);
-  int warps = warps_for(E, kBalanceWarps);
+  int warps = warps_of_balance(E);
   if (T < warps) warps = T < 4 ? 4 : static_cast<int>(T);
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr;
@@ -397,7 +426,7 @@ fg_status fg_moe_balance_loss(const void* logits, int type, int64_t T, int E, in
                                : cudaLaunchKernelEx(&cfg, balance_kernel<__nv_bfloat16, VPL>, p);
   });
   if (e == cudaSuccess && blocks > 1) {
-    config(cfg, attr, 1, E <= 256 ? 256 : 1024, 0, static_cast<cudaStream_t>(stream));
+    config(cfg, attr, 1, 1024, 0, static_cast<cudaStream_t>(stream));
     e = cudaLaunchKernelEx(&cfg, balance_finish_kernel, p, blocks);
   }
   return e == cudaSuccess ? FG_OK : cuda_fail(e, "balance loss launch");
