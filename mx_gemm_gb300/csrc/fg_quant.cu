@@ -170,33 +170,41 @@ __global__ void __launch_bounds__(256) quantize_kernel(const T* __restrict__ x, 
 // pass: 4 bytes read and 3 written per value of the activation, where three calls
 // of the quantiser read 8.  Bound by HBM: 32761 x 2048 in 32-K blocks in 93 us
 // (5.1 TB/s).
-template <int MODE, typename T>
+template <int MODE, int ROWS, typename T>
 __global__ void __launch_bounds__(256) checkpoint_kernel(const T* __restrict__ x, int64_t M, int64_t K, int64_t ldx,
                                                          void* __restrict__ codes, void* __restrict__ scales,
                                                          void* __restrict__ saved, void* __restrict__ saved_scales) {
   pdl_wait();
   pdl_launch_dependents();
   const int64_t cpr = K / kVec;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * (blockDim.y * ROWS) + threadIdx.y;
   const int64_t c = static_cast<int64_t>(blockIdx.y) * blockDim.x + threadIdx.x;
-  const bool live = row < M && c < cpr;
-  Raw8<T> a, b;
-  a.zero();
-  b.zero();
-  if (live) {
-    const T* src = x + row * ldx + c * kVec;
-    a.load_once(src);
-    b.load_once(src + K);
-  }
-  float v[kVec], u[kVec];
-  a.widen(v);
-  b.widen(u);
+  Raw8<T> a[ROWS], b[ROWS];
 #pragma unroll
-  for (int j = 0; j < kVec; j += 2) swiglu2(v[j], v[j + 1], u[j], u[j + 1]);
-  quantize8<MODE>(v, live, static_cast<size_t>(row * cpr + c), codes, scales);
-  a.widen(v);
-  quantize8<MODE>(v, live, static_cast<size_t>(2 * row * cpr + c), saved, saved_scales);
-  quantize8<MODE>(u, live, static_cast<size_t>((2 * row + 1) * cpr + c), saved, saved_scales);
+  for (int i = 0; i < ROWS; ++i) {
+    const int64_t row = row0 + i * blockDim.y;
+    a[i].zero();
+    b[i].zero();
+    if (row < M && c < cpr) {
+      const T* src = x + row * ldx + c * kVec;
+      a[i].load_once(src);
+      b[i].load_once(src + K);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    const int64_t row = row0 + i * blockDim.y;
+    const bool live = row < M && c < cpr;
+    float v[kVec], u[kVec];
+    a[i].widen(v);
+    b[i].widen(u);
+#pragma unroll
+    for (int j = 0; j < kVec; j += 2) swiglu2(v[j], v[j + 1], u[j], u[j + 1]);
+    quantize8<MODE>(v, live, static_cast<size_t>(row * cpr + c), codes, scales);
+    a[i].widen(v);
+    quantize8<MODE>(v, live, static_cast<size_t>(2 * row * cpr + c), saved, saved_scales);
+    quantize8<MODE>(u, live, static_cast<size_t>((2 * row + 1) * cpr + c), saved, saved_scales);
+  }
 }
 
 // -------------------------------------------------------- RMS norm, quantise
@@ -324,12 +332,15 @@ cudaError_t launch_checkpoint(const void* x, int64_t M, int64_t K, int64_t ldx, 
                               void* saved_scales, cudaStream_t st) {
   const int64_t cpr = K / kVec;
   const int bx = thread_columns(cpr), by = 256 / bx;
+  const int64_t cols = (cpr + bx - 1) / bx;
+  const bool many = (M + 2 * by - 1) / (2 * by) * cols >= 8 * sm_count();  // as in launch_quantize
+  const int64_t rows = many ? 2 * by : by;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr;
-  pdl_config(cfg, attr, dim3(static_cast<unsigned>((M + by - 1) / by), static_cast<unsigned>((cpr + bx - 1) / bx)), dim3(bx, by),
-             st);
-  return cudaLaunchKernelEx(&cfg, checkpoint_kernel<MODE, T>, static_cast<const T*>(x), M, K, ldx, codes, scales, saved,
-                            saved_scales);
+  pdl_config(cfg, attr, dim3(static_cast<unsigned>((M + rows - 1) / rows), static_cast<unsigned>(cols)), dim3(bx, by), st);
+  const T* src = static_cast<const T*>(x);
+  return many ? cudaLaunchKernelEx(&cfg, checkpoint_kernel<MODE, 2, T>, src, M, K, ldx, codes, scales, saved, saved_scales)
+              : cudaLaunchKernelEx(&cfg, checkpoint_kernel<MODE, 1, T>, src, M, K, ldx, codes, scales, saved, saved_scales);
 }
 
 template <int MODE, int ACT, typename T>

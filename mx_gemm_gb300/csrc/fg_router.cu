@@ -67,18 +67,23 @@ __device__ __forceinline__ float warp_max(float v) {
 }
 
 // exp(l - top) of a lane's logits (0 for -infinity and NaN) and the largest, `top`
-// (-infinity: nothing to pick).
+// (-infinity: nothing to pick; +infinity: the infinite ones share alike).
 template <typename T, int VPL>
 __device__ __forceinline__ float exponentials(const Logits<T, VPL>& l, float (&p)[VPL]) {
   float top = -INFINITY;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
-    p[i] = __uint_as_float(sizeof(T) == 2 ? l.bits[i] << 16 : l.bits[i]);
-    top = fmaxf(top, p[i]);  // (a NaN is not kept)
+    p[i] = fmaxf(__uint_as_float(sizeof(T) == 2 ? l.bits[i] << 16 : l.bits[i]), -INFINITY);  // (a NaN is not kept)
+    top = fmaxf(top, p[i]);
   }
   top = warp_max(top);
+  if (fabsf(top) < INFINITY) {
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) p[i] = p[i] > -INFINITY ? exp_below(p[i], top) : 0.f;
+    for (int i = 0; i < VPL; ++i) p[i] = expf(p[i] - top);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) p[i] = top > 0.f && p[i] == top ? 1.f : 0.f;
+  }
   return top;
 }
 
@@ -97,6 +102,7 @@ __device__ void finish(const BalanceParams& p, const float* part, int blocks) {
   if (lane == 0) count_sh[warp] = mine;
   if (warp == 0) {
     float n = 0.f;  // whole numbers below 2^24 in each partial: exact up to T = 2^24
+#pragma unroll 8
     for (int b = lane; b < blocks; b += 32) n += part[static_cast<size_t>(b) * stride + p.E];
     n = warp_sum(n);
     if (lane == 0) tokens_sh = n;
@@ -206,6 +212,8 @@ __global__ void __launch_bounds__(1024) balance_finish_kernel(const BalanceParam
 
 // ----------------------------------------------------------- logits' gradient
 
+constexpr int kBackwardWarps = 8;
+
 struct BackwardParams {
   const void* logits;
   const int32_t* experts;  // [T][k] (dweights given)
@@ -216,14 +224,14 @@ struct BackwardParams {
   int E, k, renormalize, whole, whole_out;
 };
 
-// Dynamic shared memory: a row of E values for each warp, zero between tokens.
+// Shared memory: a row of values for each warp, zero between tokens.
 template <typename T, int VPL>
-__global__ void __launch_bounds__(256) route_backward_kernel(const BackwardParams p) {
+__global__ void __launch_bounds__(32 * kBackwardWarps) route_backward_kernel(const BackwardParams p) {
   using L = Logits<T, VPL>;
-  extern __shared__ float rows_sh[];
+  __shared__ __align__(16) float rows_sh[kBackwardWarps][32 * VPL];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  float* row = rows_sh + warp * p.E;
-  for (int e = lane; e < p.E; e += 32) row[e] = 0.f;
+  float* row = rows_sh[warp];
+  for (int e = lane; e < 32 * VPL; e += 32) row[e] = 0.f;
   __syncwarp();
   pdl_wait();
   pdl_launch_dependents();
@@ -287,11 +295,17 @@ __global__ void __launch_bounds__(256) route_backward_kernel(const BackwardParam
 #pragma unroll
     for (int c = 0; c < VPL; c += L::V) {
       const int e0 = L::expert(c, lane);
-      float d[L::V];
+      alignas(16) float d[L::V];
+      if constexpr (L::V % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < L::V; i += 4) *reinterpret_cast<float4*>(&d[i]) = *reinterpret_cast<const float4*>(row + e0 + i);
+      } else {
+#pragma unroll
+        for (int i = 0; i < L::V; ++i) d[i] = row[e0 + i];
+      }
 #pragma unroll
       for (int i = 0; i < L::V; ++i) {
-        d[i] = v[c + i] * r * (slope[c + i] - dot);
-        if (p.dweights && e0 + i < p.E) d[i] += row[e0 + i];
+        d[i] = fmaf(v[c + i] * r, slope[c + i] - dot, d[i]);
       }
       if (p.whole_out && e0 + L::V <= p.E) {
         constexpr int BYTES = L::V * sizeof(T);
@@ -339,15 +353,6 @@ cudaError_t by_share(int E, F f) {
   if (vpl <= 16) return f(std::integral_constant<int, 16>());
   return f(std::integral_constant<int, 32>());
 }
-
-// Warps of a block of the gradient whose rows of E values fit 32 KB.
-int warps_for(int E, int most) {
-  int w = most;
-  while (w > 4 && w * (E + 1) * 4 > 33 * 1024) w /= 2;
-  return w;
-}
-
-constexpr int kBackwardWarps = 8;
 
 // Warps of a block of the balance loss for E experts (their rows fit 33 KB).
 int warps_of_balance(int E) { return E <= 256 ? balance_warps(8) : (E <= 512 ? balance_warps(16) : balance_warps(32)); }
@@ -448,11 +453,10 @@ fg_status fg_moe_route_backward(const void* logits, int type, int64_t T, int E, 
   if ((s = check_arch()) != FG_OK) return s;
   BackwardParams p{logits, experts, dweights, slopes, out, T, ldl, E, top_k, (flags & FG_FLAG_RENORMALIZE) ? 1 : 0,
                    whole_rows(logits, type, T, E, ldl), whole_rows(out, type, T, E, E)};
-  const int warps = warps_for(E, kBackwardWarps);
-  const int64_t want = (T + warps - 1) / warps, most = 8 * static_cast<int64_t>(sm_count());
+  const int64_t want = (T + kBackwardWarps - 1) / kBackwardWarps, most = 8 * static_cast<int64_t>(sm_count());
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr;
-  config(cfg, attr, want < most ? want : most, 32 * warps, warps * E * 4, static_cast<cudaStream_t>(stream));
+  config(cfg, attr, want < most ? want : most, 32 * kBackwardWarps, 0, static_cast<cudaStream_t>(stream));
   const cudaError_t e = by_share(E, [&](auto share) {
     constexpr int VPL = decltype(share)::value;
     return type == FG_TYPE_F32 ? cudaLaunchKernelEx(&cfg, route_backward_kernel<float, VPL>, p)

@@ -130,6 +130,27 @@ __device__ __forceinline__ float f32_scale_of(uint32_t amax) {
                    : (amax < (1u << 17) ? __uint_as_float((amax + 447u) / 448u) : __fdiv_rn(__uint_as_float(amax), 448.f));
 }
 
+// v / s for a block's fp32 scale s, rounded to nearest: with r = 1 / s rounded to nearest
+// and q = v r, the remainder v - q s is exact in one fused multiply-add and q + (v - q s)
+// r is the quotient (Markstein 1990, "Computation of elementary functions on the IBM RISC
+// System/6000 processor").  Three instructions for two values, where a division takes ten
+// for one.  It holds where nothing leaves the normal numbers: `sure`, for quotients that
+// are no less than half an e4m3 step; a smaller one's code is 0 whatever its last bits.
+struct Over {
+  Pair r, minus_s;
+  bool sure;
+  __device__ __forceinline__ explicit Over(float s) {
+    const float x = __frcp_rn(s);
+    r = pair_of(x, x);
+    minus_s = pair_of(-s, -s);
+    sure = s > 0x1p-100f && s < 0x1p100f;
+  }
+  __device__ __forceinline__ Pair operator()(Pair v) const {
+    const Pair q = mul(v, r);
+    return fma(fma(q, minus_s, v), r, q);
+  }
+};
+
 // Two values of two e4m3 codes, the lower half's first.
 __device__ __forceinline__ float2 e4m3_values(uint32_t codes) {
   uint32_t h;

@@ -302,3 +302,20 @@ def test_wgrad_that_times_out_says_so_and_the_next_call_is_right():
         fg.set_wait_timeout_ns(4_000_000_000)
     same(fg.grouped_wgrad(a, a, offsets), want)
     assert fg.get_error() == fg.FG_OK
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("size", [0, 30, -30, 110, -110])
+def test_weight_quotients_are_those_of_the_division(dtype, size):
+    """Sixteen million of them, bf16's among which are many next to a border between two codes; and sizes at both ends."""
+    w = torch.ldexp(rand(24, 4096, 4096), torch.tensor(size, device="cuda")).to(dtype)
+    codes, scales = fg.quantize_weight("fp8_block128", w)
+    s = scales.repeat_interleave(128, 0).repeat_interleave(128, 1)
+    want = (w.float() / s).to(torch.float8_e4m3fn)               # (tensor by tensor: rounded once)
+    same(codes.view(torch.uint8), want.view(torch.uint8))
+    # and the row blocks of the gated activation's gradient
+    x = w.float()[:512]
+    saved, saved_scales = fg.quantize("fp8_block128", torch.cat([x * 0 + 88, x * 0 + 1], 1))
+    d = fg.swiglu_backward("fp8_block128", x, saved, saved_scales, plain=True)
+    s = d.scales.repeat_interleave(128, 1)
+    same(d.codes.view(torch.uint8), (d.dx / s).to(torch.float8_e4m3fn).view(torch.uint8))
