@@ -54,16 +54,17 @@ __device__ __forceinline__ void decode(uint2 codes, float scale, Pair (&v)[4]) {
 }
 
 // Eight consecutive values of a row on their way.
+constexpr int scale_block(int fmt) { return fmt == kE8m0By32 ? 32 : 128; }
+
 template <int FMT>
 struct Eight {
+  static constexpr int BYTES = 1;  // of a value
   uint2 codes;
   uint32_t scale;  // as it lies in memory: worked out here, it would be waited for
-  __device__ __forceinline__ void load(const Source& s, int64_t row, int64_t col) {
-    codes = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(s.x) + row * s.ld + col));
-    if (FMT == kF32By128)
-      scale = __ldg(static_cast<const uint32_t*>(s.scales) + row * (s.cols / 128) + col / 128);
-    else
-      scale = __ldg(static_cast<const uint8_t*>(s.scales) + row * (s.cols / (FMT == kE8m0By128 ? 128 : 32)) + col / (FMT == kE8m0By128 ? 128 : 32));
+  __device__ __forceinline__ void load(uintptr_t row, uintptr_t scales, int col) {
+    codes = __ldcs(reinterpret_cast<const uint2*>(row + col));
+    if (FMT == kF32By128) scale = __ldg(reinterpret_cast<const uint32_t*>(scales) + col / scale_block(FMT));
+    else scale = __ldg(reinterpret_cast<const uint8_t*>(scales) + col / scale_block(FMT));
   }
   __device__ __forceinline__ void zero() {
     codes = make_uint2(0, 0);
@@ -76,10 +77,9 @@ struct Eight {
 
 template <typename T>
 struct PlainEight {
+  static constexpr int BYTES = sizeof(T);
   Raw8<T> raw;
-  __device__ __forceinline__ void load(const Source& s, int64_t row, int64_t col) {
-    raw.load_once(static_cast<const T*>(s.x) + row * s.ld + col);
-  }
+  __device__ __forceinline__ void load(uintptr_t row, uintptr_t, int col) { raw.load_once(reinterpret_cast<const T*>(row) + col); }
   __device__ __forceinline__ void zero() { raw.zero(); }
   __device__ __forceinline__ void widen(Pair (&v)[4]) const {
     float f[8];
@@ -114,11 +114,20 @@ __device__ __forceinline__ void halve(uint32_t* m, int bit) {
   }
 }
 
-// The warp's square as 32 columns x 32 places: columns f0 .. + 31, places 32 b .. of
-// slab `slab`.  The scale's byte goes into byte b of `word`, for the column that
-// this lane keeps.
-__device__ __forceinline__ void store_columns(const Square& v, const Image& im, int f0, int slab, int b, uint32_t& word) {
-  const int lane = threadIdx.x & 31, tl = lane >> 2, fl = lane & 3;
+// Where this lane's eight columns begin in slab `slab` of an image: columns f0 + 8 (lane
+// % 4), places 4 (lane / 4).  16-byte piece i of a column's places lies at i ^ (column %
+// 8), which is 0 for the first of the eight.
+__device__ __forceinline__ uintptr_t lane_place(const Image& im, int f0, int slab) {
+  const int lane = threadIdx.x & 31;
+  return reinterpret_cast<uintptr_t>(im.data) + (static_cast<size_t>(f0 >> 7) * im.slabs + slab) * kColumnSlab + (f0 & 127) * 128 +
+         (lane & 3) * 1024 + (lane >> 2) * 4;
+}
+
+// The warp's square as 32 columns x 32 places, the places 32 b .. of the slab that
+// `place` is lane_place() of.  The scale's byte goes into byte b of `word`, for the
+// column that this lane keeps.
+__device__ __forceinline__ void store_columns(const Square& v, uintptr_t place, int b, uint32_t& word) {
+  const int fl = threadIdx.x & 3;
   uint32_t m[8];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
@@ -134,10 +143,7 @@ __device__ __forceinline__ void store_columns(const Square& v, const Image& im, 
   word |= static_cast<uint32_t>(c) << (8 * b);
   const float mine = e8m0_down(finite ? c : 127);
   const bool whole = __all_sync(0xffffffffu, finite);
-  const int row = (f0 & 127) + fl * 8;
-  // 16-byte piece 2 b + tl / 4 of a column's places; column j has it at piece ^ j
-  const uintptr_t out = reinterpret_cast<uintptr_t>(im.data) + (static_cast<size_t>(f0 >> 7) * im.slabs + slab) * kColumnSlab +
-                        row * 128 + (2 * b + (tl >> 2)) * 16 + (tl & 3) * 4;
+  const uintptr_t out = place + b * 32;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     // the lane that kept column j: bits 16, 8, 4 of its index are those of j
@@ -199,7 +205,8 @@ struct ColumnsParams {
 // 113, whose 12 instructions a value take 71.
 template <int FMT>
 __global__ void __launch_bounds__(kThreads) columns_kernel(const ColumnsParams p) {
-  __shared__ int4 row_sh[kPlaces / 4];  // the places' rows, -1 for none
+  // the places' rows and their scales; none: null
+  __shared__ __align__(16) uintptr_t row_sh[kPlaces], scale_sh[kPlaces];
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tl = lane >> 2, fl = lane & 3;
@@ -208,33 +215,37 @@ __global__ void __launch_bounds__(kThreads) columns_kernel(const ColumnsParams p
   const SlabRows q = slab_rows(p.offsets, p.R, p.E, slab);
   const int squares = min(max((q.count + 31) / 32 - b0, 0), span);  // with a row, of this block's
   {
-    int row = -1;
+    uintptr_t x = 0, scales = 0;
     if (threadIdx.x < q.count) {
-      row = q.row0 + threadIdx.x;
+      int64_t row = q.row0 + threadIdx.x;
       if (p.rows) row = min(max(__ldg(p.rows + row), 0), p.T - 1);
+      x = reinterpret_cast<uintptr_t>(p.in.x) + row * p.in.ld * Eight<FMT>::BYTES;
+      scales = reinterpret_cast<uintptr_t>(p.in.scales) + row * (p.in.cols / scale_block(FMT)) * (FMT == kF32By128 ? 4 : 1);
     }
-    reinterpret_cast<int*>(row_sh)[threadIdx.x] = row;
+    row_sh[threadIdx.x] = x;
+    scale_sh[threadIdx.x] = scales;
   }
   __syncthreads();
   Eight<FMT> next[4];
   // the values of square n: places 32 (b0 + n % squares), column tile n / squares of the block's
   const int count = squares * ((tiles - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
-  int ask_b = 0, ask_tile = blockIdx.x;
+  int ask_b = 0, ask_col = blockIdx.x * kWide + warp * 32 + fl * 8;
   auto ask = [&] {
-    const int4 r = row_sh[8 * (b0 + ask_b) + tl];
-    const int rows[4] = {r.x, r.y, r.z, r.w};
+    const int at = 32 * (b0 + ask_b) + 4 * tl;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+      const uintptr_t row = row_sh[at + i];
       next[i].zero();
-      if (rows[i] >= 0) next[i].load(p.in, rows[i], ask_tile * kWide + warp * 32 + fl * 8);
+      if (row) next[i].load(row, scale_sh[at + i], ask_col);
     }
     if (++ask_b == squares) {
       ask_b = 0;
-      ask_tile += gridDim.x;
+      ask_col += gridDim.x * kWide;
     }
   };
   if (count > 0) ask();
   int n = 0;
+  uintptr_t place = lane_place(p.image, blockIdx.x * kWide + warp * 32, slab);
 #pragma unroll 1
   for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
     const int f0 = tile * kWide + warp * 32;
@@ -245,8 +256,9 @@ __global__ void __launch_bounds__(kThreads) columns_kernel(const ColumnsParams p
 #pragma unroll
       for (int i = 0; i < 4; ++i) next[i].widen(v.p[i]);
       if (++n < count) ask();
-      store_columns(v, p.image, f0, slab, b0 + b, word);
+      store_columns(v, place, b0 + b, word);
     }
+    place += static_cast<size_t>(gridDim.x) * p.image.slabs * kColumnSlab;
     for (int b = squares; b < span; ++b) store_no_columns(p.image, f0, slab, b0 + b, word);
     store_atoms(p.image, f0, slab, gridDim.z, b0, word);
   }
@@ -264,20 +276,19 @@ struct SwigluParams {
   uint8_t* codes;         // [R][2 K]
   void* scales;
   void* dx;               // [R][2 K] (null: not wanted)
-  float* dots;            // [R][column tiles] (weights given)
+  float* dots;            // [R][dot_parts]: sums over 32 columns each (weights given)
   Image dx_image, act_image;
-  int T, R, E, K, k;
+  int T, R, E, K, k, dot_parts;
 };
 
-constexpr int row_block(int fmt) { return fmt == kE8m0By32 ? 32 : 128; }
-
-// Codes and scales of the warp's square along its rows, at column `col0` of the
-// [R][2 K] output; row0: the square's first row, `rows` of them.  Scale blocks of
-// 128 take the maximum over the four warps, through `part` [4][32].
+// Codes and scales of the warp's square along its rows, `rows` of them.  out: where
+// this lane's eight codes of its first row go, `cols` bytes from row to row; block: the
+// first row's scale block.  Scale blocks of 128 take the maximum over the four warps,
+// through `part` [4][32].
 template <int FMT>
-__device__ __forceinline__ void store_rows(const Square& v, const SwigluParams& p, int row0, int rows, int64_t col0,
+__device__ __forceinline__ void store_rows(const Square& v, uint8_t* out, int64_t cols, void* scales, int64_t block, int rows,
                                            uint32_t (*part)[32]) {
-  const int lane = threadIdx.x & 31, tl = lane >> 2, fl = lane & 3;
+  const int lane = threadIdx.x & 31, tl = lane >> 2;
   uint32_t m[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -294,17 +305,16 @@ __device__ __forceinline__ void store_rows(const Square& v, const SwigluParams& 
     m[0] = max(max(part[0][mine], part[1][mine]), max(part[2][mine], part[3][mine]));
   }
   const bool finite = m[0] < 0x7f800000u;
-  const int64_t cols = 2 * static_cast<int64_t>(p.K);
-  const int64_t block = (row0 + mine) * (cols / row_block(FMT)) + col0 / row_block(FMT);
+  const int64_t at = block + mine * (cols / scale_block(FMT));
   const bool stores = mine < rows && (FMT == kE8m0By32 || threadIdx.x < 32);
   float scale;  // what values are multiplied by (E8M0) or divided by
   if (FMT == kF32By128) {
     scale = f32_scale_of(finite ? m[0] : 0u);
-    if (stores) static_cast<float*>(p.scales)[block] = finite ? scale : __uint_as_float(0x7fc00000u);
+    if (stores) static_cast<float*>(scales)[at] = finite ? scale : __uint_as_float(0x7fc00000u);
   } else {
     const int c = finite ? e8m0_of(m[0]) : 127;
     scale = e8m0_down(c);
-    if (stores) static_cast<uint8_t*>(p.scales)[block] = static_cast<uint8_t>(finite ? c : 255);
+    if (stores) static_cast<uint8_t*>(scales)[at] = static_cast<uint8_t>(finite ? c : 255);
   }
   const bool whole = __all_sync(0xffffffffu, finite);
 #pragma unroll
@@ -337,7 +347,7 @@ __device__ __forceinline__ void store_rows(const Square& v, const SwigluParams& 
       }
     }
     const uint2 o = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
-    if (4 * tl + i < rows) *reinterpret_cast<uint2*>(p.codes + (row0 + 4 * tl + i) * cols + col0 + fl * 8) = o;
+    if (4 * tl + i < rows) *reinterpret_cast<uint2*>(out + i * cols) = o;
   }
 }
 
@@ -371,20 +381,18 @@ __device__ __forceinline__ void fetch8(void* dst, const void* src, bool there) {
 template <int FMT, typename T>
 __global__ void __launch_bounds__(kThreads, 4) swiglu_backward_kernel(const SwigluParams p) {
   __shared__ uint32_t part[2][2][4][32];
-  __shared__ float dot_sh[2][4][32];
   __shared__ float weight_sh[kPlaces];
   extern __shared__ uint8_t landing_sh[];
   Landing<T>* landing = reinterpret_cast<Landing<T>*>(landing_sh);
   pdl_wait();
   pdl_launch_dependents();
+  constexpr int S = scale_block(FMT);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, tl = lane >> 2, fl = lane & 3;
   const int slab = blockIdx.y, tiles = (p.K + kWide - 1) / kWide;
   const int64_t cols = 2 * static_cast<int64_t>(p.K);
   const SlabRows q = slab_rows(p.offsets, p.R, p.E, slab);
-  const int span = 4 / gridDim.z, b0 = blockIdx.z * span;               // squares of this block, and the first
-  const int squares = min(max((q.count + 31) / 32 - b0, 0), span);     // ... that have a row
-  // square n of this block's: rows 32 (b0 + n % squares), column tile n / squares
-  const int count = squares * ((tiles - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
+  const int span = 4 / gridDim.z, b0 = blockIdx.z * span;             // squares of this block, and the first
+  const int squares = min(max((q.count + 31) / 32 - b0, 0), span);   // ... that have a row
   if (squares > 0) {
     // the slab's routing weights: a row's is that of the choice whose slot it is
     float w = 1.f;
@@ -402,47 +410,43 @@ __global__ void __launch_bounds__(kThreads, 4) swiglu_backward_kernel(const Swig
     weight_sh[tid] = w;
   }
   __syncthreads();
-  // the checkpoint's scales of row `lane` of the next square, as they lie in memory
+  // The next square: rows 32 next_b of the slab, column tile next_tile.  The
+  // checkpoint's scales of its row `lane` as they lie in memory, and its bytes.
+  int next_b = b0, next_tile = blockIdx.x;
   uint32_t gs_next = 0, us_next = 0;
-  auto ask = [&](int n) {
-    const int b = b0 + n % squares, f0 = (blockIdx.x + n / squares * gridDim.x) * kWide + warp * 32;
-    const int row0 = q.row0 + 32 * b, rows = min(q.count - 32 * b, 32);
-    Landing<T>& to = landing[n & 1];
-    const bool inside = f0 < p.K;  // (32-blocks: the last warps may have no columns)
+  auto ask = [&](int stage) {
+    const int f0 = next_tile * kWide + warp * 32;
+    // (32-blocks: the last warps may have no columns)
+    const int mine = f0 < p.K ? q.count - 32 * next_b - 4 * tl : 0;  // rows from this lane's first
+    const int64_t row = q.row0 + 32 * next_b + 4 * tl;
+    const int c = f0 + fl * 8;
+    const T* dy = static_cast<const T*>(p.dy.x) + row * p.dy.ld + c;
+    const uint8_t* saved = static_cast<const uint8_t*>(p.saved.x) + row * cols + c;
+    Landing<T>& to = landing[stage];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const bool there = inside && 4 * tl + i < rows;
-      const int64_t row = there ? row0 + 4 * tl + i : q.row0;
-      const int c = inside ? f0 + fl * 8 : 0;
-      const T* dy = static_cast<const T*>(p.dy.x) + row * p.dy.ld + c;
-      const uint8_t* saved = static_cast<const uint8_t*>(p.saved.x) + row * cols + c;
 #pragma unroll
-      for (int h = 0; h < static_cast<int>(sizeof(T) / 2); ++h) fetch16(&to.dy[i][h][tid], dy + 8 * h / static_cast<int>(sizeof(T) / 2), there);
-      fetch8(&to.g[i][tid], saved, there);
-      fetch8(&to.u[i][tid], saved + p.K, there);
+      for (int h = 0; h < static_cast<int>(sizeof(T) / 2); ++h)
+        fetch16(&to.dy[i][h][tid], dy + i * p.dy.ld + 8 * h / static_cast<int>(sizeof(T) / 2), i < mine);
+      fetch8(&to.g[i][tid], saved + i * cols, i < mine);
+      fetch8(&to.u[i][tid], saved + i * cols + p.K, i < mine);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  auto ask_scales = [&](int n) {
-    const int b = b0 + n % squares, f0 = (blockIdx.x + n / squares * gridDim.x) * kWide + warp * 32;
-    const int row0 = q.row0 + 32 * b, rows = min(q.count - 32 * b, 32);
+  auto ask_scales = [&] {
+    const int f0 = next_tile * kWide + warp * 32;
     gs_next = us_next = 0;  // (rows that are not there have codes 0)
-    if (f0 < p.K && lane < rows) {
-      constexpr int S = row_block(FMT);
-      const int64_t g_at = (row0 + lane) * (cols / S) + f0 / S, u_at = g_at + p.K / S;
+    if (f0 < p.K && 32 * next_b + lane < q.count) {
+      const int64_t at = (q.row0 + 32 * next_b + lane) * (cols / S) + f0 / S;
       if (FMT == kF32By128) {
-        gs_next = __ldg(static_cast<const uint32_t*>(p.saved.scales) + g_at);
-        us_next = __ldg(static_cast<const uint32_t*>(p.saved.scales) + u_at);
+        gs_next = __ldg(static_cast<const uint32_t*>(p.saved.scales) + at);
+        us_next = __ldg(static_cast<const uint32_t*>(p.saved.scales) + at + p.K / S);
       } else {
-        gs_next = __ldg(static_cast<const uint8_t*>(p.saved.scales) + g_at);
-        us_next = __ldg(static_cast<const uint8_t*>(p.saved.scales) + u_at);
+        gs_next = __ldg(static_cast<const uint8_t*>(p.saved.scales) + at);
+        us_next = __ldg(static_cast<const uint8_t*>(p.saved.scales) + at + p.K / S);
       }
     }
   };
-  if (count > 0) {
-    ask(0);
-    ask_scales(0);
-  }
   // zeros in the block's squares from r on, and all their scales
   auto close = [&](int f0, int r, uint32_t g, uint32_t u, uint32_t a) {
     for (; r < b0 + span; ++r) {
@@ -454,104 +458,112 @@ __global__ void __launch_bounds__(kThreads, 4) swiglu_backward_kernel(const Swig
     store_atoms(p.dx_image, p.K + f0, slab, gridDim.z, b0, u);
     store_atoms(p.act_image, f0, slab, gridDim.z, b0, a);
   };
-  uint32_t word_g = 0, word_u = 0, word_a = 0;
+  if (squares > 0) {
+    ask(0);
+    ask_scales();
+  }
+  int stage = 0;
 #pragma unroll 1
-  for (int n = 0; n < count; ++n) {
-    const int b = b0 + n % squares, tile = blockIdx.x + n / squares * gridDim.x, f0 = tile * kWide + warp * 32;
-    const int row0 = q.row0 + 32 * b, rows = min(q.count - 32 * b, 32);
+  for (int tile = blockIdx.x; squares > 0 && tile < tiles; tile += gridDim.x) {
+    const int f0 = tile * kWide + warp * 32;
     const bool inside = f0 < p.K;
-    auto scale = [](uint32_t x) { return FMT == kF32By128 ? __uint_as_float(x) : e8m0_up(x); };
-    const uint32_t gs_row = gs_next, us_row = us_next;
-    if (n + 1 < count) {
-      ask(n + 1);
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
-    } else {
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
-    }
-    const Landing<T>& from = landing[n & 1];
-    Square act, dg, du;
-    float dot[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float w = weight_sh[32 * b + 4 * tl + i];
-      const float gs = scale(__shfl_sync(0xffffffffu, gs_row, 4 * tl + i)), us = scale(__shfl_sync(0xffffffffu, us_row, 4 * tl + i));
-      Pair g[4], u[4], dy[4];
-      decode(from.g[i][tid], gs, g);
-      decode(from.u[i][tid], us, u);
-      Eight<sizeof(T) == 2 ? kBf16Rows : kF32Rows> raw;
-#pragma unroll
-      for (int h = 0; h < static_cast<int>(sizeof(T) / 2); ++h) raw.raw.q[h] = from.dy[i][h][tid];
-      raw.widen(dy);
-      Pair sum = pair_of(0.f, 0.f);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        constexpr float kLog2e = 1.44269504088896341f;
-        float2 e = halves(mul(g[c], pair_of(-kLog2e, -kLog2e)));
-        e = make_float2(fminf(e.x, 127.9f), fminf(e.y, 127.9f));  // (a NaN is in g too)
-        asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.x));
-        asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.y));
-        const Pair ee = pair_of(e.x, e.y), one = pair_of(1.f, 1.f);
-        float2 h = halves(add(ee, one));
-        asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(h.x));
-        asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(h.y));
-        const Pair sg = pair_of(h.x, h.y), gs_ = mul(g[c], sg), up = fma(gs_, ee, one);  // up: 1 + g (1 - s)
-        const Pair a = mul(gs_, u[c]), d = mul(dy[c], pair_of(w, w));
-        sum = fma(dy[c], a, sum);
-        act.p[i][c] = mul(a, pair_of(w, w));
-        dg.p[i][c] = mul(mul(d, u[c]), mul(sg, up));
-        du.p[i][c] = mul(d, gs_);
+    uint32_t word_g = 0, word_u = 0, word_a = 0;
+#pragma unroll 1
+    for (int b = b0; b < b0 + squares; ++b, stage ^= 1) {
+      const uint32_t gs_row = gs_next, us_row = us_next;
+      if (++next_b == b0 + squares) {
+        next_b = b0;
+        next_tile += gridDim.x;
       }
-      const float2 s = halves(sum);
-      dot[i] = s.x + s.y;
-    }
-    if (p.dots) {
+      const bool more = next_tile < tiles;
+      if (more) {
+        ask(stage ^ 1);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+      } else {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+      }
+      const Landing<T>& from = landing[stage];
+      auto scale = [](uint32_t x) { return FMT == kF32By128 ? __uint_as_float(x) : e8m0_up(x); };
+      const int64_t row0 = q.row0 + 32 * b;
+      const int rows = q.count - 32 * b;
+      Square act, dg, du;
+      float dot[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        dot[i] += __shfl_xor_sync(0xffffffffu, dot[i], 1);
-        dot[i] += __shfl_xor_sync(0xffffffffu, dot[i], 2);
-        if (fl == i) dot_sh[n & 1][warp][4 * tl + i] = dot[i];
+        const float w = weight_sh[32 * b + 4 * tl + i];
+        const float gs = scale(__shfl_sync(0xffffffffu, gs_row, 4 * tl + i)), us = scale(__shfl_sync(0xffffffffu, us_row, 4 * tl + i));
+        Pair g[4], u[4], dy[4];
+        decode(from.g[i][tid], gs, g);
+        decode(from.u[i][tid], us, u);
+        Eight<sizeof(T) == 2 ? kBf16Rows : kF32Rows> raw;
+#pragma unroll
+        for (int h = 0; h < static_cast<int>(sizeof(T) / 2); ++h) raw.raw.q[h] = from.dy[i][h][tid];
+        raw.widen(dy);
+        Pair sum = pair_of(0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          constexpr float kLog2e = 1.44269504088896341f;
+          float2 e = halves(mul(g[c], pair_of(-kLog2e, -kLog2e)));
+          e = make_float2(fminf(e.x, 127.9f), fminf(e.y, 127.9f));  // (a NaN is in g too)
+          asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.x));
+          asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.y));
+          const Pair ee = pair_of(e.x, e.y), one = pair_of(1.f, 1.f);
+          float2 h = halves(add(ee, one));
+          asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(h.x));
+          asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(h.y));
+          const Pair sg = pair_of(h.x, h.y), gs_ = mul(g[c], sg), up = fma(gs_, ee, one);  // up: 1 + g (1 - s)
+          const Pair a = mul(gs_, u[c]), d = mul(dy[c], pair_of(w, w));
+          sum = fma(dy[c], a, sum);
+          act.p[i][c] = mul(a, pair_of(w, w));
+          dg.p[i][c] = mul(mul(d, u[c]), mul(sg, up));
+          du.p[i][c] = mul(d, gs_);
+        }
+        const float2 s = halves(sum);
+        dot[i] = s.x + s.y;
       }
-      __syncthreads();
-      if (tid < rows)
-        p.dots[static_cast<size_t>(row0 + tid) * tiles + tile] =
-            (dot_sh[n & 1][0][lane] + dot_sh[n & 1][1][lane]) + (dot_sh[n & 1][2][lane] + dot_sh[n & 1][3][lane]);
-    }
-    if (inside && p.dx_image.data) store_columns(act, p.act_image, f0, slab, b, word_a);
-    // Only now, with the activation's values gone: scales asked for together with the
-    // rows would live in registers that there are none of, and spilling them waits
-    // for the load.
-    if (n + 1 < count) ask_scales(n + 1);
-    if (inside) {
+      if (p.dots) {
+        // by halves, as the maxima: each lane keeps one row's sum over its eight columns x four
+        const bool odd = (lane & 1) != 0, upper = (lane & 2) != 0;
+        const float x = (odd ? dot[2] : dot[0]) + __shfl_xor_sync(0xffffffffu, odd ? dot[0] : dot[2], 1);
+        const float y = (odd ? dot[3] : dot[1]) + __shfl_xor_sync(0xffffffffu, odd ? dot[1] : dot[3], 1);
+        const float z = (upper ? y : x) + __shfl_xor_sync(0xffffffffu, upper ? x : y, 2);
+        const int mine = 4 * tl + 2 * (lane & 1) + ((lane >> 1) & 1);
+        if (inside && mine < rows) p.dots[(row0 + mine) * p.dot_parts + tile * 4 + warp] = z;
+      }
+      if (inside && p.dx_image.data) store_columns(act, lane_place(p.act_image, f0, slab), b, word_a);
+      // Only now, with the activation's values gone: scales asked for together with the
+      // rows would live in registers that there are none of, and spilling them waits
+      // for the load.
+      if (more) ask_scales();
+      if (!inside) continue;
       if (p.dx_image.data) {
-        store_columns(dg, p.dx_image, f0, slab, b, word_g);
-        store_columns(du, p.dx_image, p.K + f0, slab, b, word_u);
+        store_columns(dg, lane_place(p.dx_image, f0, slab), b, word_g);
+        store_columns(du, lane_place(p.dx_image, p.K + f0, slab), b, word_u);
+        if (b + 1 == b0 + squares) close(f0, b + 1, word_g, word_u, word_a);
       }
-      store_rows<FMT>(dg, p, row0, rows, f0, part[n & 1][0]);
-      store_rows<FMT>(du, p, row0, rows, p.K + f0, part[n & 1][1]);
+      const int64_t out = (row0 + 4 * tl) * cols + f0 + fl * 8, block = row0 * (cols / S) + f0 / S;
+      store_rows<FMT>(dg, p.codes + out, cols, p.scales, block, rows, part[stage][0]);
+      store_rows<FMT>(du, p.codes + out + p.K, cols, p.scales, block + p.K / S, rows, part[stage][1]);
       if (p.dx) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if (4 * tl + i < rows) {
-            T* out = static_cast<T*>(p.dx) + (row0 + 4 * tl + i) * cols + f0 + fl * 8;
+            T* to = static_cast<T*>(p.dx) + out + i * cols;
             float x[8], y[8];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               *reinterpret_cast<float2*>(&x[2 * c]) = halves(dg.p[i][c]);
               *reinterpret_cast<float2*>(&y[2 * c]) = halves(du.p[i][c]);
             }
-            store8(out, x);
-            store8(out + p.K, y);
+            store8(to, x);
+            store8(to + p.K, y);
           }
         }
       }
     }
-    if (p.dx_image.data && b == b0 + squares - 1) {
-      close(f0, b + 1, word_g, word_u, word_a);
-      word_g = word_u = word_a = 0;
-    }
   }
   // Rows that no expert has: zeros.  The slabs are more than the rows / 128, so
-  // that each takes its 128 of them.  And a slab without rows is zeros.
+  // that each takes its 128 of them.  And squares without rows are zeros.
   const int none = q.first + (p.R - q.last);
   for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
     if (squares == 0 && p.dx_image.data) close(tile * kWide + warp * 32, b0, 0, 0, 0);
@@ -559,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 4) swiglu_backward_kernel(const Swig
     for (int i = slab * kPlaces + warp; i < min(none, (slab + 1) * kPlaces); i += 4) {
       const int64_t row = i < q.first ? i : q.last + (i - q.first);
       const int c = tile * kWide + lane * 4;
-      if (p.dots && lane == 0) p.dots[row * tiles + tile] = 0.f;
+      if (p.dots && lane < 4 && tile * 4 + lane < p.dot_parts) p.dots[row * p.dot_parts + tile * 4 + lane] = 0.f;
       if (c >= p.K) continue;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -569,30 +581,33 @@ __global__ void __launch_bounds__(kThreads, 4) swiglu_backward_kernel(const Swig
 #pragma unroll
           for (int j = 0; j < 4; ++j) static_cast<T*>(p.dx)[at + j] = T(0.f);
         }
-        if (c % row_block(FMT) == 0) {
+        if (c % S == 0) {
           if (FMT == kF32By128) static_cast<float*>(p.scales)[at / 128] = 1.f;
-          else static_cast<uint8_t*>(p.scales)[at / row_block(FMT)] = 127;
+          else static_cast<uint8_t*>(p.scales)[at / S] = 127;
         }
       }
     }
   }
 }
 
-// dweights[t][j] = the sum of the partial dots of its slot's row, in the order of
-// the columns; 0 where there is no choice.
+// dweights[t][j] = the sum of the partial dots of its slot's row, always in the same
+// order; 0 where there is no choice.  Eight threads a choice, so that they read whole
+// sectors.
 __global__ void __launch_bounds__(256) dweights_kernel(const float* __restrict__ dots, const int32_t* __restrict__ slots,
                                                        int64_t choices, int R, int parts, float* __restrict__ dweights) {
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (i >= choices) return;
-  const int slot = __ldg(slots + i);
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * (blockDim.x / 8) + threadIdx.x / 8;
+  const int slot = i < choices ? __ldg(slots + i) : -1;
   float sum = 0.f;
   if (slot >= 0 && slot < R) {
     const float* d = dots + static_cast<size_t>(slot) * parts;
-    for (int x = 0; x < parts; ++x) sum += __ldcg(d + x);
+#pragma unroll 8
+    for (int x = threadIdx.x & 7; x < parts; x += 8) sum += __ldcg(d + x);
   }
-  dweights[i] = sum;
+#pragma unroll
+  for (int d = 4; d > 0; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  if (i < choices && (threadIdx.x & 7) == 0) dweights[i] = sum;
 }
 
 // ------------------------------------------------------------------ weights
@@ -853,7 +868,7 @@ fg_status fg_swiglu_backward_workspace_size(int64_t R, int64_t K, int weighted, 
   if (!bytes) return fail(FG_ERR_INVALID_ARG, "null output");
   if (R < 0 || R > (int64_t(1) << 24) || K <= 0 || K > (int64_t(1) << 20))
     return fail(FG_ERR_SHAPE, "fg_swiglu_backward: R=%lld, K=%lld", (long long)R, (long long)K);
-  *bytes = weighted ? static_cast<uint64_t>(R) * tiles_of(K) * 4 : 0;
+  *bytes = weighted ? static_cast<uint64_t>(R) * (K / 32) * 4 : 0;
   return FG_OK;
 }
 
@@ -872,8 +887,8 @@ fg_status fg_swiglu_backward(int mode, const void* dy, int type, int64_t R, int6
   uint64_t need = 0;
   fg_status s = fg_swiglu_backward_workspace_size(R, K, weighted, &need);
   if (s != FG_OK) return s;
-  if (K % row_block(fmt))
-    return fail(FG_ERR_SHAPE, "%s: K=%lld must be a multiple of %d for %s", what, (long long)K, row_block(fmt), mode_name(mode));
+  if (K % scale_block(fmt))
+    return fail(FG_ERR_SHAPE, "%s: K=%lld must be a multiple of %d for %s", what, (long long)K, scale_block(fmt), mode_name(mode));
   if (columns) {
     if ((s = check_columns(what, K, R, E)) != FG_OK) return s;
     if ((s = check_image(what, dx_data, dx_sf, dx_desc)) != FG_OK) return s;
@@ -907,7 +922,7 @@ fg_status fg_swiglu_backward(int mode, const void* dy, int type, int64_t R, int6
                  static_cast<uint8_t*>(codes), scales, dx, weighted ? static_cast<float*>(workspace) : nullptr,
                  columns ? Image{static_cast<uint8_t*>(dx_data), static_cast<uint8_t*>(dx_sf), static_cast<int>(slabs)} : none,
                  columns ? Image{static_cast<uint8_t*>(act_data), static_cast<uint8_t*>(act_sf), static_cast<int>(slabs)} : none,
-                 static_cast<int>(T), static_cast<int>(R), E, static_cast<int>(K), top_k};
+                 static_cast<int>(T), static_cast<int>(R), E, static_cast<int>(K), top_k, static_cast<int>(K / 32)};
   // column tiles are shared out over blocks until there are sixteen for an SM
   const int64_t tiles = tiles_of(K), shares = (16 * sm_count() + slabs - 1) / slabs;
   // (and slabs cut in four where there would be fewer blocks than the GPU holds)
@@ -926,8 +941,8 @@ fg_status fg_swiglu_backward(int mode, const void* dy, int type, int64_t R, int6
   if (e != cudaSuccess) return cuda_fail(e, "gated activation's backward launch");
   if (weighted && T > 0) {
     const int64_t choices = T * top_k;
-    e = launch(dweights_kernel, dim3(static_cast<unsigned>((choices + 255) / 256)), 256, st, static_cast<const float*>(p.dots), slots,
-               choices, p.R, static_cast<int>(tiles), dweights);
+    e = launch(dweights_kernel, dim3(static_cast<unsigned>((choices + 31) / 32)), 256, st, static_cast<const float*>(p.dots), slots,
+               choices, p.R, p.dot_parts, dweights);
     if (e != cudaSuccess) return cuda_fail(e, "routing weights' gradient launch");
   }
   if (columns) {

@@ -111,8 +111,8 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
 // E8M0 code of a block of e4m3 values whose largest magnitude has these bits:
 // 127 + ceil(log2(amax / 448)), at least 0, 127 for zero (not for infinities and NaN).
 __device__ __forceinline__ int e8m0_of(uint32_t amax) {
-  const int c = static_cast<int>(amax >> 23) - 8 + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0);
-  return amax == 0 ? 127 : (c < 0 ? 0 : c);
+  const int c = max(static_cast<int>((amax + 0x1fffffu) >> 23) - 8, 0);  // one more where the fraction is above 1.75's
+  return amax == 0 ? 127 : c;
 }
 
 // 2^(127 - c), what values are multiplied by, and 2^(c - 127), what codes stand for
