@@ -21,7 +21,8 @@
 // 826 us to 805.  On pairs of SMs (256 x 256, 32 KB an SM and step) the fold holds
 // it as it does here: 817 and 1006 us, and 423 for 346 at 128 rows an expert.  There
 // a step without the fold's arithmetic would take 671 of 832 us, without its reads
-// 652, without both 586.
+// 652, without both 586.  Sixteen warps of 64 columns each, with the factors from two
+// warps of their own, took 840 for 805: it is the work that adds up, not its latency.
 //
 // Gathered rows are laid out one after the other by a kernel before this one (55 us
 // for 32768 rows of 7168).  Copied by the idle warps here they held the product up:
