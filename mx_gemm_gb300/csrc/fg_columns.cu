@@ -376,8 +376,11 @@ __device__ __forceinline__ void fetch8(void* dst, const void* src, bool there) {
 // A block of threads takes one slab's 128 rows x 128 columns at a time, 32 rows in
 // turn, and asks for the next 32 rows' bytes before it works on these: with four
 // blocks an SM, whose registers they fill, nothing else covers the loads.  32760 x
-// 2048 with columns in 232 us; 371 without that, and with the values not kept as
-// pairs.
+// 2048 with columns in 194 us, where its bytes take 91: bound by instructions, some 60
+// for each value of the activation, whose three results are each rounded twice, along
+// rows and along columns.  371 with loads that are waited for and values one by one
+// instead of in pairs, 208 with addresses worked out for each.  Blocks of threads that
+// stay and take several slabs spill: 321.
 template <int FMT, typename T>
 __global__ void __launch_bounds__(kThreads, 4) swiglu_backward_kernel(const SwigluParams p) {
   __shared__ uint32_t part[2][2][4][32];
@@ -515,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 4) swiglu_backward_kernel(const Swig
           const Pair a = mul(gs_, u[c]), d = mul(dy[c], pair_of(w, w));
           sum = fma(dy[c], a, sum);
           act.p[i][c] = mul(a, pair_of(w, w));
-          dg.p[i][c] = mul(mul(d, u[c]), mul(sg, up));
+          dg.p[i][c] = mul(d, mul(u[c], mul(sg, up)));  // (no product larger than its result but by rounding)
           du.p[i][c] = mul(d, gs_);
         }
         const float2 s = halves(sum);
