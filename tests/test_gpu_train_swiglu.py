@@ -134,6 +134,20 @@ def test_gates_from_one_end_to_the_other():
     assert torch.isfinite(d.dx).all()
 
 
+def test_products_that_pass_32_bits_before_they_are_small():
+    """dy * u is above every 32-bit number, its product with the activation's slope is not."""
+    x = torch.empty(64, 256, device="cuda")
+    x[:, :128] = torch.tensor([-28.0, -60.0, -80.0, -104.0], device="cuda").repeat(16)[:, None]
+    x[:, 128:] = 2.0 ** 30
+    saved, scales = fg.quantize("mxfp8_b32", x)
+    dy = torch.full((64, 128), 2.0 ** 100, device="cuda")
+    d = fg.swiglu_backward("mxfp8_b32", dy, saved, scales, plain=True)
+    v = ref.decoded(saved, scales)
+    want, mag, _, _ = formula(dy.double(), v[:, :128], v[:, 128:], 1.0)
+    assert (dy.double() * v[:, 128:]).min() > 3.5e38
+    ref.within(d.dx, want, ref.REL * mag + 2.0 ** -24 * want.abs() + SMALL)
+
+
 def test_values_that_are_not_numbers_stay_within_their_blocks():
     x = rand(9, 64, 512)
     x[3, 5], x[40, 256 + 130] = NAN, INF
