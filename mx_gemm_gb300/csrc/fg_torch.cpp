@@ -171,6 +171,31 @@ at::Tensor make(at::IntArrayRef sizes, at::ScalarType type, const at::Device& de
   return at::detail::empty_cuda(sizes, type, device, std::nullopt);
 }
 
+// Two tensors in one allocation, which costs the host about as much as a launch: what
+// always goes together, values and their scales.  The second begins at a multiple of
+// 128 bytes.
+struct Both {
+  at::Tensor first, second;
+};
+
+at::Tensor part(const at::Tensor& whole, int64_t byte, at::IntArrayRef sizes, at::ScalarType type) {
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(), c10::scalarTypeToTypeMeta(type));
+  t.unsafeGetTensorImpl()->set_storage_offset(byte / static_cast<int64_t>(c10::elementSize(type)));
+  t.unsafeGetTensorImpl()->set_sizes_contiguous(sizes);
+  return t;
+}
+
+Both make_both(at::IntArrayRef sizes, at::ScalarType type, at::IntArrayRef sizes2, at::ScalarType type2, const at::Device& device) {
+  auto bytes = [](at::IntArrayRef v, at::ScalarType t) {
+    int64_t n = static_cast<int64_t>(c10::elementSize(t));
+    for (const int64_t d : v) n *= d;
+    return n;
+  };
+  const int64_t at2 = (bytes(sizes, type) + 127) / 128 * 128;
+  const at::Tensor whole = make({at2 + bytes(sizes2, type2)}, at::kByte, device);
+  return {part(whole, 0, sizes, type), part(whole, at2, sizes2, type2)};
+}
+
 PyObject* wrap(const at::Tensor& t) {
   if (t.defined()) return THPVariable_Wrap(t);
   Py_RETURN_NONE;
@@ -225,11 +250,10 @@ struct Codes {
 };
 
 Codes make_codes(int mode, int64_t m, int64_t k, const at::Device& device) {
-  Codes c;
-  c.codes = mode == FG_MXFP4 ? make({m, k / 2}, at::kByte, device) : make({m, k}, at::kFloat8_e4m3fn, device);
-  c.scales = mode == FG_FP8_BLOCK128 ? make({m, k / 128}, at::kFloat, device)
-                                     : make({m, k / (mode == FG_MXFP8 ? 128 : 32)}, at::kFloat8_e8m0fnu, device);
-  return c;
+  const bool half = mode == FG_MXFP4, wide = mode == FG_FP8_BLOCK128;
+  Both b = make_both({m, half ? k / 2 : k}, half ? at::kByte : at::kFloat8_e4m3fn, {m, k / (wide || mode == FG_MXFP8 ? 128 : 32)},
+                     wide ? at::kFloat : at::kFloat8_e8m0fnu, device);
+  return {std::move(b.first), std::move(b.second)};
 }
 
 void* data(const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
@@ -592,8 +616,9 @@ void make_columns(ColumnOperand& c, int64_t columns, int64_t rows, int experts, 
   int64_t places = 0;
   uint64_t data_bytes = 0, sf_bytes = 0;
   check(fg_columns_size(columns, rows, experts, &places, &data_bytes, &sf_bytes));
-  c.data = make({static_cast<int64_t>(data_bytes)}, at::kByte, device);
-  c.sf = make({static_cast<int64_t>(sf_bytes)}, at::kByte, device);
+  Both b = make_both({static_cast<int64_t>(data_bytes)}, at::kByte, {static_cast<int64_t>(sf_bytes)}, at::kByte, device);
+  c.data = std::move(b.first);
+  c.sf = std::move(b.second);
 }
 
 PyObject* wrap(const ColumnOperand& c) {
@@ -621,8 +646,9 @@ PyObject* quantize_weight(PyObject*, PyObject* const* a, Py_ssize_t n) {
       Unlocked u;
       Pool pool(launch);
       const int64_t rows = transpose ? K : N, cols = transpose ? N : K;
-      codes = make({E * rows, cols}, at::kFloat8_e4m3fn, device);
-      scales = make({E * rows / 128, cols / 128}, at::kFloat, device);
+      Both b = make_both({E * rows, cols}, at::kFloat8_e4m3fn, {E * rows / 128, cols / 128}, at::kFloat, device);
+      codes = std::move(b.first);
+      scales = std::move(b.second);
       check(fg_quantize_weight(mode, w.data_ptr(), type, (int)E, N, K, ld, stride, transpose, codes.data_ptr(), scales.data_ptr(),
                                launch.stream));
       keep(launch, {&codes, &scales}, {&w});
