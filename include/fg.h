@@ -312,8 +312,8 @@ FG_API fg_status fg_gemm_noalloc(const void* A, const void* a_scales, int64_t M,
  * (1 for an all-zero block; rounded to nearest, for amax < 2^-132 upwards, so
  * never 0), code = RNE(v / scale).  A block with a NaN or an infinity gets the
  * NaN scale (255; fp32 NaN) and zero codes.
- * A weight's [N][K] rows quantise the same way (not FP8_BLOCK128, whose
- * weights have 128 x 128 blocks).
+ * A weight's [N][K] rows quantise the same way (FP8_BLOCK128's weights have
+ * 128 x 128 blocks: fg_quantize_weight).
  * Errors: INVALID_ARG, SHAPE (K not a multiple of the block), ALIGN (x and its
  * rows 16 bytes, codes 16, fp32 scales 4), UNSUPPORTED_ARCH, CUDA.
  */
