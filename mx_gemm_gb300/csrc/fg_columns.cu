@@ -376,11 +376,11 @@ __device__ __forceinline__ void fetch8(void* dst, const void* src, bool there) {
 // A block of threads takes one slab's 128 rows x 128 columns at a time, 32 rows in
 // turn, and asks for the next 32 rows' bytes before it works on these: with four
 // blocks an SM, whose registers they fill, nothing else covers the loads.  32760 x
-// 2048 with columns in 194 us, where its bytes take 91: bound by instructions, some 60
+// 2048 with columns in 192 us, where its bytes take 91: bound by instructions, some 60
 // for each value of the activation, whose three results are each rounded twice, along
 // rows and along columns.  371 with loads that are waited for and values one by one
 // instead of in pairs, 208 with addresses worked out for each.  Blocks of threads that
-// stay and take several slabs spill: 321.
+// stay and take several slabs spill: 321; so do two results' exchanges side by side: 236.
 template <int FMT, typename T>
 __global__ void __launch_bounds__(kThreads, 4) swiglu_backward_kernel(const SwigluParams p) {
   __shared__ uint32_t part[2][2][4][32];
@@ -396,23 +396,6 @@ __global__ void __launch_bounds__(kThreads, 4) swiglu_backward_kernel(const Swig
   const SlabRows q = slab_rows(p.offsets, p.R, p.E, slab);
   const int span = 4 / gridDim.z, b0 = blockIdx.z * span;             // squares of this block, and the first
   const int squares = min(max((q.count + 31) / 32 - b0, 0), span);   // ... that have a row
-  if (squares > 0) {
-    // the slab's routing weights: a row's is that of the choice whose slot it is
-    float w = 1.f;
-    if (p.weights) {
-      w = 0.f;
-      if (tid < q.count) {
-        const int64_t t = min(max(__ldg(p.rows + q.row0 + tid), 0), p.T - 1);
-        for (int j0 = 0; j0 < p.k; j0 += 8) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (j0 + j < p.k && __ldg(p.slots + t * p.k + j0 + j) == q.row0 + tid) w = __ldg(p.weights + t * p.k + j0 + j);
-        }
-      }
-    }
-    weight_sh[tid] = w;
-  }
-  __syncthreads();
   // The next square: rows 32 next_b of the slab, column tile next_tile.  The
   // checkpoint's scales of its row `lane` as they lie in memory, and its bytes.
   int next_b = b0, next_tile = blockIdx.x;
@@ -464,7 +447,22 @@ __global__ void __launch_bounds__(kThreads, 4) swiglu_backward_kernel(const Swig
   if (squares > 0) {
     ask(0);
     ask_scales();
+    // meanwhile the slab's routing weights: a row's is that of the choice whose slot it is
+    float w = 1.f;
+    if (p.weights) {
+      w = 0.f;
+      if (tid < q.count) {
+        const int64_t t = min(max(__ldg(p.rows + q.row0 + tid), 0), p.T - 1);
+        for (int j0 = 0; j0 < p.k; j0 += 8) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j0 + j < p.k && __ldg(p.slots + t * p.k + j0 + j) == q.row0 + tid) w = __ldg(p.weights + t * p.k + j0 + j);
+        }
+      }
+    }
+    weight_sh[tid] = w;
   }
+  __syncthreads();
   int stage = 0;
 #pragma unroll 1
   for (int tile = blockIdx.x; squares > 0 && tile < tiles; tile += gridDim.x) {
@@ -926,7 +924,8 @@ fg_status fg_swiglu_backward(int mode, const void* dy, int type, int64_t R, int6
                  columns ? Image{static_cast<uint8_t*>(dx_data), static_cast<uint8_t*>(dx_sf), static_cast<int>(slabs)} : none,
                  columns ? Image{static_cast<uint8_t*>(act_data), static_cast<uint8_t*>(act_sf), static_cast<int>(slabs)} : none,
                  static_cast<int>(T), static_cast<int>(R), E, static_cast<int>(K), top_k, static_cast<int>(K / 32)};
-  // column tiles are shared out over blocks until there are sixteen for an SM
+  // column tiles are shared out over blocks until there are sixteen for an SM (12: 201
+  // us, 24: 201, 32: 197 for the rows above)
   const int64_t tiles = tiles_of(K), shares = (16 * sm_count() + slabs - 1) / slabs;
   // (and slabs cut in four where there would be fewer blocks than the GPU holds)
   const bool few = tiles * slabs < 4 * static_cast<int64_t>(sm_count());
