@@ -58,13 +58,24 @@ constexpr int block_of(int mode) { return (mode == kMXFP8 || mode == kBlock) ? 1
 // Quantise this thread's eight values of a block spread over block_of(MODE) / 8
 // consecutive lanes and store codes and scale.  chunk: index of the eight
 // values in the contiguous [M][K] output.  Every lane of the warp calls it;
-// `live` lanes store.
-template <int MODE>
+// `live` lanes store.  BITS: the largest magnitude by whole numbers, two instructions a
+// value, instead of half of one; it is the faster where the values come out of the
+// fast power and reciprocal (the gated activation of 32761 x 2048 bf16: 48.8 us against
+// 50.9) and the slower where they come from memory (32761 x 4096: 63.2 against 60.4), or
+// with fp32 scales (the activation: 62.9 against 61.4).
+template <int MODE, bool BITS = false>
 __device__ __forceinline__ void quantize8(float (&v)[kVec], bool live, size_t chunk, void* codes, void* scales) {
   constexpr int LANES = block_of(MODE) / kVec;
   uint32_t amax = 0;  // of |v|'s bits: their order is that of the values, NaN above infinity
+  if (BITS) {
 #pragma unroll
-  for (int i = 0; i < kVec; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7fffffffu);
+    for (int i = 0; i < kVec; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7fffffffu);
+  } else {
+    float most = 0.f;
+#pragma unroll
+    for (int i = 0; i < kVec; i += 2) most = largest(most, v[i], v[i + 1]);
+    amax = __float_as_uint(most);
+  }
 #pragma unroll
   for (int d = 1; d < LANES; d *= 2) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, d));
   const bool finite = amax < 0x7f800000u;
@@ -74,13 +85,23 @@ __device__ __forceinline__ void quantize8(float (&v)[kVec], bool live, size_t ch
     // before them it costs four registers, and the norm of 32761 x 4096 an eighth
     // of its warps (170 us; 145 so).
     const float s = f32_scale_of(finite ? amax : 0u);
+    const Over over(s);
+    if (over.sure && finite) {
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) v[i] = __fdiv_rn(finite ? v[i] : 0.f, s);
+      for (int i = 0; i < kVec; i += 2) {
+        const float2 q = halves(over(pair_of(v[i], v[i + 1])));
+        v[i] = q.x;
+        v[i + 1] = q.y;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) v[i] = __fdiv_rn(finite ? v[i] : 0.f, s);
+    }
     if (live && first) static_cast<float*>(scales)[chunk / LANES] = finite ? s : __uint_as_float(0x7fc00000u);
   } else {
     constexpr int SHIFT = MODE == kMXFP4 ? 2 : 8;
-    constexpr uint32_t TOP = MODE == kMXFP4 ? 0x400000u : 0x600000u;  // fraction bits of 1.5, 1.75
-    int c = static_cast<int>(amax >> 23) - SHIFT + ((amax & 0x7fffffu) > TOP ? 1 : 0);
+    constexpr uint32_t TOP = MODE == kMXFP4 ? 0x400000u : 0x600000u;  // fraction bits of 1.5, 1.75: one more above them
+    int c = static_cast<int>((amax + (0x7fffffu - TOP)) >> 23) - SHIFT;
     c = amax == 0 ? 127 : (c < 0 ? 0 : c);
     // a block of other than finite values: all codes zero
     const float f = __uint_as_float(static_cast<uint32_t>(254 - c) << 23);
@@ -161,15 +182,16 @@ __global__ void __launch_bounds__(256) quantize_kernel(const T* __restrict__ x, 
 #pragma unroll
       for (int j = 0; j < kVec; j += 2) swiglu2(v[j], v[j + 1], u[j], u[j + 1]);
     }
-    quantize8<MODE>(v, row < M && c < cpr, static_cast<size_t>(row * cpr + c), codes, scales);
+    quantize8<MODE, ACT == FG_ACT_SWIGLU && MODE != kBlock>(v, row < M && c < cpr, static_cast<size_t>(row * cpr + c), codes, scales);
   }
 }
 
 // The gated activation with its checkpoint: codes and scales of silu(g) * u, and
 // of g and u themselves, as the forward pass of a training step keeps them.  One
 // pass: 4 bytes read and 3 written per value of the activation, where three calls
-// of the quantiser read 8.  Bound by HBM: 32761 x 2048 in 32-K blocks in 84 us
-// (5.7 TB/s of the 6.8 that a copy reaches) with two rows a thread, 94 with one.
+// of the quantiser read 8.  Bound by HBM: 32761 x 2048 in 32-K blocks in 73.5 us
+// (6.5 TB/s of the 6.8 that a copy reaches); in fp32 blocks of 128 in 109, whose scales'
+// and quotients' instructions take longer.
 template <int MODE, int ROWS, typename T>
 __global__ void __launch_bounds__(256) checkpoint_kernel(const T* __restrict__ x, int64_t M, int64_t K, int64_t ldx,
                                                          void* __restrict__ codes, void* __restrict__ scales,
@@ -195,14 +217,15 @@ __global__ void __launch_bounds__(256) checkpoint_kernel(const T* __restrict__ x
   for (int i = 0; i < ROWS; ++i) {
     const int64_t row = row0 + i * blockDim.y;
     const bool live = row < M && c < cpr;
-    float v[kVec], u[kVec];
-    a[i].widen(v);
+    float v[kVec], g[kVec], u[kVec];
+    a[i].widen(g);
     b[i].widen(u);
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) v[j] = g[j];
 #pragma unroll
     for (int j = 0; j < kVec; j += 2) swiglu2(v[j], v[j + 1], u[j], u[j + 1]);
     quantize8<MODE>(v, live, static_cast<size_t>(row * cpr + c), codes, scales);
-    a[i].widen(v);
-    quantize8<MODE>(v, live, static_cast<size_t>(2 * row * cpr + c), saved, saved_scales);
+    quantize8<MODE>(g, live, static_cast<size_t>(2 * row * cpr + c), saved, saved_scales);
     quantize8<MODE>(u, live, static_cast<size_t>((2 * row + 1) * cpr + c), saved, saved_scales);
   }
 }
