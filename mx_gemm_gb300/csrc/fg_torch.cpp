@@ -16,9 +16,11 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <array>
 #include <cstdarg>
 #include <cstdio>
 #include <string>
+#include <utility>
 
 #include "../../include/fg.h"
 
@@ -171,29 +173,33 @@ at::Tensor make(at::IntArrayRef sizes, at::ScalarType type, const at::Device& de
   return at::detail::empty_cuda(sizes, type, device, std::nullopt);
 }
 
-// Two tensors in one allocation, which costs the host about as much as a launch: what
-// always goes together, values and their scales.  The second begins at a multiple of
-// 128 bytes.
-struct Both {
-  at::Tensor first, second;
+// Tensors that always go together, in one allocation, which costs the host about as
+// much as a launch: values and their scales, a loss and what comes with it.  Each begins
+// at a multiple of 128 bytes.
+struct Shape {
+  at::IntArrayRef sizes;
+  at::ScalarType type;
 };
 
-at::Tensor part(const at::Tensor& whole, int64_t byte, at::IntArrayRef sizes, at::ScalarType type) {
-  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(), c10::scalarTypeToTypeMeta(type));
-  t.unsafeGetTensorImpl()->set_storage_offset(byte / static_cast<int64_t>(c10::elementSize(type)));
-  t.unsafeGetTensorImpl()->set_sizes_contiguous(sizes);
-  return t;
-}
-
-Both make_both(at::IntArrayRef sizes, at::ScalarType type, at::IntArrayRef sizes2, at::ScalarType type2, const at::Device& device) {
-  auto bytes = [](at::IntArrayRef v, at::ScalarType t) {
-    int64_t n = static_cast<int64_t>(c10::elementSize(t));
-    for (const int64_t d : v) n *= d;
-    return n;
-  };
-  const int64_t at2 = (bytes(sizes, type) + 127) / 128 * 128;
-  const at::Tensor whole = make({at2 + bytes(sizes2, type2)}, at::kByte, device);
-  return {part(whole, 0, sizes, type), part(whole, at2, sizes2, type2)};
+template <size_t N>
+std::array<at::Tensor, N> make_together(const Shape (&what)[N], const at::Device& device) {
+  int64_t at[N], bytes = 0;
+  for (size_t i = 0; i < N; ++i) {
+    at[i] = bytes = (bytes + 127) / 128 * 128;
+    int64_t n = static_cast<int64_t>(c10::elementSize(what[i].type));
+    for (const int64_t d : what[i].sizes) n *= d;
+    bytes += n;
+  }
+  const at::Tensor whole = make({bytes}, at::kByte, device);
+  std::array<at::Tensor, N> out;
+  for (size_t i = 0; i < N; ++i) {
+    out[i] = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(),
+                                                      c10::scalarTypeToTypeMeta(what[i].type));
+    c10::TensorImpl* t = out[i].unsafeGetTensorImpl();
+    t->set_storage_offset(at[i] / static_cast<int64_t>(c10::elementSize(what[i].type)));
+    t->set_sizes_contiguous(what[i].sizes);
+  }
+  return out;
 }
 
 PyObject* wrap(const at::Tensor& t) {
@@ -251,9 +257,10 @@ struct Codes {
 
 Codes make_codes(int mode, int64_t m, int64_t k, const at::Device& device) {
   const bool half = mode == FG_MXFP4, wide = mode == FG_FP8_BLOCK128;
-  Both b = make_both({m, half ? k / 2 : k}, half ? at::kByte : at::kFloat8_e4m3fn, {m, k / (wide || mode == FG_MXFP8 ? 128 : 32)},
-                     wide ? at::kFloat : at::kFloat8_e8m0fnu, device);
-  return {std::move(b.first), std::move(b.second)};
+  auto [codes, scales] = make_together({{{m, half ? k / 2 : k}, half ? at::kByte : at::kFloat8_e4m3fn},
+                                        {{m, k / (wide || mode == FG_MXFP8 ? 128 : 32)}, wide ? at::kFloat : at::kFloat8_e8m0fnu}},
+                                       device);
+  return {std::move(codes), std::move(scales)};
 }
 
 void* data(const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
@@ -616,9 +623,10 @@ void make_columns(ColumnOperand& c, int64_t columns, int64_t rows, int experts, 
   int64_t places = 0;
   uint64_t data_bytes = 0, sf_bytes = 0;
   check(fg_columns_size(columns, rows, experts, &places, &data_bytes, &sf_bytes));
-  Both b = make_both({static_cast<int64_t>(data_bytes)}, at::kByte, {static_cast<int64_t>(sf_bytes)}, at::kByte, device);
-  c.data = std::move(b.first);
-  c.sf = std::move(b.second);
+  auto [data, sf] =
+      make_together({{{static_cast<int64_t>(data_bytes)}, at::kByte}, {{static_cast<int64_t>(sf_bytes)}, at::kByte}}, device);
+  c.data = std::move(data);
+  c.sf = std::move(sf);
 }
 
 PyObject* wrap(const ColumnOperand& c) {
@@ -646,9 +654,9 @@ PyObject* quantize_weight(PyObject*, PyObject* const* a, Py_ssize_t n) {
       Unlocked u;
       Pool pool(launch);
       const int64_t rows = transpose ? K : N, cols = transpose ? N : K;
-      Both b = make_both({E * rows, cols}, at::kFloat8_e4m3fn, {E * rows / 128, cols / 128}, at::kFloat, device);
-      codes = std::move(b.first);
-      scales = std::move(b.second);
+      auto both = make_together({{{E * rows, cols}, at::kFloat8_e4m3fn}, {{E * rows / 128, cols / 128}, at::kFloat}}, device);
+      codes = std::move(both[0]);
+      scales = std::move(both[1]);
       check(fg_quantize_weight(mode, w.data_ptr(), type, (int)E, N, K, ld, stride, transpose, codes.data_ptr(), scales.data_ptr(),
                                launch.stream));
       keep(launch, {&codes, &scales}, {&w});
@@ -852,10 +860,11 @@ PyObject* moe_balance_loss(PyObject*, PyObject* const* a, Py_ssize_t n) {
       uint64_t need = 0;
       check(fg_moe_balance_loss_workspace_size(r.m, E, &need));
       if (need) ws = make({static_cast<int64_t>(need)}, at::kByte, device);
-      loss = make({}, at::kFloat, device);
-      counts = make({r.k}, at::kInt, device);
-      probs = make({r.k}, at::kFloat, device);
-      slopes = make({r.k}, at::kFloat, device);
+      auto all = make_together({{{}, at::kFloat}, {{r.k}, at::kInt}, {{r.k}, at::kFloat}, {{r.k}, at::kFloat}}, device);
+      loss = std::move(all[0]);
+      counts = std::move(all[1]);
+      probs = std::move(all[2]);
+      slopes = std::move(all[3]);
       check(fg_moe_balance_loss(x.data_ptr(), type, r.m, E, r.ld, ints(offsets), (float)coefficient, loss.data_ptr<float>(),
                                 counts.data_ptr<int32_t>(), probs.data_ptr<float>(), slopes.data_ptr<float>(), data(ws), need,
                                 launch.stream));

@@ -319,3 +319,18 @@ def test_weight_quotients_are_those_of_the_division(dtype, size):
     d = fg.swiglu_backward("fp8_block128", x, saved, saved_scales, plain=True)
     s = d.scales.repeat_interleave(128, 1)
     same(d.codes.view(torch.uint8), (d.dx / s).to(torch.float8_e4m3fn).view(torch.uint8))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("size", [0, 30, -30, 110, -110])
+def test_row_quotients_are_those_of_the_division(dtype, size):
+    """The same for rows' blocks, of the quantiser and of both halves of a checkpoint."""
+    x = torch.ldexp(rand(25, 2048, 4096), torch.tensor(size, device="cuda")).to(dtype)
+    codes, scales = fg.quantize("fp8_block128", x)
+    _, _, saved, saved_scales = fg.swiglu_checkpoint("fp8_block128", x)
+    top = x.float().view(2048, 32, 128).abs().amax(2)
+    same(scales, torch.where(top == 0, torch.ones_like(top), ref.over_448(top).float()))
+    want = (x.float() / scales.repeat_interleave(128, 1)).to(torch.float8_e4m3fn)
+    same(codes.view(torch.uint8), want.view(torch.uint8))
+    same(saved.view(torch.uint8), want.view(torch.uint8))
+    same(saved_scales, scales)
