@@ -615,8 +615,8 @@ __global__ void __launch_bounds__(256) dweights_kernel(const float* __restrict__
 
 // 128 x 128 blocks of weights: scale and codes, straight or transposed, by 16 warps, a
 // square each, so that the values wait for the block's maximum in registers.  Blocks of
-// threads stay and take every gridDim.x-th block of the weights; the next one's bytes,
-// each thread's own, are on their way to shared memory meanwhile.  8 weights of 4096 x
+// threads stay and take every gridDim.x-th block of the weights; the next one's bytes
+// are on their way to shared memory meanwhile.  8 weights of 4096 x
 // 7168 bf16, transposed, in 108 us (6.5 TB/s, 0.96 of a copy's rate); 150 with a block of
 // threads for each block of weights and a division for each value.
 constexpr int kWeightThreads = 512;
@@ -645,12 +645,19 @@ __global__ void __launch_bounds__(kWeightThreads, 2) weight_kernel(const T* __re
     return a;
   };
   const int in_n = 32 * (warp >> 2) + 4 * tl, in_k = 32 * (warp & 3) + 8 * fl;
+  // Four lanes fetch neighbouring pieces, so that an instruction takes whole sectors, also
+  // where a lane's eight values are two pieces: fp32 weights of the size above in 272 us
+  // straight and 268 transposed; 273 and 292 with each lane fetching its own.
   auto ask = [&](const At& a, int stage) {
-    const T* src = w + a.e * stride + (a.n * 128 + in_n) * ld + a.k * 128 + in_k;
+    const T* src = w + a.e * stride + (a.n * 128 + in_n) * ld + a.k * 128 + 32 * (warp & 3);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4; ++i) {
 #pragma unroll
-      for (int h = 0; h < Q; ++h) fetch16(&landing[stage][i][h][threadIdx.x], src + i * ld + h * (8 / Q), true);
+      for (int h = 0; h < Q; ++h) {
+        const int piece = 4 * h + fl;
+        fetch16(&landing[stage][i][piece % Q][threadIdx.x - fl + piece / Q], src + i * ld + piece * (8 / Q), true);
+      }
+    }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   At next = place(blockIdx.x);
@@ -666,6 +673,7 @@ __global__ void __launch_bounds__(kWeightThreads, 2) weight_kernel(const T* __re
     } else {
       asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
+    __syncwarp();
     const int64_t e = a.e;
     const int n = a.n * 128 + in_n, k = a.k * 128 + in_k;
     float v[4][8], most = 0.f;
