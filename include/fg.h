@@ -498,7 +498,8 @@ FG_API fg_status fg_moe_balance_loss(const void* logits, int type, int64_t T, in
 /*
  * Gradient of the logits (out [T][E], their type) from the gradients dweights
  * [T][top_k] of the routing weights of `experts` (both as fg_moe_route orders them;
- * NULL: none; expert -1 is no choice) and the balance loss's slopes (NULL: none):
+ * NULL: none; an expert outside 0..E-1, or whose logit is NaN or -infinity, is no
+ * choice, whatever lies in its dweights) and the balance loss's slopes (NULL: none):
  *   out[t][e] = p_te (slopes[e] - sum_i p_ti slopes[i])
  *             + q_j (dweights[t][j] - sum_i q_i dweights[t][i])   where e = experts[t][j],
  * q being the softmax over the chosen experts with FG_FLAG_RENORMALIZE; without it

@@ -270,15 +270,17 @@ __global__ void __launch_bounds__(32 * kBackwardWarps) route_backward_kernel(con
       if (expert >= p.E) expert = -1;
       if (expert >= 0) {
         const T* l = static_cast<const T*>(p.logits) + t * p.ldl + expert;
-        chosen = static_cast<float>(*l);
+        chosen = fmaxf(static_cast<float>(*l), -INFINITY);  // (a NaN is not kept)
       }
+      // what lies beside no choice is not a number that q = 0 could be multiplied with
+      dw = chosen > -INFINITY ? dw : 0.f;
     }
     if (t + step < p.T) next.load(p, t + step, lane);
     float v[VPL];
     const float top = exponentials(now, v);
     // sums of the exponentials, of their products with the slopes, and of the chosen
     // ones' and theirs with dweights
-    const float q = expert >= 0 && chosen > -INFINITY ? exp_below(chosen, top) : 0.f;
+    const float q = chosen > -INFINITY ? exp_below(chosen, top) : 0.f;
     float sums[4] = {0.f, 0.f, q, q * dw};
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
