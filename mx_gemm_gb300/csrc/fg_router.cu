@@ -278,9 +278,12 @@ __global__ void __launch_bounds__(32 * kBackwardWarps) route_backward_kernel(con
     if (t + step < p.T) next.load(p, t + step, lane);
     float v[VPL];
     const float top = exponentials(now, v);
+    // The chosen ones' exponentials: renormalised by their own largest logit, which may
+    // lie so far below the token's that those against that one would all be zero.
+    const float from = p.renormalize ? warp_max(chosen) : top;
+    const float q = chosen > -INFINITY ? exp_below(chosen, from) : 0.f;
     // sums of the exponentials, of their products with the slopes, and of the chosen
     // ones' and theirs with dweights
-    const float q = chosen > -INFINITY ? exp_below(chosen, top) : 0.f;
     float sums[4] = {0.f, 0.f, q, q * dw};
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {

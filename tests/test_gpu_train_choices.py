@@ -1,5 +1,5 @@
-"""The logits' gradient for choices that routing would not have made: of no expert, and
-of logits that are not numbers."""
+"""The logits' gradient for choices that routing would not have made: of no expert, of
+logits that are not numbers, and far below the token's largest logit."""
 import pytest
 import torch
 
@@ -39,3 +39,41 @@ def test_what_no_choice_carries_is_not_read(renormalize, dtype):
     ref.within(clean, want, ref.REL * mag + EPS[dtype] * want.abs() + 1e-38)
     for odd in (NAN, INF, -INF):
         same(fg.moe_route_backward(l, of(chosen), torch.where(none, odd, dw), slopes, renormalize=renormalize), clean)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("below", [0.0, 90.0, 103.0, 150.0, 1e30])
+def test_choices_far_below_the_largest_logit(below, dtype):
+    """Renormalised weights are the softmax of the chosen logits alone, however far the largest one is."""
+    tokens, experts, top_k = 60, 40, 4
+    l = logits_of(tokens, experts, 3).to(dtype)
+    l[:, 10:20] += below
+    g = torch.Generator(device="cuda").manual_seed(4)
+    chosen = torch.rand(tokens, 10, generator=g, device="cuda").argsort(1)[:, :top_k].int()
+    chosen[::4, 3] = -1
+    dw = torch.randn(tokens, top_k, generator=g, device="cuda")
+    d = fg.moe_route_backward(l, of(chosen), dw)
+    x, ok, at = l.double(), chosen >= 0, chosen.clamp(min=0).long()
+    q = torch.softmax(torch.where(ok, torch.gather(x, 1, at), -INF), 1)
+    w = torch.where(ok, dw.double(), 0.0)
+    mean, size = (q * w).sum(1, keepdim=True), (q * w.abs()).sum(1, keepdim=True)
+    want = torch.zeros_like(x).scatter_add_(1, at, q * (w - mean))
+    mag = torch.zeros_like(x).scatter_add_(1, at, q * (w.abs() + size))
+    assert (want.abs().amax(1) > 1e-3).sum() > tokens // 2
+    ref.within(d, want, ref.REL * mag + EPS[dtype] * want.abs() + 1e-38)
+
+
+def test_one_choice_of_infinity():
+    l = logits_of(3, 8, 5)
+    l[0, 1] = INF           # not chosen
+    l[1, 2] = l[1, 3] = INF  # both chosen, with a finite one
+    l[2, 4] = INF           # chosen, twice
+    chosen = torch.tensor([[2, 3, 4], [2, 3, 4], [4, 5, 4]])
+    dw = torch.tensor([[1.0, 2.0, 4.0]] * 3, device="cuda")
+    d = fg.moe_route_backward(l, of(chosen), dw).double()
+    assert torch.isfinite(d).all()
+    q = torch.softmax(l[0, 2:5].double(), 0)
+    want = q * (dw[0].double() - (q * dw[0].double()).sum())
+    ref.within(d[0, 2:5], want, ref.REL * (q * 8))
+    same(d[1], torch.tensor([0, 0, -0.25, 0.25, 0, 0, 0, 0], device="cuda", dtype=torch.float64))
+    same(d[2], torch.zeros(8, device="cuda", dtype=torch.float64))
