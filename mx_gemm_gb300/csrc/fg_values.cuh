@@ -134,8 +134,11 @@ __device__ __forceinline__ float f32_scale_of(uint32_t amax) {
 // and q = v r, the remainder v - q s is exact in one fused multiply-add and q + (v - q s)
 // r is the quotient (Markstein 1990, "Computation of elementary functions on the IBM RISC
 // System/6000 processor").  Three instructions for two values, where a division takes ten
-// for one (a checkpoint of 32761 x 2048: 154 us with divisions, 109 so).  It holds where nothing leaves the normal numbers: `sure`, for quotients that
-// are no less than half an e4m3 step; a smaller one's code is 0 whatever its last bits.
+// for one (a checkpoint of 32761 x 2048: 154 us with divisions, 109 so).  It holds while the
+// remainder is a multiple of fp32's smallest step, 2^-149: with q >= 2^a and s >= 2^b it is
+// one of 2^(a + b - 46).  Quotients below half an e4m3 step, 2^-10, have code 0 whatever
+// their last bits, so b >= -93 is enough.  `sure` keeps three powers of two from there, and
+// as many values as can be from fp32's upper end.
 struct Over {
   Pair r, minus_s;
   bool sure;
@@ -143,7 +146,7 @@ struct Over {
     const float x = __frcp_rn(s);
     r = pair_of(x, x);
     minus_s = pair_of(-s, -s);
-    sure = s > 0x1p-100f && s < 0x1p100f;
+    sure = s >= 0x1p-90f && s < 0x1p100f;
   }
   __device__ __forceinline__ Pair operator()(Pair v) const {
     const Pair q = mul(v, r);
