@@ -307,7 +307,7 @@ __device__ __forceinline__ void store_rows(const Square& v, uint8_t* out, int64_
   const bool finite = m[0] < 0x7f800000u;
   const int64_t at = block + mine * (cols / scale_block(FMT));
   const bool stores = mine < rows && (FMT == kE8m0By32 || threadIdx.x < 32);
-  float scale;  // what values are multiplied by (E8M0) or divided by
+  float scale;  // what values are multiplied by (E8M0) or divided by (with their signs turned: see Over)
   if (FMT == kF32By128) {
     scale = f32_scale_of(finite ? m[0] : 0u);
     if (stores) static_cast<float*>(scales)[at] = finite ? scale : __uint_as_float(0x7fc00000u);
@@ -335,7 +335,7 @@ __device__ __forceinline__ void store_rows(const Square& v, uint8_t* out, int64_
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const float2 x = halves(v.p[i][q]);
-          w[q] = e4m3x2(ok ? __fdiv_rn(x.x, f) : 0.f, ok ? __fdiv_rn(x.y, f) : 0.f);
+          w[q] = e4m3x2(ok ? __fdiv_rn(x.x, -f) : -0.f, ok ? __fdiv_rn(x.y, -f) : -0.f);
         }
       }
     } else {
@@ -346,7 +346,8 @@ __device__ __forceinline__ void store_rows(const Square& v, uint8_t* out, int64_
         w[q] = e4m3x2(x.x, x.y);
       }
     }
-    const uint2 o = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+    constexpr uint32_t TURN = FMT == kF32By128 ? kMinusCodes : 0u;
+    const uint2 o = make_uint2((w[0] | (w[1] << 16)) ^ TURN, (w[2] | (w[3] << 16)) ^ TURN);
     if (4 * tl + i < rows) *reinterpret_cast<uint2*>(out + i * cols) = o;
   }
 }
@@ -699,7 +700,7 @@ __global__ void __launch_bounds__(kWeightThreads, 2) weight_kernel(const T* __re
     const Over over(s);
     // words of four codes: column j's, or (row i, half) 2 i + half
     uint32_t c[8];
-    auto words = [&](auto quotient) {  // of the pairs of a row
+    auto words = [&](auto quotient) {  // the negative one of the pairs of a row
       float2 x[4][4];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -708,18 +709,18 @@ __global__ void __launch_bounds__(kWeightThreads, 2) weight_kernel(const T* __re
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if (TRANSPOSE) {
-          c[2 * j] = e4m3x2(x[0][j].x, x[1][j].x) | (e4m3x2(x[2][j].x, x[3][j].x) << 16);
-          c[2 * j + 1] = e4m3x2(x[0][j].y, x[1][j].y) | (e4m3x2(x[2][j].y, x[3][j].y) << 16);
+          c[2 * j] = (e4m3x2(x[0][j].x, x[1][j].x) | (e4m3x2(x[2][j].x, x[3][j].x) << 16)) ^ kMinusCodes;
+          c[2 * j + 1] = (e4m3x2(x[0][j].y, x[1][j].y) | (e4m3x2(x[2][j].y, x[3][j].y) << 16)) ^ kMinusCodes;
         } else {
-          c[2 * j] = e4m3x2(x[j][0].x, x[j][0].y) | (e4m3x2(x[j][1].x, x[j][1].y) << 16);
-          c[2 * j + 1] = e4m3x2(x[j][2].x, x[j][2].y) | (e4m3x2(x[j][3].x, x[j][3].y) << 16);
+          c[2 * j] = (e4m3x2(x[j][0].x, x[j][0].y) | (e4m3x2(x[j][1].x, x[j][1].y) << 16)) ^ kMinusCodes;
+          c[2 * j + 1] = (e4m3x2(x[j][2].x, x[j][2].y) | (e4m3x2(x[j][3].x, x[j][3].y) << 16)) ^ kMinusCodes;
         }
       }
     };
     if (over.sure && finite)
       words([&](float x, float y) { return halves(over(pair_of(x, y))); });
     else
-      words([&](float x, float y) { return make_float2(finite ? __fdiv_rn(x, s) : 0.f, finite ? __fdiv_rn(y, s) : 0.f); });
+      words([&](float x, float y) { return make_float2(finite ? __fdiv_rn(x, -s) : -0.f, finite ? __fdiv_rn(y, -s) : -0.f); });
     if (TRANSPOSE) {
       uint8_t* out = codes + (e * K + k) * static_cast<int64_t>(N) + n;
 #pragma unroll

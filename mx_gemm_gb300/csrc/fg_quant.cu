@@ -81,9 +81,8 @@ __device__ __forceinline__ void quantize8(float (&v)[kVec], bool live, size_t ch
   const bool finite = amax < 0x7f800000u;
   const bool first = (threadIdx.x & (LANES - 1)) == 0;
   if (MODE == kBlock) {
-    // The NaN scale is put in after the divisions, which take zeros then: chosen
-    // before them it costs four registers, and the norm of 32761 x 4096 an eighth
-    // of its warps (170 us; 145 so).
+    // v becomes the negative quotients.  The NaN scale is put in after them, which are
+    // of zeros then.
     const float s = f32_scale_of(finite ? amax : 0u);
     const Over over(s);
     if (over.sure && finite) {
@@ -95,7 +94,7 @@ __device__ __forceinline__ void quantize8(float (&v)[kVec], bool live, size_t ch
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) v[i] = __fdiv_rn(finite ? v[i] : 0.f, s);
+      for (int i = 0; i < kVec; ++i) v[i] = __fdiv_rn(finite ? v[i] : 0.f, -s);
     }
     if (live && first) static_cast<float*>(scales)[chunk / LANES] = finite ? s : __uint_as_float(0x7fc00000u);
   } else {
@@ -117,9 +116,10 @@ __device__ __forceinline__ void quantize8(float (&v)[kVec], bool live, size_t ch
   if (MODE == kMXFP4) {
     static_cast<uint32_t*>(codes)[chunk] = e2m1x8(v);
   } else {
+    constexpr uint32_t TURN = MODE == kBlock ? kMinusCodes : 0u;
     uint2 o;
-    o.x = e4m3x2(v[0], v[1]) | (e4m3x2(v[2], v[3]) << 16);
-    o.y = e4m3x2(v[4], v[5]) | (e4m3x2(v[6], v[7]) << 16);
+    o.x = (e4m3x2(v[0], v[1]) | (e4m3x2(v[2], v[3]) << 16)) ^ TURN;
+    o.y = (e4m3x2(v[4], v[5]) | (e4m3x2(v[6], v[7]) << 16)) ^ TURN;
     static_cast<uint2*>(codes)[chunk] = o;
   }
 }

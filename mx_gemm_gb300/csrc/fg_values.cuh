@@ -130,29 +130,33 @@ __device__ __forceinline__ float f32_scale_of(uint32_t amax) {
                    : (amax < (1u << 17) ? __uint_as_float((amax + 447u) / 448u) : __fdiv_rn(__uint_as_float(amax), 448.f));
 }
 
-// v / s for a block's fp32 scale s, rounded to nearest: with r = 1 / s rounded to nearest
+// -(v / s) for a block's fp32 scale s, rounded to nearest: with r = 1 / s rounded to nearest
 // and q = v r, the remainder v - q s is exact in one fused multiply-add and q + (v - q s)
 // r is the quotient (Markstein 1990, "Computation of elementary functions on the IBM RISC
 // System/6000 processor").  Three instructions for two values, where a division takes ten
 // for one (a checkpoint of 32761 x 2048: 154 us with divisions, 109 so).  It holds while the
 // remainder is a multiple of fp32's smallest step, 2^-149: with q >= 2^a and s >= 2^b it is
 // one of 2^(a + b - 46).  Quotients below half an e4m3 step, 2^-10, have code 0 whatever
-// their last bits, so b >= -93 is enough.  `sure` keeps three powers of two from there, and
-// as many values as can be from fp32's upper end.
+// their last bits, so b >= -93 is enough; `sure` keeps three powers of two from there, and
+// r and all products from the ends of fp32.
+//
+// Every sign is turned: of v = -0 this leaves +0, where q + (v - q s) r, a sum of zeros of
+// both signs, would be +0 for either.  The codes' sign bits are turned back (kMinusCodes).
 struct Over {
-  Pair r, minus_s;
+  Pair minus_r, s2;
   bool sure;
   __device__ __forceinline__ explicit Over(float s) {
-    const float x = __frcp_rn(s);
-    r = pair_of(x, x);
-    minus_s = pair_of(-s, -s);
+    const float x = -__frcp_rn(s);
+    minus_r = pair_of(x, x);
+    s2 = pair_of(s, s);
     sure = s >= 0x1p-90f && s < 0x1p100f;
   }
   __device__ __forceinline__ Pair operator()(Pair v) const {
-    const Pair q = mul(v, r);
-    return fma(fma(q, minus_s, v), r, q);
+    const Pair q = mul(v, minus_r);
+    return fma(fma(q, s2, v), minus_r, q);
   }
 };
+constexpr uint32_t kMinusCodes = 0x80808080u;  // sign bits of four codes
 
 // Two values of two e4m3 codes, the lower half's first.
 __device__ __forceinline__ float2 e4m3_values(uint32_t codes) {

@@ -1,6 +1,6 @@
 """fp8_block128's codes are the quotients v / s rounded once, whatever way they are
 worked out: at block scales near the smallest ones, where a remainder is no longer
-exact."""
+exact, and for zeros, which keep their sign."""
 import pytest
 import torch
 
@@ -56,6 +56,55 @@ def test_next_to_borders_between_codes(exponent):
     # and the rows of the activation's gradient: gates of 88 and values of 1 leave dg near dy
     saved, saved_scales = fg.quantize(MODE, torch.cat([torch.full_like(x, 88.0), torch.ones_like(x)], 1))
     d = fg.swiglu_backward(MODE, x, saved, saved_scales, plain=True)
+    same(d.codes.view(torch.uint8), quotients(d.dx, d.scales.repeat_interleave(128, 1)))
+
+
+def with_zeros(seed, *shape):
+    """Values among which are zeros of either sign, and blocks of nothing else."""
+    x = rand(seed, *shape)
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    where = torch.rand(shape, generator=g, device="cuda")
+    x = torch.where(where < 0.2, 0.0, torch.where(where < 0.4, -0.0, x))
+    x.view(-1, x.shape[-1])[:128, :128] = -0.0
+    return x
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("size", [0, 110, -110])
+def test_zeros_keep_their_sign(size, dtype):
+    x = torch.ldexp(with_zeros(1, 256, 512), torch.tensor(size, device="cuda")).to(dtype)
+    assert torch.signbit(x[0, 0]) and not x[0, 0]
+    codes, scales = fg.quantize(MODE, x)
+    want = quotients(x.float(), scales.repeat_interleave(128, 1))
+    same(codes.view(torch.uint8), want)
+    _, _, saved, _ = fg.swiglu_checkpoint(MODE, x)
+    same(saved.view(torch.uint8), want)
+    for transpose in (False, True):
+        codes, scales = fg.quantize_weight(MODE, x, transpose=transpose)
+        v = (x.T if transpose else x).float()
+        same(codes.view(torch.uint8), quotients(v, scales.repeat_interleave(128, 0).repeat_interleave(128, 1)))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_zeros_of_the_norm_and_the_activation_keep_their_sign(dtype):
+    x = with_zeros(2, 256, 512).to(dtype)
+    codes, scales, _, y = fg.rmsnorm_quantize(MODE, x, torch.ones(512, device="cuda", dtype=dtype), normed=True)
+    zero = y == 0
+    assert torch.signbit(y[zero]).any() and not torch.signbit(y[zero]).all()
+    same(codes.view(torch.uint8)[zero], torch.where(torch.signbit(y[zero]), 0x80, 0).to(torch.uint8))
+    # gate 0 or -0, and value 0 or -0: the product's sign is that of either
+    codes, _ = fg.quantize(MODE, x, act="swiglu")
+    g, u = x.float().chunk(2, 1)
+    zero = (g == 0) | (u == 0)
+    sign = torch.signbit(g) ^ torch.signbit(u)
+    same(codes.view(torch.uint8)[zero], torch.where(sign[zero], 0x80, 0).to(torch.uint8))
+
+
+def test_zeros_of_the_gradient_keep_their_sign():
+    dy = with_zeros(3, 256, 256)
+    saved, saved_scales = fg.quantize(MODE, rand(4, 256, 512))
+    d = fg.swiglu_backward(MODE, dy, saved, saved_scales, plain=True)
+    assert torch.signbit(d.dx[d.dx == 0]).any() and not torch.signbit(d.dx[d.dx == 0]).all()
     same(d.codes.view(torch.uint8), quotients(d.dx, d.scales.repeat_interleave(128, 1)))
 
 
