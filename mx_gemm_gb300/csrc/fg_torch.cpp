@@ -379,10 +379,10 @@ PyObject* moe_route(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // (A, weight data, descriptor's address, offsets, a_scales or None, rows or None,
-//  Y or None, workspace or None, flags, stream) -> Y
+//  Y or None, workspace or None, flags, stream, weight's scale image or None) -> Y
 PyObject* grouped_gemm(PyObject*, PyObject* const* v, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
-    arity(n, 10, "grouped_gemm");
+    arity(n, 11, "grouped_gemm");
     const at::Tensor& weight = tensor(v[1], "the weight");
     const at::Device device = weight.device();
     const fg_bshuf* b = reinterpret_cast<const fg_bshuf*>(static_cast<intptr_t>(integer(v[2], "the descriptor's address")));
@@ -445,6 +445,7 @@ PyObject* grouped_gemm(PyObject*, PyObject* const* v, Py_ssize_t n) {
       contiguous(ws, "workspace");
     }
     const uint32_t flags = flag_bits(v[8], "flags");
+    const at::Tensor* sf = v[10] == Py_None ? nullptr : &tensor(v[10], "the scale image");
     const Launch launch = launch_of(v[9], device);
     {
       Unlocked u;
@@ -460,7 +461,7 @@ PyObject* grouped_gemm(PyObject*, PyObject* const* v, Py_ssize_t n) {
       check(fg_grouped_gemm(A.data_ptr(), scales ? scales->data_ptr() : nullptr, T, rows ? rows->data_ptr<int32_t>() : nullptr, R,
                             offsets.data_ptr<int32_t>(), (int)E, b, mode, Y.data_ptr(), data(ws), bytes, flags,
                             launch.stream));
-      keep(launch, {&Y}, {&A, &weight, &offsets, scales, rows, &Y, &ws});
+      keep(launch, {&Y}, {&A, &weight, sf, &offsets, scales, rows, &Y, &ws});
     }
     return wrap(Y);
   });

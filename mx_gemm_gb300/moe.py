@@ -120,7 +120,7 @@ def grouped_gemm(A, pb, offsets, a_scales=None, rows=None, Y=None, workspace=Non
     allocated here when one is needed and none is given.
     """
     return (_binding or binding()).grouped_gemm(A, pb.data, ctypes.addressof(pb.desc), offsets, a_scales, rows, Y, workspace,
-                                                flags, _handle(stream))
+                                                flags, _handle(stream), pb.sf)
 
 
 def moe_combine(Y, slots, weights, residual=None, stream=None):

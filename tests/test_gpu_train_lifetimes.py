@@ -1,0 +1,47 @@
+"""Weights that a training step lays out anew, let go of while another stream still
+reads them."""
+import pytest
+import torch
+
+import mx_gemm_gb300 as fg
+from tests import train_ref as ref
+from tests.test_gpu_streams import SLOW, rows, same
+
+pytestmark = pytest.mark.gpu
+
+
+def busy(stream):
+    overwrite((1,))  # a kernel's first launch, which loads it, waits for the device
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(SLOW)
+
+
+def overwrite(like):
+    """Memory of the sizes of `like` on the current stream, written to."""
+    junk = []
+    for t in like:
+        for _ in range(4):
+            junk.append(torch.full((t,), 0x7b, dtype=torch.uint8, device="cuda"))
+    return junk
+
+
+@pytest.mark.parametrize("mode", ["mxfp8_b32", "fp8_block128"])
+@pytest.mark.parametrize("total", [24, 4096])
+def test_weights_of_a_grouped_product(mode, total):
+    a, a_s = fg.quantize(mode, rows(1, total, 1024))
+    b, b_s = (fg.quantize_weight if mode == "fp8_block128" else fg.quantize)(mode, rows(2, 8 * 512, 1024))
+    offsets = ref.fixed_offsets([total // 8] * 8)
+    want = fg.grouped_gemm(a, fg.preshuffle_b(mode, b, b_s), offsets, a_s)
+    pb = fg.preshuffle_b(mode, b, b_s)
+    sizes = pb.data.numel(), pb.sf.numel()
+    other = torch.cuda.Stream()
+    busy(other)
+    got = fg.grouped_gemm(a, pb, offsets, a_s, stream=other)
+    del pb
+    junk = overwrite(sizes)
+    torch.cuda.current_stream().synchronize()
+    assert not other.query() and junk
+    torch.cuda.synchronize()
+    assert same((got,), (want,))
