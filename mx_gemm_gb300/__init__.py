@@ -236,6 +236,19 @@ def _empty(shape, dtype, device, stream):
     return t
 
 
+def _keep(device, stream, *tensors):
+    """The memory of the caller's tensors is not reused before `stream`, if it is another one than the current, is done
+    with them: relayouts are given codes and scales that nobody else holds."""
+    handle = None if stream is None else _stream(stream)
+    handle = 0 if handle == 1 else handle
+    if handle is None or handle == torch._C._cuda_getCurrentRawStream(device.index):
+        return
+    other = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(other)
+
+
 def set_wait_timeout_ns(ns):
     lib().fg_set_wait_timeout_ns(int(ns))
 
@@ -296,6 +309,7 @@ def preshuffle_b(mode, B, b_scales=None, K=None, stream=None):
     desc = BShuf()
     _check(lib().fg_preshuffle_b(mode, _ptr(B), _ptr(b_scales), N, K, _ptr(data), nb, _ptr(sf), ns,
                                  ctypes.byref(desc), _stream(stream)))
+    _keep(B.device, stream, B, b_scales)
     return PreshuffledB(desc, data, sf)
 
 
@@ -314,6 +328,7 @@ def unshuffle_b(pb, stream=None):
     elif mode in (FG_MXFP4, FG_MXFP8_B32, FG_MXFP4_FP8A):
         sc = _empty((N, K // 32), torch.uint8, B.device, stream)
     _check(lib().fg_unshuffle_b(ctypes.byref(pb.desc), _ptr(B), _ptr(sc), _stream(stream)))
+    _keep(B.device, stream, pb.data, pb.sf)
     return B, sc
 
 

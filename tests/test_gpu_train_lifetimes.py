@@ -45,3 +45,40 @@ def test_weights_of_a_grouped_product(mode, total):
     assert not other.query() and junk
     torch.cuda.synchronize()
     assert same((got,), (want,))
+
+
+@pytest.mark.parametrize("mode", ["mxfp8_b32", "fp8_block128"])
+def test_weights_on_their_way_into_the_images(mode):
+    quantize = fg.quantize_weight if mode == "fp8_block128" else fg.quantize
+    w = rows(3, 1024, 2048)
+    parts = quantize(mode, w)
+    want = fg.preshuffle_b(mode, *parts)
+    sizes = parts[0].numel(), parts[1].numel() * parts[1].element_size(), parts[0].untyped_storage().nbytes()
+    other = torch.cuda.Stream()
+    del parts
+    parts = quantize(mode, w)
+    busy(other)
+    got = fg.preshuffle_b(mode, *parts, stream=other)
+    del parts
+    junk = overwrite(sizes)
+    torch.cuda.current_stream().synchronize()
+    assert not other.query() and junk
+    torch.cuda.synchronize()
+    assert same((got.data, got.sf), (want.data, want.sf))
+
+
+@pytest.mark.parametrize("mode", ["mxfp8_b32", "fp8_block128"])
+def test_images_on_their_way_back(mode):
+    b, b_s = (fg.quantize_weight if mode == "fp8_block128" else fg.quantize)(mode, rows(4, 1024, 2048))
+    pb = fg.preshuffle_b(mode, b, b_s)
+    want = fg.unshuffle_b(pb)
+    sizes = pb.data.numel(), pb.sf.numel()
+    other = torch.cuda.Stream()
+    busy(other)
+    got = fg.unshuffle_b(pb, stream=other)
+    del pb
+    junk = overwrite(sizes)
+    torch.cuda.current_stream().synchronize()
+    assert not other.query() and junk
+    torch.cuda.synchronize()
+    assert same(got, want)
