@@ -7,6 +7,10 @@ errors); ``include/fg.h`` has the formulas.  An input's gradient is
 ``grouped_gemm`` with the transposed weight.  Gradients are calls, not autograd
 nodes, and nothing waits for the device, so that a whole training step can be
 captured in a CUDA graph.
+
+Outputs that go together (codes and their scales, a column operand's two images, a
+Balance's tensors) share one allocation: keeping one of them keeps the others' memory,
+and saving one writes it too.  clone() what is kept or saved by itself.
 """
 import ctypes
 from typing import NamedTuple, Optional

@@ -1,5 +1,5 @@
 """Weights that a training step lays out anew, let go of while another stream still
-reads them."""
+reads them; and codes and scales that can be let go of one without the other."""
 import pytest
 import torch
 
@@ -82,3 +82,13 @@ def test_images_on_their_way_back(mode):
     assert not other.query() and junk
     torch.cuda.synchronize()
     assert same(got, want)
+
+
+@pytest.mark.parametrize("mode", ["mxfp8", "mxfp8_b32", "mxfp4", "fp8_block128"])
+def test_codes_and_scales_have_memory_of_their_own(mode):
+    """One can be kept, saved or handed on without the other."""
+    x = rows(5, 33, 1024)
+    for codes, scales in (fg.quantize(mode, x), fg.quantize(mode, x, act="swiglu"),
+                          fg.rmsnorm_quantize(mode, x, torch.ones(1024, device="cuda", dtype=torch.bfloat16))[:2]):
+        for t in (codes, scales):
+            assert t.storage_offset() == 0 and t.untyped_storage().nbytes() == t.numel() * t.element_size()
