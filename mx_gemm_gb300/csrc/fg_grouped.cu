@@ -733,11 +733,28 @@ GroupedPlan grouped_plan(int mode, int64_t R, int64_t E, int64_t N, int64_t K, b
   g.tt = R <= 8 * E || few ? 32 : 256;
   // FP8_BLOCK128: tiles of 128 rows on one SM above 32 rows an expert, where 32-row
   // tiles read the weights again (64 experts, 4096 x 7168: 32 rows each 279 us with
-  // 32 and 287 with 128, 48 rows 346 and 291, 512 rows 2640 and 805), if there are
-  // units for a third of the SMs: below that the cut line wins (8 experts of 512 x
-  // 7168, 128 rows: 25 us against 30; 2048 x 4096, 64 rows, 96 units: 19 and 20; 97
-  // rows 33 and 20).
-  if (block) g.tt = R > 32 * E && (R / 128 + active) * wpairs >= 48 ? 128 : 32;
+  // 32 and 287 with 128, 48 rows 346 and 291, 512 rows 2640 and 805), unless they lose
+  // that by idle SMs, or by the layout of gathered rows where a weight is narrow: what
+  // a call takes is estimated for either.  Both spend 0.5 us on a block's K step and 1 us
+  // on a unit; 32-row tiles are cut evenly over two blocks an SM, 128-row units of two
+  // weight tiles go whole, half a round idle behind the first; half of the experts' last
+  // tiles are counted.  Below four K steps a block of the cut line joins parts of several
+  // units, which is the slower wherever they fall (one step, 32 experts of 384, 45 rows
+  // each: 11.0 us with 32 and 6.2 with 128).
+  // In 800 calls with random routing (2 to 128 experts of 128 x 128 to 4096 x 7168, 32 to
+  // 600 rows each) this takes 1.006 times the faster form's time, 128-row tiles from 48
+  // units on 1.040, 32-row tiles alone 1.33; it is slower than 32-row tiles by more than
+  // 5 % in 14 of them (84 from 48 units on), at worst for 16 experts of 2304 x 4096, 42
+  // rows each gathered: 38 us with 32 and 48 with 128.  64 experts of 128 x 7168, 300
+  // rows gathered: 73 and 101 (32 chosen); 8 of 2048 x 4096, 97 rows: 33 and 20 (128).
+  if (block) {
+    const double sms = sm_count(), halves = 0.5 * static_cast<double>(active), unit = 0.5 * KB + 1.0;
+    const double line = (R / 32.0 + halves) * static_cast<double>(N / 128) / (kBlocksPerSm * sms);
+    const double whole = (R / 128.0 + halves) * static_cast<double>(wpairs) / sms;
+    const double us32 = 5.7 + unit * line;
+    const double us128 = 5.0 + unit * (whole > 1.0 ? whole + 0.5 : 1.0) + (gather ? 1.5 + 0.24e-6 * R * K : 0.0);
+    g.tt = R > 32 * E && (KB < kMinSlabs || us128 < 0.96 * us32) ? 128 : 32;
+  }
   g.tiles = R / g.tt + active;
   const int64_t units = g.tiles * (g.tt == 32 ? N / 128 : wpairs);
   const int64_t line = ((R / 32 + active) * (N / 128) * KB + kMinSlabs - 1) / kMinSlabs;  // blocks of a line of 32-row tiles
@@ -785,6 +802,10 @@ fg_status fg_grouped_gemm_workspace_size(int mode, int64_t R, int E, int64_t N, 
   fg_status s = check_grouped(mode, R, E, N, K);
   if (s != FG_OK) return s;
   *bytes = grouped_plan(mode, R, E, N, K, gather != 0).total();
+  // (FP8_BLOCK128's form can change back with more rows: what is enough for a call is
+  // enough for one of fewer rows, as before it had two forms)
+  if (mode == FG_FP8_BLOCK128 && gather && R > 32 * static_cast<int64_t>(E))
+    *bytes = std::max(*bytes, static_cast<uint64_t>(R) * static_cast<uint64_t>(K));
   return FG_OK;
 }
 
