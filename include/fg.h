@@ -446,6 +446,9 @@ FG_API fg_status fg_quantize_columns(int mode, const void* x, const void* scales
  * (1 + exp(-g)), 0 where that is under 2^-126, and w the row's routing weight (1
  * without weights), in 32 bits:
  *   dg = w dy u s (1 + g (1 - s)),  du = w dy g s,  act = g s u.
+ * s comes from the fast power and reciprocal: it is within (8 + 1.3 |g|) 2^-24 of
+ * itself where g is negative, within 8 * 2^-24 elsewhere; 32-bit dx and dweights
+ * carry that error.
  *  codes, scales  of (dg, du) [R][2K] in `mode`, which is the checkpoint's too;
  *  dx             (dg, du) in dy's type (NULL: not wanted);
  *  dx_data .. dx_desc, act_data .. act_desc  column operands of (dg, du) (2K
@@ -458,7 +461,7 @@ FG_API fg_status fg_quantize_columns(int mode, const void* x, const void* scales
  *                 read; their codes and dx are zero, their scales 127 (fp32: 1).
  *  workspace      fg_swiglu_backward_workspace_size bytes (weighted: weights given).
  * Errors: INVALID_ARG, SHAPE (K not a multiple of the block, or of 128 with
- * columns), ALIGN, WORKSPACE, UNSUPPORTED_ARCH, CUDA.
+ * columns; R / 128 + min(E, R) above 65535), ALIGN, WORKSPACE, UNSUPPORTED_ARCH, CUDA.
  */
 FG_API fg_status fg_swiglu_backward_workspace_size(int64_t R, int64_t K, int weighted, uint64_t* bytes);
 FG_API fg_status fg_swiglu_backward(int mode, const void* dy, int type, int64_t R, int64_t K, int64_t ldd, const void* saved,
@@ -472,7 +475,8 @@ FG_API fg_status fg_swiglu_backward(int mode, const void* dy, int type, int64_t 
  * Weight gradients grouped by expert: out[e][n][k] = the sum over the rows i of
  * expert e of a[i][n] * b[i][k], fp32 accumulation, for column operands a and b
  * (N and K columns) of the same offsets, R and E.  out [E][N][K] in fp32 or bf16;
- * accumulate: fp32 out is added to.  An expert without rows has gradient 0.
+ * accumulate: fp32 out is added to, by additions in memory, which may take values
+ * and sums under 2^-126 for 0.  An expert without rows has gradient 0.
  * Errors: INVALID_ARG, SHAPE (operands of another R or E), ALIGN, LAYOUT,
  * UNSUPPORTED_ARCH, CUDA.
  */

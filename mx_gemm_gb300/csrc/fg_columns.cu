@@ -371,15 +371,19 @@ __device__ __forceinline__ void fetch8(void* dst, const void* src, bool there) {
 // With g, u the checkpoint's values, s = sigmoid(g) and w the row's routing weight:
 //   act = g s u,  dots = sum dy act,  dg = w dy u s (1 + g (1 - s)),  du = w dy g s.
 // e = exp(-g), held below 2^128, and s = 1 / (1 + e) come from the fast power and
-// reciprocal (2 ulp each), so s is 0 below g = -87.3, where it is under 2^-126.  g (1 -
-// s) is g s e, without the cancellation of 1 - s that a large g would multiply.
+// reciprocal (2 ulp and 1 ulp), so s is 0 below g = -87.3, where it is under 2^-126.  The
+// exponent -g log2(e) is off by its own rounding and the constant's, together 1.22 * 2^-24
+// of itself, and so e by 1.22 |g| 2^-24 more: s is within (8 + 1.3 |g|) 2^-24 of itself for
+// negative g, within 8 * 2^-24 for others, whose e is the smaller part of 1 + e.  g (1 - s)
+// is g s e, without the cancellation of 1 - s that a large g would multiply.
 //
 // A block of threads takes one slab's 128 rows x 128 columns at a time, 32 rows in
 // turn, and asks for the next 32 rows' bytes before it works on these: with four
 // blocks an SM, whose registers they fill, nothing else covers the loads.  32760 x
-// 2048 with columns in 192 us, where its bytes take 91: bound by instructions, some 60
-// for each value of the activation, whose three results are each rounded twice, along
-// rows and along columns.  371 with loads that are waited for and values one by one
+// 2048 with columns in 192 us, where its bytes take 91: some 60 instructions for each value
+// of the activation, whose three results are each rounded twice, along rows and along
+// columns, and 54 % of the issue slots used by the four warps that their registers leave a
+// scheduler.  371 with loads that are waited for and values one by one
 // instead of in pairs, 208 with addresses worked out for each.  Blocks of threads that
 // stay and take several slabs spill: 321; so do two results' exchanges side by side: 236.
 template <int FMT, typename T>

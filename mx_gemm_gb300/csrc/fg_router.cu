@@ -14,9 +14,10 @@
 // A warp takes a token, its logits in registers.  The sums over tokens stay in
 // registers to the end of a warp's tokens, go over shared memory in the order of
 // the warps, and over the blocks' partials in theirs: the same call gives the same
-// bits.  Both are bound by the exponentials and by their start, not by HBM: 16383 x 256
-// bf16 in 10 us with the counts (balance and its sums; 14 with the blocks' sums joined
-// by one block) and 8.7 us (gradient), where the bytes take 1.2 and 2.5.
+// bits.  Both are bound by instructions and by their start, not by HBM: 16383 x 256 bf16
+// in 10 us with the counts (balance and its sums; 14 with the blocks' sums joined by one
+// block) and 8.7 us (gradient), where the bytes take 1.2 and 2.5.  A token takes some 400
+// and 550 instructions of a warp, 8 exponentials among them.
 #include <cuda_bf16.h>
 
 #include <type_traits>
