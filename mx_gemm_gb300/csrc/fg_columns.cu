@@ -335,7 +335,7 @@ __device__ __forceinline__ void store_rows(const Square& v, uint8_t* out, int64_
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const float2 x = halves(v.p[i][q]);
-          w[q] = e4m3x2(ok ? __fdiv_rn(x.x, -f) : -0.f, ok ? __fdiv_rn(x.y, -f) : -0.f);
+          w[q] = e4m3x2(ok ? __fdiv_rn(-x.x, f) : -0.f, ok ? __fdiv_rn(-x.y, f) : -0.f);
         }
       }
     } else {
@@ -724,7 +724,7 @@ __global__ void __launch_bounds__(kWeightThreads, 2) weight_kernel(const T* __re
     if (over.sure && finite)
       words([&](float x, float y) { return halves(over(pair_of(x, y))); });
     else
-      words([&](float x, float y) { return make_float2(finite ? __fdiv_rn(x, -s) : -0.f, finite ? __fdiv_rn(y, -s) : -0.f); });
+      words([&](float x, float y) { return make_float2(finite ? __fdiv_rn(-x, s) : -0.f, finite ? __fdiv_rn(-y, s) : -0.f); });
     if (TRANSPOSE) {
       uint8_t* out = codes + (e * K + k) * static_cast<int64_t>(N) + n;
 #pragma unroll

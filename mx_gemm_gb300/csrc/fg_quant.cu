@@ -82,7 +82,8 @@ __device__ __forceinline__ void quantize8(float (&v)[kVec], bool live, size_t ch
   const bool first = (threadIdx.x & (LANES - 1)) == 0;
   if (MODE == kBlock) {
     // v becomes the negative quotients.  The NaN scale is put in after them, which are
-    // of zeros then.
+    // of zeros then.  (Divided by -s instead of negated, v takes six registers more, and
+    // the norm of 8191 x 7168 a quarter of its warps: 72 us for 61.)
     const float s = f32_scale_of(finite ? amax : 0u);
     const Over over(s);
     if (over.sure && finite) {
@@ -94,7 +95,7 @@ __device__ __forceinline__ void quantize8(float (&v)[kVec], bool live, size_t ch
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) v[i] = __fdiv_rn(finite ? v[i] : 0.f, -s);
+      for (int i = 0; i < kVec; ++i) v[i] = __fdiv_rn(finite ? -v[i] : -0.f, s);
     }
     if (live && first) static_cast<float*>(scales)[chunk / LANES] = finite ? s : __uint_as_float(0x7fc00000u);
   } else {

@@ -16,7 +16,7 @@
 // the warps, and over the blocks' partials in theirs: the same call gives the same
 // bits.  Both are bound by instructions and by their start, not by HBM: 16383 x 256 bf16
 // in 10 us with the counts (balance and its sums; 14 with the blocks' sums joined by one
-// block) and 8.7 us (gradient), where the bytes take 1.2 and 2.5.  A token takes some 400
+// block) and 9.0 us (gradient), where the bytes take 1.2 and 2.5.  A token takes some 400
 // and 550 instructions of a warp, 8 exponentials among them.
 #include <cuda_bf16.h>
 
@@ -271,20 +271,18 @@ __global__ void __launch_bounds__(32 * kBackwardWarps) route_backward_kernel(con
       if (expert >= p.E) expert = -1;
       if (expert >= 0) {
         const T* l = static_cast<const T*>(p.logits) + t * p.ldl + expert;
-        chosen = fmaxf(static_cast<float>(*l), -INFINITY);  // (a NaN is not kept)
+        chosen = static_cast<float>(*l);
       }
-      // what lies beside no choice is not a number that q = 0 could be multiplied with
-      dw = chosen > -INFINITY ? dw : 0.f;
     }
     if (t + step < p.T) next.load(p, t + step, lane);
     float v[VPL];
     const float top = exponentials(now, v);
-    // The chosen ones' exponentials: renormalised by their own largest logit, which may
-    // lie so far below the token's that those against that one would all be zero.
-    const float from = p.renormalize ? warp_max(chosen) : top;
-    const float q = chosen > -INFINITY ? exp_below(chosen, from) : 0.f;
+    chosen = fmaxf(chosen, -INFINITY);  // (a NaN is not kept)
+    // what lies beside no choice need not be a number that q = 0 could be multiplied with
+    dw = chosen > -INFINITY ? dw : 0.f;
     // sums of the exponentials, of their products with the slopes, and of the chosen
     // ones' and theirs with dweights
+    float q = chosen > -INFINITY ? exp_below(chosen, top) : 0.f;
     float sums[4] = {0.f, 0.f, q, q * dw};
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
@@ -292,6 +290,16 @@ __global__ void __launch_bounds__(32 * kBackwardWarps) route_backward_kernel(con
       sums[1] = fmaf(v[i], slope[i], sums[1]);
     }
     warp_sums(sums);
+    // Choices that routing would not make may lie so far below the token's largest logit
+    // that all of theirs are 0: renormalised, they are taken by their own largest.
+    if (p.renormalize && p.dweights && sums[2] < 0.0625f) {
+      const float own = warp_max(chosen);
+      q = chosen > -INFINITY ? exp_below(chosen, own) : 0.f;
+      float s[2] = {q, q * dw};
+      warp_sums(s);
+      sums[2] = s[0];
+      sums[3] = s[1];
+    }
     const float r = sums[0] > 0.f ? 1.f / sums[0] : 0.f;
     const float share = p.renormalize ? (sums[2] > 0.f ? 1.f / sums[2] : 0.f) : r;
     const float mean = sums[3] * share;
