@@ -622,7 +622,7 @@ __global__ void __launch_bounds__(256) dweights_kernel(const float* __restrict__
 // square each, so that the values wait for the block's maximum in registers.  Blocks of
 // threads stay and take every gridDim.x-th block of the weights; the next one's bytes
 // are on their way to shared memory meanwhile.  8 weights of 4096 x
-// 7168 bf16, transposed, in 108 us (6.5 TB/s, 0.96 of a copy's rate); 150 with a block of
+// 7168 bf16, transposed, in 110 us (6.4 TB/s, 0.94 of a copy's rate); 150 with a block of
 // threads for each block of weights and a division for each value.
 constexpr int kWeightThreads = 512;
 
