@@ -54,7 +54,8 @@ class MoeTrainingLayer:
     def __init__(self, mode, router, gate_up, down, top_k, balance=0.01):
         self.mode, self.top_k, self.balance = mode, top_k, balance
         self.router, self.gate_up, self.down = router, gate_up, down
-        self.update()
+        self.up, self.up_t = self._pair(gate_up)
+        self.out, self.out_t = self._pair(down)
 
     def _pair(self, w):
         """Preshuffled weight [E * N][K] and its transpose [E * K][N]."""
@@ -65,9 +66,11 @@ class MoeTrainingLayer:
         return [fg.preshuffle_b(self.mode, *p) for p in parts]
 
     def update(self):
-        """The 8-bit weights anew from the fp32 ones."""
-        self.up, self.up_t = self._pair(self.gate_up)
-        self.out, self.out_t = self._pair(self.down)
+        """The 8-bit weights anew from the fp32 ones, in the memory that they have: a captured step reads them there."""
+        for kept, w in (((self.up, self.up_t), self.gate_up), ((self.out, self.out_t), self.down)):
+            for old, new in zip(kept, self._pair(w)):
+                old.data.copy_(new.data)
+                old.sf.copy_(new.sf)
 
     def forward(self, x):
         """(output bf16 [T][H], what backward() takes) of x bf16 [T][H]."""
