@@ -367,7 +367,9 @@ FG_API fg_status fg_moe_route(const void* logits, int type, int64_t T, int E, in
  *           largest before it), clamped into 0..R.  Rows of Y before offsets[0]
  *           and from offsets[E] on are not written.
  *  workspace  fg_grouped_gemm_workspace_size bytes (gather: rows given); any contents.  Calls that
- *           overlap on the GPU need a workspace each.
+ *           overlap on the GPU need a workspace each.  FP8_BLOCK128 runs with the bytes for
+ *           gather = 0 too, which never fall with more rows; gathered calls of many rows an
+ *           expert are slower then (and may differ in last bits, by the order of their sums).
  * All modes; E <= 1024; R, T <= 2^24.
  * Errors: INVALID_ARG, SHAPE, ALIGN, LAYOUT, WORKSPACE, UNSUPPORTED_ARCH, CUDA.
  */
@@ -476,7 +478,8 @@ FG_API fg_status fg_swiglu_backward(int mode, const void* dy, int type, int64_t 
  * expert e of a[i][n] * b[i][k], fp32 accumulation, for column operands a and b
  * (N and K columns) of the same offsets, R and E.  out [E][N][K] in fp32 or bf16;
  * accumulate: fp32 out is added to, by additions in memory, which may take values
- * and sums under 2^-126 for 0.  An expert without rows has gradient 0.
+ * and sums under 2^-126 for 0; after FG_ERR_TIMEOUT part of it has been added.  An
+ * expert without rows has gradient 0.
  * Errors: INVALID_ARG, SHAPE (operands of another R or E), ALIGN, LAYOUT,
  * UNSUPPORTED_ARCH, CUDA.
  */

@@ -711,7 +711,8 @@ struct GroupedPlan {
   }
 };
 
-GroupedPlan grouped_plan(int mode, int64_t R, int64_t E, int64_t N, int64_t K, bool gather) {
+// have: bytes of workspace that the call is given.
+GroupedPlan grouped_plan(int mode, int64_t R, int64_t E, int64_t N, int64_t K, bool gather, uint64_t have = UINT64_MAX) {
   GroupedPlan g;
   memset(&g, 0, sizeof g);
   if (R == 0) return g;
@@ -754,6 +755,8 @@ GroupedPlan grouped_plan(int mode, int64_t R, int64_t E, int64_t N, int64_t K, b
     const double us32 = 5.7 + unit * line;
     const double us128 = 5.0 + unit * (whole > 1.0 ? whole + 0.5 : 1.0) + (gather ? 1.5 + 0.24e-6 * R * K : 0.0);
     g.tt = R > 32 * E && (KB < kMinSlabs || us128 < 0.96 * us32) ? 128 : 32;
+    // (32-row tiles gather as they copy: a workspace without room for the rows will do)
+    if (g.tt == 128 && gather && have < static_cast<uint64_t>(R * K)) g.tt = 32;
   }
   g.tiles = R / g.tt + active;
   const int64_t units = g.tiles * (g.tt == 32 ? N / 128 : wpairs);
@@ -802,10 +805,6 @@ fg_status fg_grouped_gemm_workspace_size(int mode, int64_t R, int E, int64_t N, 
   fg_status s = check_grouped(mode, R, E, N, K);
   if (s != FG_OK) return s;
   *bytes = grouped_plan(mode, R, E, N, K, gather != 0).total();
-  // (FP8_BLOCK128's form can change back with more rows: what is enough for a call is
-  // enough for one of fewer rows, as before it had two forms)
-  if (mode == FG_FP8_BLOCK128 && gather && R > 32 * static_cast<int64_t>(E))
-    *bytes = std::max(*bytes, static_cast<uint64_t>(R) * static_cast<uint64_t>(K));
   return FG_OK;
 }
 
@@ -832,7 +831,7 @@ fg_status fg_grouped_gemm(const void* A, const void* a_scales, int64_t T, const 
   if (!aligned(offsets, 4) || !aligned(rows, 4) || ((mode == FG_FP8_TENSOR || mode == FG_FP8_BLOCK128) && !aligned(a_scales, 4)))
     return fail(FG_ERR_ALIGN, "%s: offsets, rows and fp32 scales must be 4-byte aligned", what);
   const int64_t rb = row_bytes(mode, K);
-  const GroupedPlan g = grouped_plan(mode, R, E, N, K, rows != nullptr);
+  const GroupedPlan g = grouped_plan(mode, R, E, N, K, rows != nullptr, workspace ? workspace_bytes : 0);
   const uint64_t need = g.total();
   if (need) {
     if (!workspace || workspace_bytes < need)

@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(256) quantize_kernel(const T* __restrict__ x, 
 // of g and u themselves, as the forward pass of a training step keeps them.  One
 // pass: 4 bytes read and 3 written per value of the activation, where three calls
 // of the quantiser read 8.  Bound by HBM: 32761 x 2048 in 32-K blocks in 73.5 us
-// (6.5 TB/s of the 6.8 that a copy reaches); in fp32 blocks of 128 in 109, whose scales'
+// (6.5 TB/s of the 6.8 that a copy reaches); in fp32 blocks of 128 in 110, whose scales'
 // and quotients' instructions take longer.
 template <int MODE, int ROWS, typename T>
 __global__ void __launch_bounds__(256) checkpoint_kernel(const T* __restrict__ x, int64_t M, int64_t K, int64_t ldx,

@@ -65,3 +65,16 @@ def test_a_call_that_ran_out_of_time_gathered():
     finally:
         fg.set_wait_timeout_ns(4_000_000_000)
     assert torch.equal(c.run(), want) and fg.get_error() == fg.FG_OK
+
+
+@pytest.mark.parametrize("counts,n,k", WIDE + NARROW)
+def test_gathered_without_room_for_the_rows(counts, n, k):
+    """The workspace of a call that gathers nothing is enough; one byte less is refused."""
+    c = Experts("fp8_block128", counts, n, k, n + k, gather_from=77)
+    size = fg.grouped_gemm_workspace_size("fp8_block128", c.r, len(counts), n, k, False)
+    buf = torch.full((size + 4096,), 0xa5, dtype=torch.uint8, device="cuda")
+    y = c.run(workspace=buf[:size])
+    assert_close(y, c.reference(), counts)
+    assert (buf[size:] == 0xa5).all()
+    with pytest.raises(fg.FgError, match="workspace"):
+        c.run(workspace=buf[:size - 1])
